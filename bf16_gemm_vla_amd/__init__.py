@@ -17,5 +17,7 @@ from ._lib import (  # noqa: F401
     vla_mlp_chain_replay, vla_set_wait_limit, vla_workspace_status,
     vla_mlp_chain_scratch_bytes, vla_pack_fp8, vla_packed_bytes, vla_probe_mfma_rate, vla_probe_stream_read, vla_quantize_act,
     VLA_MFMA_BF16_32X32X16, VLA_MFMA_BF16_16X16X32, VLA_MFMA_FP8_32X32X64, VLA_MFMA_FP8_16X16X128,
+    VLA_ROPE_HALF, VLA_ROPE_INTERLEAVED, vla_attn_prompt, vla_attn_shared_prefix,
+    vla_attn_shared_prefix_workspace_bytes, vla_qk_norm_rope_append,
     vla_quantize_act_static, vla_quantize_act_workspace_bytes, vla_quantize_pack, vla_reencode_fnuz_to_ocp,
 )

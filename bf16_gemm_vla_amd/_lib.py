@@ -30,6 +30,8 @@ VLA_WFMT_E4M3_FNUZ = 2
 VLA_WFMT_MXFP4 = 3
 VLA_LAYOUT_ROWMAJOR = 0
 VLA_LAYOUT_MFMA = 1
+VLA_ROPE_HALF = 0
+VLA_ROPE_INTERLEAVED = 1
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
@@ -51,6 +53,10 @@ SIGNATURES = {
     "vla_quantize_act_workspace_bytes": (SZ, [I64, I64]),
     "vla_quantize_act": (INT, [P, P, P, P, SZ, I64, I64, P]),
     "vla_quantize_act_static": (INT, [P, P, P, I64, I64, P]),
+    "vla_qk_norm_rope_append": (INT, [P] * 12 + [I64] * 11 + [INT, ctypes.c_float, ctypes.c_float, P]),
+    "vla_attn_prompt": (INT, [P] * 6 + [I64] * 10 + [INT, ctypes.c_float, P]),
+    "vla_attn_shared_prefix_workspace_bytes": (SZ, [I64] * 7),
+    "vla_attn_shared_prefix": (INT, [P] * 9 + [SZ] + [I64] * 11 + [INT, ctypes.c_float, P]),
     "vla_probe_stream_read": (INT, [P, SZ, P, INT, P]),
     "vla_probe_mfma_rate": (INT, [INT, P, INT, P, P, INT, P]),
     "vla_gate_residual_ada_norm": (INT, [P, P, P, P, INT, ctypes.c_float, P, P, P, I64, I64, P]),
@@ -210,6 +216,40 @@ def vla_gate_residual_ada_norm(residual, out, gate, style, style_per_row, eps, r
                                              _ptr(normalized), _ptr(next_gate), M, D, _stream(stream)),
            "vla_gate_residual_ada_norm")
 
+
+# -------------------------------------------------- attention and its cache
+
+def vla_qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, slots, q_out, k_out, k_cache, v_cache,
+                            T, Hq, Hkv, D, rot, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_slots,
+                            layout, rot_scale, eps, stream=None):
+    _check(load().vla_qk_norm_rope_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                                          _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out), _ptr(k_cache),
+                                          _ptr(v_cache), T, Hq, Hkv, D, rot, q_stride, k_stride, v_stride,
+                                          q_out_stride, k_out_stride, num_slots, layout, rot_scale, eps,
+                                          _stream(stream)), "vla_qk_norm_rope_append")
+
+
+def vla_attn_prompt(q, k, v, cu_q, cu_k, out, B, total_q, total_k, Hq, Hkv, D, q_stride, k_stride, v_stride,
+                    out_stride, causal, scale, stream=None):
+    _check(load().vla_attn_prompt(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_q), _ptr(cu_k), _ptr(out), B, total_q, total_k,
+                                  Hq, Hkv, D, q_stride, k_stride, v_stride, out_stride, int(causal), scale,
+                                  _stream(stream)), "vla_attn_prompt")
+
+
+def vla_attn_shared_prefix_workspace_bytes(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity) -> int:
+    return load().vla_attn_shared_prefix_workspace_bytes(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity)
+
+
+def vla_attn_shared_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, out, ws, ws_bytes,
+                           B, L, Hq, Hkv, D, num_pages, page_size, n_prefix_pages, pages_per_seq, q_stride,
+                           out_stride, causal, scale, stream=None):
+    _check(load().vla_attn_shared_prefix(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_pages), _ptr(prefix_len),
+                                         _ptr(block_table), _ptr(seq_lens), _ptr(out), _ptr(ws), ws_bytes, B, L, Hq,
+                                         Hkv, D, num_pages, page_size, n_prefix_pages, pages_per_seq, q_stride,
+                                         out_stride, int(causal), scale, _stream(stream)), "vla_attn_shared_prefix")
+
+
+# ----------------------------------------------------------------- probes
 
 def vla_probe_stream_read(src, nbytes, sink, blocks, stream=None):
     _check(load().vla_probe_stream_read(_ptr(src), nbytes, _ptr(sink), blocks, _stream(stream)),

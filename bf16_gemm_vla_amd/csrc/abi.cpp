@@ -77,6 +77,47 @@ int run_gemm(const char* fn, const vla::GemmProblem& pr, size_t ws_bytes, hipStr
     return VLA_OK;
 }
 
+// A strided matrix of `rows` rows of `width` bf16 values, `stride` elements
+// apart, as bytes.
+struct Region {
+    const void* p;
+    int64_t rows, width, stride;
+    size_t span() const { return p ? static_cast<size_t>((rows - 1) * stride + width) * 2 : 0; }
+};
+
+// Whether two matrices share a byte.  Column blocks of one matrix (the same
+// stride) interleave without sharing any.
+bool regions_overlap(const Region& x, const Region& y) {
+    if (!x.p || !y.p) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    if (a >= b + y.span() || b >= a + x.span()) return false;
+    if (x.stride != y.stride) return true;
+    // columns of y relative to x's, in 0 .. stride - 1
+    const int64_t d = static_cast<int64_t>(b - a) / 2;
+    const int64_t off = ((d % x.stride) + x.stride) % x.stride;
+    return off < x.width || off + y.width > x.stride;
+}
+
+Region flat(const void* p, size_t bytes) {
+    const int64_t n = static_cast<int64_t>((bytes + 1) / 2);
+    return Region{p, 1, n, n};
+}
+
+int check_heads(const char* fn, int64_t Hq, int64_t Hkv, int64_t D) {
+    if (Hq <= 0 || Hkv <= 0 || D <= 0)
+        return fail(VLA_EINVAL, fn, "Hq=%lld Hkv=%lld D=%lld must be positive", (long long)Hq, (long long)Hkv, (long long)D);
+    if (Hq % Hkv != 0 || Hq > 4096)
+        return fail(VLA_ESHAPE, fn, "Hq=%lld must be a multiple of Hkv=%lld, at most 4096", (long long)Hq, (long long)Hkv);
+    if (D % 8 != 0 || D > 256) return fail(VLA_ESHAPE, fn, "D=%lld must be a multiple of 8, at most 256", (long long)D);
+    return VLA_OK;
+}
+
+int check_stride(const char* fn, const char* name, int64_t stride, int64_t width) {
+    if (stride < width || stride % 8 != 0 || stride > (int64_t(1) << 30))
+        return fail(VLA_ESHAPE, fn, "%s=%lld must be a multiple of 8, at least %lld", name, (long long)stride, (long long)width);
+    return VLA_OK;
+}
+
 }  // namespace
 
 uint32_t vla::wait_polls() { return g_wait_polls.load(std::memory_order_relaxed); }
@@ -607,6 +648,205 @@ int vla_gate_residual_ada_norm(const uint16_t* residual, const uint16_t* out, co
     hipError_t e = vla::launch_gate_residual_ada_norm(residual, out, gate, style, style_per_row ? 1 : 0, eps,
                                                       residual_out, normalized, next_gate, M, D,
                                                       static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+
+int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* q_weight,
+                            const uint16_t* k_weight, const float* inv_freq, const int32_t* positions,
+                            const int64_t* slots, uint16_t* q_out, uint16_t* k_out, uint16_t* k_cache,
+                            uint16_t* v_cache, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                            int64_t k_out_stride, int64_t num_slots, int layout, float rot_scale, float eps,
+                            void* stream) {
+    const char* fn = "vla_qk_norm_rope_append";
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(q_out);
+    OPTIONAL_PTR(v);
+    OPTIONAL_PTR(q_weight);
+    OPTIONAL_PTR(k_weight);
+    OPTIONAL_PTR(inv_freq);
+    OPTIONAL_PTR(positions);
+    OPTIONAL_PTR(slots);
+    OPTIONAL_PTR(k_out);
+    OPTIONAL_PTR(k_cache);
+    OPTIONAL_PTR(v_cache);
+    if (T <= 0) return fail(VLA_EINVAL, fn, "T=%lld must be positive", (long long)T);
+    if (T > (int64_t(1) << 24)) return fail(VLA_ESHAPE, fn, "T=%lld too large", (long long)T);
+    if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
+    if (rot < 0 || rot > D || rot % 8 != 0)
+        return fail(VLA_ESHAPE, fn, "rot=%lld must be a multiple of 8 in 0..D", (long long)rot);
+    if (layout != VLA_ROPE_HALF && layout != VLA_ROPE_INTERLEAVED) return fail(VLA_EINVAL, fn, "unknown layout %d", layout);
+    if (!std::isfinite(rot_scale)) return fail(VLA_EINVAL, fn, "rot_scale must be finite");
+    if (!std::isfinite(eps) || eps < 0.0f) return fail(VLA_EINVAL, fn, "eps must be finite and >= 0");
+    if ((inv_freq != nullptr) != (rot > 0) || (positions != nullptr) != (rot > 0))
+        return fail(VLA_EINVAL, fn, "inv_freq and positions must be given exactly when rot > 0");
+    const bool append = k_cache != nullptr;
+    if ((v_cache != nullptr) != append || (slots != nullptr) != append || (v != nullptr) != append || (num_slots != 0) != append)
+        return fail(VLA_EINVAL, fn, "v, slots, k_cache, v_cache and num_slots must be given together");
+    if (num_slots < 0) return fail(VLA_EINVAL, fn, "num_slots=%lld must not be negative", (long long)num_slots);
+    if (num_slots >= (int64_t(1) << 31)) return fail(VLA_ESHAPE, fn, "num_slots=%lld too large", (long long)num_slots);
+    if (!append && !k_out) return fail(VLA_EINVAL, fn, "neither k_out nor a cache takes the keys");
+    if (int rc = check_stride(fn, "q_stride", q_stride, Hq * D)) return rc;
+    if (int rc = check_stride(fn, "k_stride", k_stride, Hkv * D)) return rc;
+    if (append)
+        if (int rc = check_stride(fn, "v_stride", v_stride, Hkv * D)) return rc;
+    if (int rc = check_stride(fn, "q_out_stride", q_out_stride, Hq * D)) return rc;
+    if (k_out)
+        if (int rc = check_stride(fn, "k_out_stride", k_out_stride, Hkv * D)) return rc;
+    const Region ins[8] = {{q, T, Hq * D, q_stride}, {k, T, Hkv * D, k_stride}, {v, T, Hkv * D, v_stride},
+                           flat(q_weight, D * 2), flat(k_weight, D * 2), flat(inv_freq, rot * 2),
+                           flat(positions, T * 4), flat(slots, T * 8)};
+    const Region outs[4] = {{q_out, T, Hq * D, q_out_stride}, {k_out, T, Hkv * D, k_out_stride},
+                            {k_cache, num_slots, Hkv * D, Hkv * D}, {v_cache, num_slots, Hkv * D, Hkv * D}};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 8; ++j) {
+            const bool in_place = i == j && i < 2 && outs[i].p == ins[j].p && outs[i].stride == ins[j].stride;
+            if (!in_place && regions_overlap(outs[i], ins[j])) return fail(VLA_EINVAL, fn, "output %d overlaps input %d", i, j);
+        }
+        for (int j = i + 1; j < 4; ++j)
+            if (regions_overlap(outs[i], outs[j])) return fail(VLA_EINVAL, fn, "outputs %d and %d overlap", i, j);
+    }
+    vla::RopeArgs a{};
+    a.q = q; a.k = k; a.v = v;
+    a.q_weight = q_weight; a.k_weight = k_weight;
+    a.inv_freq = inv_freq; a.positions = positions; a.slots = slots;
+    a.q_out = q_out; a.k_out = k_out; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.T = T; a.num_slots = num_slots;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+    a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
+    a.Hq = static_cast<int>(Hq); a.Hkv = static_cast<int>(Hkv); a.D = static_cast<int>(D); a.rot = static_cast<int>(rot);
+    a.interleaved = layout == VLA_ROPE_INTERLEAVED;
+    a.rot_scale = rot_scale; a.eps = eps;
+    hipError_t e = vla::launch_qk_norm_rope_append(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+
+int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, const int32_t* cu_q,
+                    const int32_t* cu_k, uint16_t* out, int64_t B, int64_t total_q, int64_t total_k, int64_t Hq,
+                    int64_t Hkv, int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                    int64_t out_stride, int causal, float scale, void* stream) {
+    const char* fn = "vla_attn_prompt";
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    REQUIRE_PTR(cu_q);
+    OPTIONAL_PTR(cu_k);
+    REQUIRE_PTR(out);
+    if (B <= 0 || total_q <= 0 || total_k <= 0)
+        return fail(VLA_EINVAL, fn, "B=%lld total_q=%lld total_k=%lld must be positive", (long long)B, (long long)total_q, (long long)total_k);
+    if (B > (int64_t(1) << 20) || total_q > (int64_t(1) << 30) || total_k > (int64_t(1) << 30))
+        return fail(VLA_ESHAPE, fn, "B=%lld total_q=%lld total_k=%lld too large", (long long)B, (long long)total_q, (long long)total_k);
+    if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
+    if (int rc = check_stride(fn, "q_stride", q_stride, Hq * D)) return rc;
+    if (int rc = check_stride(fn, "k_stride", k_stride, Hkv * D)) return rc;
+    if (int rc = check_stride(fn, "v_stride", v_stride, Hkv * D)) return rc;
+    if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
+    if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
+    if (!std::isfinite(scale) || scale <= 0.0f) return fail(VLA_EINVAL, fn, "scale must be finite and > 0");
+    // row tiles of at least 32 rows, at most one ragged one per sequence
+    if ((total_q * (Hq / Hkv) / 32 + B) * Hkv >= (int64_t(1) << 31))
+        return fail(VLA_ESHAPE, fn, "total_q=%lld rows of %lld heads are too many", (long long)total_q, (long long)Hq);
+    const Region o{out, total_q, Hq * D, out_stride};
+    const Region ins[5] = {{q, total_q, Hq * D, q_stride}, {k, total_k, Hkv * D, k_stride}, {v, total_k, Hkv * D, v_stride},
+                           flat(cu_q, (B + 1) * 4), flat(cu_k, (B + 1) * 4)};
+    for (int j = 0; j < 5; ++j)
+        if (regions_overlap(o, ins[j])) return fail(VLA_EINVAL, fn, "out overlaps input %d", j);
+    vla::PromptArgs a{};
+    a.q = q; a.k = k; a.v = v; a.out = out;
+    a.cu_q = cu_q; a.cu_k = cu_k ? cu_k : cu_q;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.out_stride = out_stride;
+    a.B = static_cast<int>(B); a.total_q = static_cast<int>(total_q); a.total_k = static_cast<int>(total_k);
+    a.Hq = static_cast<int>(Hq); a.Hkv = static_cast<int>(Hkv); a.D = static_cast<int>(D);
+    a.causal = causal;
+    a.c = scale * 1.4426950408889634f;
+    hipError_t e = vla::launch_attn_prompt(a, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+
+namespace {
+// Sizes of a shared-prefix call that do not depend on its pointers.
+int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap, int64_t suffix_cap) {
+    if (B <= 0 || L <= 0) return fail(VLA_EINVAL, fn, "B=%lld L=%lld must be positive", (long long)B, (long long)L);
+    if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
+    if (prefix_cap < 0 || suffix_cap < 0 || prefix_cap + suffix_cap == 0)
+        return fail(VLA_EINVAL, fn, "a prefix or a suffix must be there");
+    if (B > (int64_t(1) << 20) || L > (int64_t(1) << 20) || B * L * Hq >= (int64_t(1) << 31) ||
+        prefix_cap >= (int64_t(1) << 30) || suffix_cap >= (int64_t(1) << 30))
+        return fail(VLA_ESHAPE, fn, "B=%lld L=%lld Hq=%lld or the capacities %lld, %lld too large", (long long)B, (long long)L,
+                    (long long)Hq, (long long)prefix_cap, (long long)suffix_cap);
+    return VLA_OK;
+}
+}  // namespace
+
+size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
+                                              int64_t prefix_capacity, int64_t suffix_capacity) {
+    if (check_shared("vla_attn_shared_prefix_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity) != VLA_OK)
+        return 0;
+    return static_cast<size_t>(vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity).ws_bytes);
+}
+
+int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
+                           const int32_t* prefix_pages, const int32_t* prefix_len, const int32_t* block_table,
+                           const int32_t* seq_lens, uint16_t* out, void* ws, size_t ws_bytes, int64_t B, int64_t L,
+                           int64_t Hq, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                           int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
+                           int causal, float scale, void* stream) {
+    const char* fn = "vla_attn_shared_prefix";
+    REQUIRE_PTR(q);
+    REQUIRE_PTR(k_cache);
+    REQUIRE_PTR(v_cache);
+    OPTIONAL_PTR(prefix_pages);
+    OPTIONAL_PTR(prefix_len);
+    OPTIONAL_PTR(block_table);
+    OPTIONAL_PTR(seq_lens);
+    REQUIRE_PTR(out);
+    REQUIRE_PTR(ws);
+    if (num_pages <= 0 || page_size <= 0 || n_prefix_pages < 0 || pages_per_seq < 0)
+        return fail(VLA_EINVAL, fn, "num_pages=%lld page_size=%lld must be positive, n_prefix_pages=%lld pages_per_seq=%lld not negative",
+                    (long long)num_pages, (long long)page_size, (long long)n_prefix_pages, (long long)pages_per_seq);
+    if ((page_size & (page_size - 1)) != 0 || page_size > 65536)
+        return fail(VLA_ESHAPE, fn, "page_size=%lld must be a power of two, at most 65536", (long long)page_size);
+    if (num_pages >= (int64_t(1) << 31) || num_pages * page_size >= (int64_t(1) << 31) ||
+        n_prefix_pages >= (int64_t(1) << 30) || pages_per_seq >= (int64_t(1) << 30))
+        return fail(VLA_ESHAPE, fn, "num_pages=%lld n_prefix_pages=%lld pages_per_seq=%lld of %lld rows too large", (long long)num_pages,
+                    (long long)n_prefix_pages, (long long)pages_per_seq, (long long)page_size);
+    if ((prefix_pages != nullptr) != (n_prefix_pages > 0) || (prefix_len != nullptr) != (n_prefix_pages > 0))
+        return fail(VLA_EINVAL, fn, "prefix_pages and prefix_len must be given exactly when n_prefix_pages > 0");
+    if ((block_table != nullptr) != (pages_per_seq > 0) || (seq_lens != nullptr) != (pages_per_seq > 0))
+        return fail(VLA_EINVAL, fn, "block_table and seq_lens must be given exactly when pages_per_seq > 0");
+    const int64_t prefix_cap = n_prefix_pages * page_size, suffix_cap = pages_per_seq * page_size;
+    if (int rc = check_shared(fn, B, L, Hq, Hkv, D, prefix_cap, suffix_cap)) return rc;
+    if (int rc = check_stride(fn, "q_stride", q_stride, Hq * D)) return rc;
+    if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
+    if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
+    if (!std::isfinite(scale) || scale <= 0.0f) return fail(VLA_EINVAL, fn, "scale must be finite and > 0");
+    const vla::SharedPlan p = vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_cap, suffix_cap);
+    if (p.prefix_items + p.suffix_items >= (int64_t(1) << 31)) return fail(VLA_ESHAPE, fn, "too many work items");
+    if (ws_bytes < static_cast<size_t>(p.ws_bytes))
+        return fail(VLA_EWORKSPACE, fn, "workspace %zu bytes < required %lld", ws_bytes, (long long)p.ws_bytes);
+    const size_t cache_bytes = static_cast<size_t>(num_pages) * page_size * Hkv * D * 2;
+    const Region outs[2] = {{out, B * L, Hq * D, out_stride}, flat(ws, static_cast<size_t>(p.ws_bytes))};
+    const Region ins[7] = {{q, B * L, Hq * D, q_stride}, flat(k_cache, cache_bytes), flat(v_cache, cache_bytes),
+                           flat(prefix_pages, n_prefix_pages * 4), flat(prefix_len, prefix_len ? 4 : 0),
+                           flat(block_table, B * pages_per_seq * 4), flat(seq_lens, B * 4)};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 7; ++j)
+            if (regions_overlap(outs[i], ins[j])) return fail(VLA_EINVAL, fn, "%s overlaps input %d", i ? "ws" : "out", j);
+    if (regions_overlap(outs[0], outs[1])) return fail(VLA_EINVAL, fn, "out overlaps ws");
+    vla::SharedArgs a{};
+    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.prefix_pages = prefix_pages; a.prefix_len = prefix_len; a.block_table = block_table; a.seq_lens = seq_lens;
+    a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
+    a.B = static_cast<int>(B); a.L = static_cast<int>(L);
+    a.Hq = static_cast<int>(Hq); a.Hkv = static_cast<int>(Hkv); a.D = static_cast<int>(D);
+    a.causal = causal;
+    a.c = scale * 1.4426950408889634f;
+    a.page_log2 = __builtin_ctzll(static_cast<unsigned long long>(page_size));
+    a.pages_per_seq = static_cast<int>(pages_per_seq);
+    a.prefix_cap = static_cast<int>(prefix_cap); a.suffix_cap = static_cast<int>(suffix_cap);
+    a.num_pages = static_cast<uint32_t>(num_pages);
+    hipError_t e = vla::launch_attn_shared(a, p, ws, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
 }
 

@@ -1,0 +1,208 @@
+// Per-head RMS norm, rotary positions and the append to a paged key/value
+// cache in one pass over the rows of a QKV GEMM:
+//   n = x * w / sqrt(mean(x^2) + eps)                  (q and k, with a weight)
+//   (a, b) -> (a c - b s, b c + a s),  c, s = rot_scale * (cos, sin)(position * inv_freq[j])
+// with (a, b) = (n_j, n_{j + rot/2}) or (n_2j, n_2j+1); channels rot .. D-1
+// pass.  The rotated k row and the v row also go to their cache slot.
+//
+// A head is cut into units of 2 VEC channels that hold whole pairs: in the
+// rotated part of the half layout VEC channels and their VEC partners rot/2
+// further on, elsewhere 2 VEC consecutive channels.  A lane keeps one unit
+// position for every head it handles, so its VEC angles are computed once per
+// token and a wave reads 64 units (64 / GW heads of GW lanes) per step.  The
+// norm's sum of squares runs over the GW lanes of a head.
+//
+// The angle is formed in fp64 revolutions and reduced before it is rounded:
+// at position 2^20 an fp32 product alone would be off by 2^-5 radians.  The
+// mean square is fp64 and its reciprocal root taken on the mantissa, so rows
+// of the largest or smallest bf16 values neither overflow nor vanish.  Each
+// output is rounded to bf16 once, from fp32.  The kernel is bound by HBM on
+// prompts and by latency on single tokens.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "vla_device.h"
+#include "vla_internal.h"
+
+namespace vla {
+namespace {
+
+constexpr int kRThreads = 256;
+
+template <int VEC>
+struct Words;   // VEC bf16 values as loaded
+template <>
+struct Words<8> { using type = uint4; };
+template <>
+struct Words<4> { using type = uint2; };
+
+template <int VEC>
+__device__ __forceinline__ void load_bf16(const uint16_t* p, float* x) {
+    using W = typename Words<VEC>::type;
+    const W w = *reinterpret_cast<const W*>(p);
+    uint32_t u[VEC / 2];
+    __builtin_memcpy(u, &w, sizeof(w));
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+template <int VEC>
+__device__ __forceinline__ typename Words<VEC>::type to_words(const float* x) {
+    using W = typename Words<VEC>::type;
+    uint32_t u[VEC / 2];
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) u[i] = f32x2_to_bf16x2(x[2 * i], x[2 * i + 1]);
+    W w;
+    __builtin_memcpy(&w, u, sizeof(w));
+    return w;
+}
+
+template <int VEC>
+__global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs a) {
+    using W = typename Words<VEC>::type;
+    const int lane = threadIdx.x & 63;
+    const int64_t wave = static_cast<int64_t>(blockIdx.x) * (kRThreads / 64) + (threadIdx.x >> 6);
+    const int64_t t = wave / a.chunks;
+    if (t >= a.T) return;
+    const int chunk = static_cast<int>(wave - t * a.chunks);
+    const int u = lane & (a.gw - 1), hs = lane >> a.gw_log2;
+    const int hpw = 64 >> a.gw_log2;                     // heads per wave step
+    const int units = a.D / (2 * VEC), rot_units = a.rot / (2 * VEC);
+    const bool live = u < units, turned = u < rot_units;
+    const int lo = (turned && !a.interleaved) ? u * VEC : 2 * VEC * u;
+    const int hi = (turned && !a.interleaved) ? a.rot / 2 + u * VEC : 2 * VEC * u + VEC;
+
+    float c[VEC], s[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) { c[e] = 1.0f; s[e] = 0.0f; }
+    if (turned) {
+        const double pos = static_cast<double>(a.positions[t]) * 0.15915494309189533577;   // 1 / (2 pi)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const double rev = pos * static_cast<double>(a.inv_freq[u * VEC + e]);
+            const float f = 2.0f * static_cast<float>(rev - __builtin_rint(rev));
+            sincospif(f, &s[e], &c[e]);
+            s[e] *= a.rot_scale;
+            c[e] *= a.rot_scale;
+        }
+    }
+    const int64_t slot = a.slots ? a.slots[t] : -1;
+    const bool append = slot >= 0 && slot < a.num_slots;
+    const int heads = a.Hq + 2 * a.Hkv;
+    const int first = chunk * a.steps * hpw, last = min(heads, first + a.steps * hpw);
+
+    for (int h = first + hs; h < last; h += hpw) {
+        const int kind = h < a.Hq ? 0 : (h < a.Hq + a.Hkv ? 1 : 2);   // q, k, v
+        const int hh = kind == 0 ? h : (kind == 1 ? h - a.Hq : h - a.Hq - a.Hkv);
+        const uint16_t* src = kind == 0 ? a.q + t * a.q_stride : (kind == 1 ? a.k + t * a.k_stride : a.v + t * a.v_stride);
+        src += static_cast<int64_t>(hh) * a.D;
+        const int64_t at = (slot * a.Hkv + hh) * a.D;                 // in the caches
+        if (kind == 2) {
+            if (live && append) {
+                *reinterpret_cast<W*>(a.v_cache + at + 2 * VEC * u) = *reinterpret_cast<const W*>(src + 2 * VEC * u);
+                *reinterpret_cast<W*>(a.v_cache + at + 2 * VEC * u + VEC) = *reinterpret_cast<const W*>(src + 2 * VEC * u + VEC);
+            }
+            continue;
+        }
+        float x[VEC], y[VEC];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) { x[e] = 0.0f; y[e] = 0.0f; }
+        if (live) {
+            load_bf16<VEC>(src + lo, x);
+            load_bf16<VEC>(src + hi, y);
+        }
+        const uint16_t* w = kind == 0 ? a.q_weight : a.k_weight;
+        if (w) {
+            // the lanes of one head share `kind`: the whole group is here
+            double ss = 0.0;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                ss += static_cast<double>(x[e]) * x[e];
+                ss += static_cast<double>(y[e]) * y[e];
+            }
+            for (int o = a.gw >> 1; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
+            // 1 / sqrt(m 2^(2k)) = rsq(m) 2^-k with m in [1/2, 2)
+            int ex;
+            const double m = frexp(ss / a.D + static_cast<double>(a.eps), &ex);
+            const float r = __builtin_amdgcn_rsqf(static_cast<float>((ex & 1) ? 2.0 * m : m));
+            const int k2 = -((ex - (ex & 1)) / 2);
+            if (live) {
+                float wl[VEC], wh[VEC];
+                load_bf16<VEC>(w + lo, wl);
+                load_bf16<VEC>(w + hi, wh);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    x[e] = ldexpf(x[e] * r, k2) * wl[e];
+                    y[e] = ldexpf(y[e] * r, k2) * wh[e];
+                }
+            }
+        }
+        if (turned) {
+            if (a.interleaved) {
+#pragma unroll
+                for (int e = 0; e < VEC / 2; ++e) {
+                    const float p = x[2 * e], q = x[2 * e + 1];
+                    x[2 * e] = p * c[e] - q * s[e];
+                    x[2 * e + 1] = q * c[e] + p * s[e];
+                    const float p2 = y[2 * e], q2 = y[2 * e + 1];
+                    y[2 * e] = p2 * c[VEC / 2 + e] - q2 * s[VEC / 2 + e];
+                    y[2 * e + 1] = q2 * c[VEC / 2 + e] + p2 * s[VEC / 2 + e];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float p = x[e], q = y[e];
+                    x[e] = p * c[e] - q * s[e];
+                    y[e] = q * c[e] + p * s[e];
+                }
+            }
+        }
+        if (!live) continue;
+        const W wx = to_words<VEC>(x), wy = to_words<VEC>(y);
+        if (kind == 0) {
+            uint16_t* o = a.q_out + t * a.q_out_stride + static_cast<int64_t>(hh) * a.D;
+            *reinterpret_cast<W*>(o + lo) = wx;
+            *reinterpret_cast<W*>(o + hi) = wy;
+        } else {
+            if (a.k_out) {
+                uint16_t* o = a.k_out + t * a.k_out_stride + static_cast<int64_t>(hh) * a.D;
+                *reinterpret_cast<W*>(o + lo) = wx;
+                *reinterpret_cast<W*>(o + hi) = wy;
+            }
+            if (append) {
+                *reinterpret_cast<W*>(a.k_cache + at + lo) = wx;
+                *reinterpret_cast<W*>(a.k_cache + at + hi) = wy;
+            }
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s) {
+    // 16-byte words where whole pairs of them fit the head and its rotated part
+    const int vec = (a.D % 16 == 0 && a.rot % 16 == 0) ? 8 : 4;
+    const int units = a.D / (2 * vec);
+    a.gw_log2 = 0;
+    while ((1 << a.gw_log2) < units) ++a.gw_log2;
+    a.gw = 1 << a.gw_log2;
+    const int hpw = 64 >> a.gw_log2;
+    const int steps = (a.Hq + 2 * a.Hkv + hpw - 1) / hpw;    // wave steps of one token
+    // one wave per step while that fills the GPU's 1024 SIMDs some 8 times
+    // over, then one wave per token, which computes its angles once
+    int64_t chunks = (8192 + a.T - 1) / a.T;
+    if (chunks > steps) chunks = steps;
+    a.steps = static_cast<int>((steps + chunks - 1) / chunks);
+    a.chunks = (steps + a.steps - 1) / a.steps;
+    const int64_t blocks = (a.T * a.chunks + kRThreads / 64 - 1) / (kRThreads / 64);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (vec == 8) qk_norm_rope_append_kernel<8><<<grid, kRThreads, 0, s>>>(a);
+    else qk_norm_rope_append_kernel<4><<<grid, kRThreads, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace vla

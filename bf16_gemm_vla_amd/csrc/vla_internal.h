@@ -27,6 +27,58 @@ hipError_t launch_gate_residual_ada_norm(const uint16_t* resid, const uint16_t* 
                                          const uint16_t* style, int style_per_row, float eps, uint16_t* r_out,
                                          uint16_t* h_out, uint16_t* ng_out, int64_t M, int64_t D, hipStream_t s);
 bool boundary_width_ok(int64_t D);   // D a positive multiple of 4, at most 8192
+
+// ------------------------------------------------------------ attention
+struct RopeArgs {
+    const uint16_t *q, *k, *v;
+    const uint16_t *q_weight, *k_weight;       // nullable
+    const float* inv_freq;
+    const int32_t* positions;
+    const int64_t* slots;                      // nullable with the caches
+    uint16_t *q_out, *k_out, *k_cache, *v_cache;   // k_out, caches nullable
+    int64_t T, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_slots;
+    int Hq, Hkv, D, rot, interleaved;
+    float rot_scale, eps;
+    int gw, gw_log2, chunks, steps;            // set by the launcher
+};
+hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s);
+
+struct PromptArgs {
+    const uint16_t *q, *k, *v;
+    const int32_t *cu_q, *cu_k;
+    uint16_t* out;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    int B, total_q, total_k, Hq, Hkv, D, causal;
+    float c;                                   // scale * log2(e)
+    int tiles;                                 // set by the launcher: most row tiles per key/value head
+};
+hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s);
+
+struct SharedArgs {
+    const uint16_t *q, *k_cache, *v_cache;
+    const int32_t *prefix_pages, *prefix_len;  // nullable: no prefix
+    const int32_t *block_table, *seq_lens;     // nullable: no suffix
+    uint16_t* out;
+    int64_t q_stride, out_stride;
+    int B, L, Hq, Hkv, D, causal;
+    float c;
+    int page_log2, pages_per_seq, prefix_cap, suffix_cap;   // capacities in keys
+    uint32_t num_pages;
+    // set by the launcher
+    int merged, prefix_items, prefix_splits, suffix_splits, suffix_tiles, parts;
+    float *part_ml, *part_o;
+};
+// Launch plan of a shared-prefix call, from its host sizes alone.
+struct SharedPlan {
+    bool merged;         // prefix and suffix are one range of keys (one sequence, or no prefix)
+    bool prefix_many, suffix_many;
+    int64_t prefix_splits, suffix_splits, suffix_tiles, prefix_items, suffix_items, parts;
+    int64_t ml_bytes, ws_bytes;
+};
+SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
+                            int64_t suffix_cap);
+hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipStream_t s);
+
 hipError_t launch_stream_read(const void* src, size_t bytes, uint32_t* sink, int blocks, hipStream_t s);
 hipError_t launch_mfma_rate(int form, const uint32_t* src, int iters, float* out, uint64_t* clocks, int blocks,
                             hipStream_t s);

@@ -186,6 +186,123 @@ int vla_gate_residual_ada_norm(const uint16_t *residual, const uint16_t *out, co
                                const uint16_t *style, int style_per_row, float eps, uint16_t *residual_out,
                                uint16_t *normalized, uint16_t *next_gate, int64_t M, int64_t D, void *stream);
 
+/* ------------------------------------------------- attention and its cache */
+
+/* The operators between a layer's QKV GEMM and its attention-out GEMM, for
+ * the same rows: heads normed, rotated and appended to a key/value cache,
+ * attention over whole prompts, and attention of few rows per sequence over
+ * the cache.  ("FlashRT: an inference engine for real-time robot control"
+ * (itsolotime.com), section 3.4, puts attention behind one interface with
+ * stable cache addresses; "Real-time VLA inference on AMD hardware", section
+ * "The AMD stack", has it decide the whole model's latency.)
+ *
+ * Heads: Hq query heads share Hkv key/value heads, Hq a multiple of Hkv;
+ * query head h reads key/value head h / (Hq / Hkv).  A head has D channels, D
+ * a multiple of 8, at most 256 (VLA_ESHAPE).  A token's row holds its heads
+ * one after another; rows are `*_stride` elements apart (a multiple of 8, at
+ * least heads * D, else VLA_ESHAPE), so q, k and v may be the column blocks
+ * of one QKV GEMM output.
+ *
+ * The cache: k_cache and v_cache, device bf16, num_pages pages of page_size
+ * rows of Hkv * D elements each; row r of page p is slot p * page_size + r.
+ * Fewer than 2^31 slots (VLA_ESHAPE); their bytes may pass 4 GiB.
+ *
+ * Values in device arrays (offsets, lengths, slots, page numbers) are bounded
+ * in the kernels: none of them can lead outside the tensors the sizes
+ * describe.  No output may overlap an input or another output
+ * (VLA_EINVAL) except where stated. */
+
+#define VLA_ROPE_HALF 0         /* pairs (j, j + rot/2) */
+#define VLA_ROPE_INTERLEAVED 1  /* pairs (2j, 2j + 1) */
+
+/* Per token t, each query and key head: RMS norm over its D channels, then the
+ * rotation of its first `rot` channels, then the append:
+ *   n = x * w / sqrt(mean(x^2) + eps)                 (without a weight: n = x)
+ *   (a, b) -> (a c - b s, b c + a s) for pair j,
+ *   c, s = rot_scale * cos, sin (positions[t] * inv_freq[j])
+ *   k_cache[slots[t]] = the rotated k row, v_cache[slots[t]] = the v row.
+ * fp64 angles, mean squares; fp32 products; each output rounded to bf16 once.
+ * Scaling for long contexts is in inv_freq and rot_scale.
+ *   q, k, v      device bf16, T rows of Hq, Hkv, Hkv heads; v is read only by
+ *                the append and must be NULL without it;
+ *   q_weight, k_weight  device bf16[D], or NULL: no norm of q / of k;
+ *   inv_freq     device float[rot / 2];  positions  device int32[T], any
+ *                sign; both NULL when rot == 0, else neither;
+ *   slots        device int64[T]; a token whose slot is outside 0 ..
+ *                num_slots - 1 (by convention -1: padding) is not appended.
+ *                Tokens of one call must not share a slot;
+ *   q_out        device bf16, T rows of Hq heads; may be q itself (same stride);
+ *   k_out        device bf16, T rows of Hkv heads (for vla_attn_prompt), may be
+ *                k itself (same stride), or NULL;
+ *   k_cache, v_cache  device bf16, num_slots rows of Hkv * D.  v, slots,
+ *                k_cache and v_cache are all NULL (num_slots 0: no append, then
+ *                k_out must be given) or none of them is;
+ *   rot          0 .. D, a multiple of 8 (VLA_ESHAPE);
+ *   layout       VLA_ROPE_*;  rot_scale finite;  eps finite and >= 0.
+ * T in 1 .. 2^24. */
+int vla_qk_norm_rope_append(const uint16_t *q, const uint16_t *k, const uint16_t *v, const uint16_t *q_weight,
+                            const uint16_t *k_weight, const float *inv_freq, const int32_t *positions,
+                            const int64_t *slots, uint16_t *q_out, uint16_t *k_out, uint16_t *k_cache,
+                            uint16_t *v_cache, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                            int64_t k_out_stride, int64_t num_slots, int layout, float rot_scale, float eps,
+                            void *stream);
+
+/* Attention over B packed sequences: rows cu_q[b] .. cu_q[b+1]-1 of q attend
+ * to rows cu_k[b] .. cu_k[b+1]-1 of k and v,
+ *   out_i = sum_j softmax_j(scale q_i . k_j) v_j.
+ * causal: with n_q rows and n_k keys, row i sees keys j <= i + n_k - n_q (the
+ * ends of rows and keys are aligned; keys of earlier chunks come first).  A
+ * row that sees no key gives 0.  What a row does not see has no part in it,
+ * whatever its value, infinities and NaN included.  fp32 scores and sums;
+ * the weights are rounded to bf16 for the second product.
+ *   q, k, v   device bf16, total_q, total_k, total_k rows;
+ *   cu_q      device int32[B + 1], non-decreasing, cu_q[0] >= 0;
+ *   cu_k      device int32[B + 1], or NULL: the same as cu_q;
+ *   out       device bf16, total_q rows; rows in no sequence stay as they were;
+ *   scale     finite and > 0, causal 0 or 1 (VLA_EINVAL).
+ * B in 1 .. 2^20, total_q and total_k in 1 .. 2^30. */
+int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
+                    const int32_t *cu_k, uint16_t *out, int64_t B, int64_t total_q, int64_t total_k, int64_t Hq,
+                    int64_t Hkv, int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                    int64_t out_stride, int causal, float scale, void *stream);
+
+/* Attention of L query rows for each of B sequences over the cache.  Every
+ * sequence sees the shared prefix, whose keys are read once for the whole
+ * batch, and then its own suffix:
+ *   keys of sequence b = prefix rows 0 .. P-1, suffix rows 0 .. n_b-1,
+ * prefix row j in page prefix_pages[j / page_size], suffix row j in page
+ * block_table[b][j / page_size].  causal: row i of L sees suffix rows
+ * j <= i + n_b - L (the call's own rows are the last L of the suffix) and all
+ * of the prefix; otherwise it sees every row.  A page number outside
+ * 0 .. num_pages-1 holds no keys.  A row that sees no key gives 0; masks,
+ * sums and roundings are those of vla_attn_prompt.  B == 1 without a prefix is the
+ * ordinary decoding step, L == 1 its single-token form.
+ *   q, out        device bf16, B * L rows of Hq heads, sequence after sequence;
+ *   prefix_pages  device int32[n_prefix_pages], prefix_len device int32[1]
+ *                 (P, at most n_prefix_pages * page_size: a larger value counts
+ *                 as that), or both NULL with n_prefix_pages == 0;
+ *   block_table   device int32[B][pages_per_seq], seq_lens device int32[B]
+ *                 (n_b, bounded in the same way), or both NULL with
+ *                 pages_per_seq == 0.  One of the two must be there;
+ *   ws            device workspace of vla_attn_shared_prefix_workspace_bytes
+ *                 (capacities = n_prefix_pages * page_size and pages_per_seq *
+ *                 page_size), ZERO-FILLED before its first use; every
+ *                 completed call leaves it ready for the next, of any shape.
+ *                 Calls that overlap in time must not share it;
+ *   page_size     a power of two, 1 .. 65536 (VLA_ESHAPE).
+ * The lengths are read on the device: a captured call follows them.  Results
+ * depend on the call's sizes and lengths alone: repeated calls are bitwise
+ * equal.  B and L in 1 .. 2^20, B * L * Hq < 2^31, capacities < 2^30. */
+size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
+                                              int64_t prefix_capacity, int64_t suffix_capacity);
+int vla_attn_shared_prefix(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,
+                           const int32_t *prefix_pages, const int32_t *prefix_len, const int32_t *block_table,
+                           const int32_t *seq_lens, uint16_t *out, void *ws, size_t ws_bytes, int64_t B, int64_t L,
+                           int64_t Hq, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                           int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
+                           int causal, float scale, void *stream);
+
 /* ----------------------------------------------------------- measurement */
 
 /* Streaming-read probe: one launch of `blocks` workgroups of 256 threads

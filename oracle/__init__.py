@@ -84,6 +84,8 @@ def _load():
                 "orc_gelu_mul": (None, [P, P, I64, P]),
                 "orc_mlp_chain": (None, [P, P, P, P, P, INT, I64, I64, I64, P, P, P, P]),
                 "orc_gate_residual_ada_norm": (None, [P, P, P, P, INT, ctypes.c_float, I64, I64, P, P, P]),
+                "orc_norm_rope": (None, [P, P, P, P, I64, I64, I64, I64, I64, INT, ctypes.c_float, ctypes.c_float, P]),
+                "orc_attention": (None, [P, I64, P, P, P, I64, I64, I64, ctypes.c_float, P, P]),
                 "orc_fp4_decode": (ctypes.c_double, [ctypes.c_uint8]),
                 "orc_fp4_encode": (ctypes.c_uint8, [ctypes.c_double]),
                 "orc_mxfp4_quantize_rows": (None, [P, I64, I64, P, P]),
@@ -346,3 +348,40 @@ def mxfp4_dequant_rows(codes, scales) -> np.ndarray:
     out = np.empty((N, K), np.float64)
     _load().orc_mxfp4_dequant_rows(_p(codes), _p(scales), N, K, _p(out))
     return out
+
+
+# ------------------------------------------------- attention and its cache
+
+def norm_rope(x, w, inv_freq, positions, rot, interleaved, rot_scale=1.0, eps=0.0):
+    """Normed (w given) and rotated heads of x (T x heads x D bf16 bits), fp64, unrounded."""
+    x = _c(x, np.uint16)
+    T, heads, D = x.shape
+    out = np.empty((T, heads, D), np.float64)
+    w = None if w is None else _c(w, np.uint16)
+    inv_freq = None if rot == 0 else _c(inv_freq, np.float32)
+    positions = None if rot == 0 else _c(positions, np.int32)
+    _load().orc_norm_rope(_p(x), _p(w), _p(inv_freq), _p(positions), T, heads, D, rot, heads * D, int(interleaved),
+                          rot_scale, eps, _p(out))
+    return out
+
+
+def attention(q, k, v, limits, scale):
+    """(out, wabs) of rows q (n x Hq x D bf16 bits) over keys k, values v (m x Hkv x D): row i sees the first
+    limits[i] keys; out = softmax . v and wabs = softmax . |v|, fp64, zero where a row sees nothing."""
+    q, k, v = (_c(a, np.uint16) for a in (q, k, v))
+    n, hq, D = q.shape
+    m, hkv = k.shape[:2]
+    limits = _c(limits, np.int64)
+    out, wabs = np.zeros((n, hq, D)), np.zeros((n, hq, D))
+    if n == 0 or m == 0:
+        return out, wabs
+    for h in range(hq):
+        g = h // (hq // hkv)
+        rows = np.arange(m, dtype=np.int64) * (hkv * D * 2) + g * D * 2
+        kp = _c(rows + k.ctypes.data, np.int64)
+        vp = _c(rows + v.ctypes.data, np.int64)
+        o, a = np.empty((n, D)), np.empty((n, D))
+        _load().orc_attention(ctypes.c_void_p(q.ctypes.data + h * D * 2), hq * D, _p(kp), _p(vp), _p(limits), n, m, D,
+                              scale, _p(o), _p(a))
+        out[:, h], wabs[:, h] = o, a
+    return out, wabs

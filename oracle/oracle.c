@@ -560,3 +560,77 @@ void orc_mxfp4_dequant_rows(const uint8_t *codes, const uint8_t *scales, int64_t
         for (int64_t k = 0; k < K; ++k)
             out[n * K + k] = ldexp(orc_fp4_decode(codes[n * K + k]), (int)scales[n * (K / 32) + k / 32] - 127);
 }
+
+/* ------------------------------------------------- attention and its cache */
+
+/* Heads of T rows (`heads` heads of D bf16 values, rows `stride` values
+ * apart), normed with weight w (NULL: not) and rotated, unrounded (fp64,
+ * T x heads x D).  Pair j of the first `rot` channels is (j, j + rot/2), or
+ * (2j, 2j + 1) when interleaved; it turns by positions[t] * inv_freq[j]
+ * radians and is scaled by rot_scale ([RT] names the operators between the
+ * QKV and attention-out projections; the formulas are RMS norm and rotary
+ * position embedding, Su et al. 2021). */
+void orc_norm_rope(const uint16_t *x, const uint16_t *w, const float *inv_freq, const int32_t *positions,
+                   int64_t T, int64_t heads, int64_t D, int64_t rot, int64_t stride, int interleaved,
+                   float rot_scale, float eps, double *out)
+{
+    for (int64_t t = 0; t < T; ++t)
+        for (int64_t h = 0; h < heads; ++h) {
+            const uint16_t *r = x + t * stride + h * D;
+            double *o = out + (t * heads + h) * D;
+            double ss = 0.0;
+            for (int64_t d = 0; d < D; ++d) {
+                o[d] = orc_bf16_value(r[d]);
+                ss += o[d] * o[d];
+            }
+            if (w) {
+                double rms = sqrt(ss / (double)D + (double)eps);
+                for (int64_t d = 0; d < D; ++d) o[d] = o[d] / rms * orc_bf16_value(w[d]);
+            }
+            for (int64_t j = 0; j < rot / 2; ++j) {
+                int64_t ia = interleaved ? 2 * j : j, ib = interleaved ? 2 * j + 1 : j + rot / 2;
+                double angle = (double)positions[t] * (double)inv_freq[j];
+                double c = (double)rot_scale * cos(angle), s = (double)rot_scale * sin(angle);
+                double a = o[ia], b = o[ib];
+                o[ia] = a * c - b * s;
+                o[ib] = b * c + a * s;
+            }
+        }
+}
+
+/* Attention of n query rows (bf16, one head of D values, rows q_stride apart)
+ * over keys and values given row by row as pointers (one head each): row i
+ * sees the first limits[i] of the m keys.  out: n x D fp64, zero where a row
+ * sees nothing; wabs (nullable): sum_j p_j |v_j|, the size rounding errors
+ * are measured by. */
+void orc_attention(const uint16_t *q, int64_t q_stride, const uint16_t *const *k, const uint16_t *const *v,
+                   const int64_t *limits, int64_t n, int64_t m, int64_t D, float scale, double *out, double *wabs)
+{
+#pragma omp parallel for schedule(dynamic)
+    for (int64_t i = 0; i < n; ++i) {
+        int64_t lim = limits[i] < m ? limits[i] : m;
+        double *p = malloc(sizeof(double) * (size_t)(m > 0 ? m : 1));
+        double top = -INFINITY, sum = 0.0;
+        for (int64_t j = 0; j < lim; ++j) {
+            double s = 0.0;
+            for (int64_t d = 0; d < D; ++d) s += orc_bf16_value(q[i * q_stride + d]) * orc_bf16_value(k[j][d]);
+            p[j] = s * (double)scale;
+            if (p[j] > top) top = p[j];
+        }
+        for (int64_t j = 0; j < lim; ++j) {
+            p[j] = exp(p[j] - top);
+            sum += p[j];
+        }
+        for (int64_t d = 0; d < D; ++d) {
+            double o = 0.0, a = 0.0;
+            for (int64_t j = 0; j < lim; ++j) {
+                double x = orc_bf16_value(v[j][d]);
+                o += p[j] * x;
+                a += p[j] * fabs(x);
+            }
+            out[i * D + d] = lim > 0 ? o / sum : 0.0;
+            if (wabs) wabs[i * D + d] = lim > 0 ? a / sum : 0.0;
+        }
+        free(p);
+    }
+}
