@@ -113,8 +113,8 @@ int check_heads(const char* fn, int64_t Hq, int64_t Hkv, int64_t D) {
 }
 
 int check_stride(const char* fn, const char* name, int64_t stride, int64_t width) {
-    if (stride < width || stride % 8 != 0 || stride > (int64_t(1) << 30))
-        return fail(VLA_ESHAPE, fn, "%s=%lld must be a multiple of 8, at least %lld", name, (long long)stride, (long long)width);
+    if (stride < width || stride % 8 != 0 || stride > (int64_t(1) << 24))
+        return fail(VLA_ESHAPE, fn, "%s=%lld must be a multiple of 8 in %lld .. 2^24", name, (long long)stride, (long long)width);
     return VLA_OK;
 }
 

@@ -24,13 +24,12 @@
 // that of the output's own rounding and averages over the keys.  Scores,
 // maxima, sums and O are fp32; the sum is that of the unrounded weights.
 //
-// K and V rows go global -> LDS with 16-byte loads that write LDS directly,
-// double-buffered, one barrier per stage.  The 16-byte chunks of a row are
-// XOR-swizzled so that the operand reads of K (32 rows, one chunk) and the
-// transpose reads of V (4 keys x 64 bytes) spread over the banks.  A row that is no key (past the
-// range, on a page that does not exist) and channels past D load zeros from a
-// constant instead, so nothing outside the tensors is read and no stale value
-// meets a zero weight.
+// K and V rows go global -> LDS with 16-byte loads that write LDS directly.
+// The 16-byte chunks of a row are XOR-swizzled so that the operand reads of K
+// (32 rows, one chunk) and the transpose reads of V (4 keys x 64 bytes) are
+// free of bank conflicts.  A row that is no key (past the range, on a page
+// that does not exist) and channels past D load zeros, so nothing outside the
+// tensors is read and no stale value meets a zero weight.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -47,29 +46,39 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 
 constexpr int kAThreads = 256;
+constexpr float kLag = 8.0f;                     // log2 of the largest weight, see weights()
+constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data format
 
 __device__ __attribute__((aligned(16))) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
 
-// QW waves along the rows x KW waves along the keys of a stage.
-template <int DP_, int QW_, int KW_>
+// MANY: four waves of 32 query rows each share stages of 64 keys; FEW: four
+// waves share 32 query rows and each walks every fourth 32-key sub-tile
+// through LDS of its own, so that no wave waits for another before the end.
+template <int DP_, bool MANY_>
 struct ACfg {
-    static constexpr int DP = DP_, QW = QW_, KW = KW_;
-    static_assert(QW * KW * 64 == kAThreads, "four waves");
-    static constexpr int TM = 32 * QW;                       // query rows per workgroup
-    static constexpr int WK = KW == 1 ? 64 : 32;             // keys per wave per stage
-    static constexpr int ST = WK * KW;                       // keys per stage
-    static constexpr int SUB = WK / 32;                      // 32-key sub-tiles per wave per stage
+    static constexpr int DP = DP_;
+    static constexpr bool MANY = MANY_;
+    static constexpr int WAVES = DP <= 128 ? 2 : 1;          // per SIMD: 256 or 512 registers each
+    static constexpr int TM = MANY ? 128 : 32;               // query rows per workgroup
+    static constexpr int ST = MANY ? 64 : 128;               // keys per workgroup step
     static constexpr int CH = DP / 8;                        // 16-byte chunks per row
     static constexpr int RB = DP * 2;                        // bytes per row
-    static constexpr int R = WK / QW;                        // rows a wave loads per stage (of K and of V)
+    static constexpr int R = MANY ? 16 : 32;                 // rows of K (and V) a wave loads at once
     static constexpr int RPI = 1024 / RB;                    // rows per load instruction
-    static constexpr int NI = R / RPI;
-    static constexpr int HALF = ST * RB;                     // bytes of K (and of V) per stage
-    static constexpr int STAGE = 2 * HALF;
+    static constexpr int NI = R / RPI;                       // load instructions for R rows
     static constexpr int NK = DP / 16;                       // MFMA steps of K Q^T
     static constexpr int ND = DP / 32;                       // 32-channel blocks of O^T
+    // LDS buffers: MANY has K and V of two stages of 64 rows, FEW K and V of
+    // one sub-tile of 32 rows per wave, each an object of its own: the
+    // compiler orders LDS reads after the loads that write the same object
+    static constexpr int BUFS = MANY ? 4 : 2;
+    static constexpr int BUF = (MANY ? 64 : 128) * RB;
+    // FEW: the waves' results join through the same buffers, maxima and sums
+    // first, then 4 KiB for each (channel block, wave that gives it away)
+    static constexpr int ML = 4 * 2 * 64 * 4;
+    static constexpr int BLOCKS0 = (BUF - ML) / 4096;        // blocks in the first buffer
     static_assert(R % RPI == 0, "whole load instructions");
-    static_assert((KW - 1) * QW * 64 * (ND * 16 + 2) * 4 <= 2 * STAGE, "the key waves join through the stage buffers");
+    static_assert(MANY || BLOCKS0 + BUF / 4096 >= 3 * ND, "the waves' results fit the two buffers");
 };
 
 // Position of a row's 16-byte chunks in LDS: chunk ^ swizzle.
@@ -82,25 +91,36 @@ __device__ __forceinline__ int swz_v(int row) { return DP == 64 ? ((row >> 1) & 
 // cache named by the page tables (first the prefix's keys, then the suffix's).
 struct PackedKeys {
     const uint16_t *k, *v;     // row 0 of this head
-    int64_t k_stride, v_stride;
+    int k_stride, v_stride;    // bytes
     int n;
 };
 struct PagedKeys {
     const uint16_t *k, *v;     // slot 0 of this head
-    int64_t stride;
+    uint32_t stride;           // bytes
     const int32_t *prefix, *suffix;
     int n_prefix, n;           // prefix keys, all keys
     int page_log2;
     uint32_t num_pages;
+    // slot of key j, or -1 where its page does not exist
+    __device__ __forceinline__ int slot(int key) const {
+        const bool pre = key < n_prefix;
+        const int j = pre ? key : key - n_prefix;
+        const uint32_t page = static_cast<uint32_t>((pre ? prefix : suffix)[j >> page_log2]);
+        const int at = static_cast<int>((page << page_log2) | (j & ((1 << page_log2) - 1)));
+        return page < num_pages ? at : -1;
+    }
 };
 
+// A wave's partial result for its 32 rows: lane = row l % 32, O^T unnormalised,
+// m the running maximum in log2 units, l the sum of weights (of this lane's
+// keys until finish()).
 template <class C>
 struct State {
     f32x16_t acc[C::ND];
     float m, l;
+    uint32_t late;     // sub-tiles left to add_late
 };
 
-// Exchange between the wave halves: the value of lane ^ 32 combined by max / +.
 __device__ __forceinline__ float half_max(float x) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
@@ -110,13 +130,13 @@ __device__ __forceinline__ float half_sum(float x) {
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Whether 32 rows of V in a stage buffer hold an infinity or NaN (any chunk
-// order: all of them are looked at).
+// Whether 32 rows of V in LDS hold an infinity or NaN (in any chunk order:
+// all of them are looked at).
 template <class C>
-__device__ __forceinline__ bool has_nonfinite(const uint8_t* buf, int row) {
-    const uint8_t* v = buf + C::HALF + row * C::RB + (threadIdx.x & 63) * 16;
+__device__ __forceinline__ bool has_nonfinite(const uint8_t* v) {
+    v += (threadIdx.x & 63) * 16;
     bool bad = false;
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 32 * C::RB / 1024; ++i) {
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + i * 1024);
 #pragma unroll
@@ -126,286 +146,446 @@ __device__ __forceinline__ bool has_nonfinite(const uint8_t* buf, int row) {
     return __any(bad);
 }
 
-// O += P V for 32 keys of the stage, one key after another, leaving out the
-// keys the lane's row does not see (key >= limit, or not in vm).  Slow and
-// rare: only values that are infinite or NaN need it.
-template <class C>
-__device__ __forceinline__ void add_by_key(const uint8_t* buf, int row, int limit, uint32_t vm, const uint32_t* pw,
-                                           State<C>& st) {
-    const int lane = threadIdx.x & 63, l32 = lane & 31, g2 = lane >> 5;
-#pragma unroll 1
-    for (int r = 0; r < 32; ++r) {
-        // weight of key r: accumulator value 4 (r / 8) + r % 4 of half (r / 4) % 2
-        const int wi = 2 * (r >> 3) + ((r & 3) >> 1);
-        uint32_t w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w = wi == i ? pw[i] : w;
-        w = __shfl(w, l32 + 32 * ((r >> 2) & 1), 64);
-        const float p = __uint_as_float((r & 1) ? (w & 0xFFFF0000u) : (w << 16));
-        const bool seen = r < limit && ((vm >> r) & 1u);
-        const uint8_t* v = buf + C::HALF + (row + r) * C::RB + g2 * 8;
-        const int sw = swz_v<C::DP>(r);
-#pragma unroll
-        for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const uint2 x = *reinterpret_cast<const uint2*>(v + ((4 * d + a) ^ sw) * 16);
-                const float f[4] = {__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
-                                    __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u)};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) st.acc[d][4 * a + j] += seen ? p * f[j] : 0.0f;
-            }
-    }
-}
-
-// Walks keys k0 .. k1-1 (a uniform range) for this wave's 32 rows.  q: the
-// lane's query row or nullptr; klim: keys the lane's row may see (its first
-// klim keys); D channels.  Leaves the row's partial result of this wave's
-// keys in st.
+// What one wave needs to walk keys for its 32 rows.
 template <class C, class Keys>
-__device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
-                                       uint8_t* buf0, uint8_t* buf1, State<C>& st) {
-    constexpr bool PAGED = std::is_same<Keys, PagedKeys>::value;
-    constexpr int DP = C::DP;
-    const int lane = threadIdx.x & 63, l32 = lane & 31, g2 = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int qw = wave % C::QW, kw = wave / C::QW;
-
-    // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
+struct Walk {
+    static constexpr bool PAGED = std::is_same<Keys, PagedKeys>::value;
+    const Keys& keys;
+    const uint16_t* q;         // the lane's row, or nullptr
+    int klim;                  // the lane's row sees keys below this
+    int kfull, kmax;           // every row sees keys below kfull, none one at or past kmax
+    int D;
+    float c;                   // scale * log2(e)
+    int l32, g2;
+    int kaddr, vaddr, vswz;    // LDS operand addresses within 32 rows
+    int lrow, lpos;            // row and chunk position this lane loads, within one instruction
     bf16x8_t qf[C::NK];
-#pragma unroll
-    for (int kk = 0; kk < C::NK; ++kk) {
-        const int d = 16 * kk + 8 * g2;
-        u32x4_t w = {0, 0, 0, 0};
-        if (q && d < D) w = *reinterpret_cast<const u32x4_t*>(q + d);
-        qf[kk] = as_bf16x8(w);
-    }
-    // bounds of the rows this wave holds: all rows see keys below kfull, none
-    // sees a key at or past kmax
-    int kfull = q ? klim : INT_MAX, kmax = q ? klim : 0;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        kfull = min(kfull, __shfl_xor(kfull, o, 64));
-        kmax = max(kmax, __shfl_xor(kmax, o, 64));
-    }
-    kfull = __builtin_amdgcn_readfirstlane(kfull);
-    kmax = __builtin_amdgcn_readfirstlane(kmax);
+    State<C>& st;
 
+    __device__ __forceinline__ Walk(const Keys& keys_, const uint16_t* q_, int klim_, int D_, float c_, State<C>& st_)
+        : keys(keys_), q(q_), klim(klim_), D(D_), c(c_), st(st_) {
+        const int lane = threadIdx.x & 63;
+        l32 = lane & 31;
+        g2 = lane >> 5;
+        // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
 #pragma unroll
-    for (int i = 0; i < C::ND; ++i) st.acc[i] = f32x16_t{};
-    st.m = -__builtin_inff();
-    st.l = 0.0f;
-
-    const int n_stages = (k1 - k0 + C::ST - 1) / C::ST;
-    if (n_stages <= 0) return;
-
-    // ---- loads of a stage.  Wave (qw, kw) loads R rows of K and of V of key
-    //      window kw; lane l keeps the slot of window key l % WK.
-    const int row0 = kw * C::WK + qw * C::R;                      // first stage row this wave loads
-    const int lrow = lane / C::CH, lpos = lane % C::CH;
-    auto table_entry = [&](int s) __attribute__((always_inline)) -> int {
-        if constexpr (!PAGED) {
-            return 0;
-        } else {
-            const int key = k0 + s * C::ST + kw * C::WK + (lane & (C::WK - 1));
-            if (key >= k1) return -1;
-            const bool pre = key < keys.n_prefix;
-            const int j = pre ? key : key - keys.n_prefix;
-            const int32_t* t = pre ? keys.prefix : keys.suffix;
-            const uint32_t page = static_cast<uint32_t>(t[j >> keys.page_log2]);
-            if (page >= keys.num_pages) return -1;
-            return static_cast<int>((page << keys.page_log2) | (j & ((1 << keys.page_log2) - 1)));
+        for (int kk = 0; kk < C::NK; ++kk) {
+            const int d = 16 * kk + 8 * g2;
+            u32x4_t w = {0, 0, 0, 0};
+            if (q && d < D) w = *reinterpret_cast<const u32x4_t*>(q + d);
+            qf[kk] = as_bf16x8(w);
         }
-    };
-    auto issue = [&](uint8_t* buf, int s, int slot) __attribute__((always_inline)) {
+        kfull = q ? klim : INT_MAX;
+        kmax = q ? klim : 0;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+            kfull = min(kfull, __shfl_xor(kfull, o, 64));
+            kmax = max(kmax, __shfl_xor(kmax, o, 64));
+        }
+        kfull = __builtin_amdgcn_readfirstlane(kfull);
+        kmax = __builtin_amdgcn_readfirstlane(kmax);
+#pragma unroll
+        for (int i = 0; i < C::ND; ++i) st.acc[i] = f32x16_t{};
+        st.m = -__builtin_inff();
+        st.l = 0.0f;
+        st.late = 0;
+        // A operand of K Q^T: row l32, chunk (2 kk + g2) ^ swizzle = kaddr ^ (kk << 5)
+        kaddr = l32 * C::RB + ((swz_k<C::DP>(l32) ^ g2) << 4);
+        // transpose read: key 4 g2 + i16/4 of an 8-key group, channels 16 g16 + 4 (i16 % 4)
+        const int i16 = lane & 15, g16 = (lane >> 4) & 1;
+        vswz = swz_v<C::DP>(i16 >> 2);
+        vaddr = (4 * g2 + (i16 >> 2)) * C::RB + (2 * g16 + ((i16 & 3) >> 1)) * 16 + (i16 & 1) * 8;
+        lrow = lane / C::CH;
+        lpos = lane % C::CH;
+    }
+
+    // ---- loads of R rows of K or V into LDS at dst; row0: their number in
+    //      the buffer modulo 32 (for the swizzle)
+    template <bool V>
+    __device__ __forceinline__ void load_packed(uint8_t* dst, int row0, int key0, int k1) const {
+        // a buffer that ends with the last key: rows past it load zeros
+        const int stride = V ? keys.v_stride : keys.k_stride;
+        const int left = min(k1 - key0, C::R);
+        const int bytes = left > 0 ? (left - 1) * stride + D * 2 : 0;
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(V ? keys.v : keys.k) + static_cast<int64_t>(key0) * stride), 0,
+            bytes, kBufferWord3);
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) {
-            const int rr = i * C::RPI + lrow;                     // row among this wave's R
-            const int sr = row0 + rr;                             // row of the stage
-            const int ck = lpos ^ swz_k<DP>(sr), cv = lpos ^ swz_v<DP>(sr);
-            const uint16_t *pk, *pv;
-            bool ok;
-            if constexpr (PAGED) {
-                const int sl = __shfl(slot, qw * C::R + rr, 64);
-                ok = sl >= 0;
-                const int64_t off = static_cast<int64_t>(sl) * keys.stride;
-                pk = keys.k + off;
-                pv = keys.v + off;
-            } else {
-                const int key = k0 + s * C::ST + sr;
-                ok = key < k1;
-                pk = keys.k + key * keys.k_stride;
-                pv = keys.v + key * keys.v_stride;
-            }
-            const uint16_t* zero = reinterpret_cast<const uint16_t*>(kZeroChunk);
-            const uint16_t* sk = ok && ck * 8 < D ? pk + ck * 8 : zero;
-            const uint16_t* sv = ok && cv * 8 < D ? pv + cv * 8 : zero;
-            uint8_t* dst = buf + (row0 + i * C::RPI) * C::RB;
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)sk,
-                                             (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)sv,
-                                             (__attribute__((address_space(3))) void*)(dst + C::HALF), 16, 0, 0);
+            const int row = row0 + i * C::RPI + lrow;
+            const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
+            const uint32_t off = ch * 8 < D ? static_cast<uint32_t>(lrow * stride + ch * 16) : 0x80000000u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, off,
+                                                     i * C::RPI * stride, 0, 0);
         }
-    };
-
-    // ---- LDS operand addresses within a stage
-    const int kbase = (kw * C::WK + l32) * C::RB + ((swz_k<DP>(l32) ^ g2) << 4);      // ^ (kk << 5)
-    const int i16 = lane & 15, g16 = (lane >> 4) & 1;
-    // transpose read: key 4 g2 + i16/4 of an 8-key group, channels 16 g16 + 4 (i16 % 4)
-    const int vrow = 4 * g2 + (i16 >> 2);
-    const int vbase = C::HALF + (kw * C::WK + vrow) * C::RB + (i16 & 1) * 8;
-    const int vchunk = 2 * g16 + ((i16 & 3) >> 1), vswz = swz_v<DP>(i16 >> 2);
-
-    auto compute = [&](const uint8_t* buf, int s, uint64_t vmask) __attribute__((always_inline)) {
+    }
+    template <bool V>
+    __device__ __forceinline__ void load_paged(uint8_t* dst, int row0, int slot, int from) const {
+        const uint16_t* base = V ? keys.v : keys.k;
 #pragma unroll
-        for (int sub = 0; sub < C::SUB; ++sub) {
-            const int key0 = k0 + s * C::ST + kw * C::WK + sub * 32;
-            if (key0 >= kmax) break;
-            f32x16_t sc = f32x16_t{};
+        for (int i = 0; i < C::NI; ++i) {
+            const int row = row0 + i * C::RPI + lrow;
+            const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
+            const int sl = __shfl(slot, from + i * C::RPI + lrow, 64);
+            const uint64_t at = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(static_cast<uint32_t>(sl)) * keys.stride + ch * 16;
+            const uint64_t src = (sl >= 0 && ch * 8 < D) ? at : reinterpret_cast<uint64_t>(kZeroChunk);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                             (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, 0, 0);
+        }
+    }
+
+    // ---- one 32-key sub-tile in LDS
+    __device__ __forceinline__ f32x16_t scores(const uint8_t* kt) const {
+        u32x4_t kf[C::NK];
 #pragma unroll
-            for (int kk = 0; kk < C::NK; ++kk) {
-                const u32x4_t kf = *reinterpret_cast<const u32x4_t*>(buf + ((kbase ^ (kk << 5)) + sub * 32 * C::RB));
-                sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf), qf[kk], sc, 0, 0, 0);
+        for (int kk = 0; kk < C::NK; ++kk) kf[kk] = *reinterpret_cast<const u32x4_t*>(kt + (kaddr ^ (kk << 5)));
+        f32x16_t sc = f32x16_t{};
+#pragma unroll
+        for (int kk = 0; kk < C::NK; ++kk)
+            sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[kk]), qf[kk], sc, 0, 0, 0);
+        return sc;
+    }
+    // Scores in log2 units; those a row does not see become -inf.
+    __device__ __forceinline__ void scale_and_mask(f32x16_t& sc, int key0, uint32_t vm) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sc[i] *= c;
+        if (key0 + 32 > kfull) {
+            const int lim = klim - key0 - 4 * g2;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[i] = 8 * (i / 4) + (i % 4) < lim ? sc[i] : -__builtin_inff();
+        }
+        if (vm != 0xFFFFFFFFu) {
+            const uint32_t w = vm >> (4 * g2);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sc[i] = (w >> (8 * (i / 4) + (i % 4))) & 1u ? sc[i] : -__builtin_inff();
+        }
+    }
+    // Weights, as bf16 pairs in accumulator order; moves the running maximum.
+    __device__ __forceinline__ void weights(const f32x16_t& sc, uint32_t* pw) const {
+        float mx = fmaxf(sc[0], sc[1]);
+#pragma unroll
+        for (int i = 2; i < 16; i += 2) mx = fmaxf(fmaxf(sc[i], sc[i + 1]), mx);
+        mx = half_max(mx);
+        // the running maximum follows once a row's scores pass it by kLag:
+        // until then weights are at most 2^kLag and lose no precision
+        if (__any(mx > st.m + kLag)) {
+            const float mn = fmaxf(st.m, mx);
+            const float al = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
+            st.m = mn;
+            st.l *= al;
+#pragma unroll
+            for (int d = 0; d < C::ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) st.acc[d][i] *= al;
+        }
+        // a row that has seen no key yet: weights exp2(-inf) = 0
+        const float m0 = st.m == -__builtin_inff() ? 0.0f : st.m;
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float p0 = __builtin_amdgcn_exp2f(sc[2 * i] - m0);
+            const float p1 = __builtin_amdgcn_exp2f(sc[2 * i + 1] - m0);
+            s0 += p0;
+            s1 += p1;
+            pw[i] = f32x2_to_bf16x2(p0, p1);
+        }
+        st.l += s0 + s1;
+    }
+    // V^T fragments: 16 keys (step k2) x 32 channels (block d)
+    __device__ __forceinline__ bf16x8_t v_frag(const uint8_t* vt, int k2, int d) const {
+        const uint8_t* va = vt + vaddr + ((d * 4) ^ vswz) * 16 + 16 * k2 * C::RB;
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)va);
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(va + 8 * C::RB));
+        const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
+        const u32x4_t vf = {a.x, a.y, b.x, b.y};
+        return as_bf16x8(vf);
+    }
+    __device__ __forceinline__ void add(const uint8_t* vt, const uint32_t* pw) const {
+        bf16x8_t vf[2][C::ND];
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2)
+#pragma unroll
+            for (int d = 0; d < C::ND; ++d) vf[k2][d] = v_frag(vt, k2, d);
+#pragma unroll
+        for (int k2 = 0; k2 < 2; ++k2) {
+            const u32x4_t pv = {pw[4 * k2], pw[4 * k2 + 1], pw[4 * k2 + 2], pw[4 * k2 + 3]};
+#pragma unroll
+            for (int d = 0; d < C::ND; ++d)
+                st.acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k2][d], as_bf16x8(pv), st.acc[d], 0, 0, 0);
+        }
+    }
+    // A zero weight times an infinity or NaN is not zero: a sub-tile that
+    // some row sees only in part and whose V holds one is left out of the
+    // product and added at the end, key by key.  Bit b of `late` is the
+    // sub-tile that ends 32 b to 32 b + 31 keys past the last key that every
+    // row sees; a tile of at most 128 rows ends at most 128 + 31 keys past it.
+    __device__ __forceinline__ bool put_off(const uint8_t* vt, int key0) const {
+        if (key0 + 32 <= kfull || !has_nonfinite<C>(vt)) return false;
+        st.late |= 1u << ((key0 + 32 - kfull) >> 5);
+        return true;
+    }
+    // key0_of: first key of this wave's sub-tile that holds a key, or -1 (another wave's)
+    template <class F>
+    __device__ __forceinline__ void add_late(int k1, F&& key0_of) const {
+        if (!st.late) return;
+        for (int key = max(kfull - 31, 0); key < min(kmax, k1); ++key) {
+            const int key0 = key0_of(key);
+            if (key0 < 0 || key0 + 32 <= kfull || !((st.late >> ((key0 + 32 - kfull) >> 5)) & 1u)) continue;
+            const uint16_t *kr, *vr;
+            if constexpr (PAGED) {
+                const int sl = keys.slot(key);
+                if (sl < 0) continue;
+                const int64_t at = static_cast<int64_t>(sl) * (keys.stride / 2);
+                kr = keys.k + at;
+                vr = keys.v + at;
+            } else {
+                kr = keys.k + static_cast<int64_t>(key) * (keys.k_stride / 2);
+                vr = keys.v + static_cast<int64_t>(key) * (keys.v_stride / 2);
             }
-            // masks: rows that end inside the tile, rows of missing pages
-            const uint32_t vm = static_cast<uint32_t>(vmask >> (32 * sub));
-            const bool ragged = key0 + 32 > kfull;                // some row does not see every key here
-            if (ragged || vm != 0xFFFFFFFFu) {
+            if (!q || key >= klim) continue;
+            float s = 0.0f;
+            for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * bf16_to_f32(kr[d]);
+            const float p = bf16_to_f32(f32_to_bf16(__builtin_amdgcn_exp2f(s * c - st.m)));
+#pragma unroll
+            for (int d = 0; d < C::ND; ++d)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int r = 8 * (i / 4) + 4 * g2 + (i % 4);
-                    sc[i] = (key0 + r < klim && ((vm >> r) & 1u)) ? sc[i] : -__builtin_inff();
+                    const int ch = 32 * d + 8 * (i / 4) + 4 * g2 + (i % 4);
+                    if (ch < D) st.acc[d][i] += p * bf16_to_f32(vr[ch]);
                 }
-            }
-            float mx = sc[0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i]);
-            mx = half_max(mx);
-            if (__any(mx > st.m)) {
-                const float mn = fmaxf(st.m, mx);
-                const float al = mn == st.m ? 1.0f : __builtin_amdgcn_exp2f((st.m - mn) * c);
-                st.m = mn;
-                st.l *= al;
-#pragma unroll
-                for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) st.acc[d][i] *= al;
-            }
-            // a row that has seen no key yet: weights exp2(-inf) = 0
-            const float mc = st.m == -__builtin_inff() ? 0.0f : st.m * c;
-            float sum = 0.0f;
-            uint32_t pw[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i], c, -mc));
-                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[2 * i + 1], c, -mc));
-                sum += p0 + p1;
-                pw[i] = f32x2_to_bf16x2(p0, p1);
-            }
-            st.l += sum;
-            // a product with a zero weight is not zero where V is infinite or
-            // NaN: such a tile that some row sees in part goes key by key
-            if (ragged && has_nonfinite<C>(buf, kw * C::WK + sub * 32)) {
-                add_by_key<C>(buf, kw * C::WK + sub * 32, klim - key0, vm, pw, st);
-                continue;
-            }
-            // O^T += V^T P^T, 16 keys per step
-#pragma unroll
-            for (int k2 = 0; k2 < 2; ++k2) {
-                const u32x4_t pv = {pw[4 * k2], pw[4 * k2 + 1], pw[4 * k2 + 2], pw[4 * k2 + 3]};
-                const bf16x8_t pf = as_bf16x8(pv);
-#pragma unroll
-                for (int d = 0; d < C::ND; ++d) {
-                    const uint8_t* va = buf + vbase + (((d * 4) ^ vswz) + vchunk) * 16 + (sub * 32 + 16 * k2) * C::RB;
-                    const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)va);
-                    const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                        (__attribute__((address_space(3))) s16x4_t*)(va + 8 * C::RB));
-                    const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
-                    const u32x4_t vf = {a.x, a.y, b.x, b.y};
-                    st.acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vf), pf, st.acc[d], 0, 0, 0);
-                }
-            }
+        }
+    }
+};
+
+// s_waitcnt immediates: at most n vector-memory operations outstanding, LDS
+// unconstrained; and all vector-memory and LDS operations done.
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0F70; }
+constexpr int kWaitAll = 0x0070;
+constexpr int kWaitLds = 0xC07F;
+
+// A point that no memory operation or instruction moves across.
+template <int IMM>
+__device__ __forceinline__ void wait_here() {
+    __builtin_amdgcn_sched_barrier(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(IMM);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Keys k0 .. k1-1 (a uniform range) for the wave's 32 rows, the workgroup's
+// four waves sharing each stage of 64 keys.
+template <class C, class Keys>
+__device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
+                                            uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
+    Walk<C, Keys> w(keys, q, klim, D, c, st);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n_stages = (k1 - k0 + 63) / 64;
+    if (n_stages <= 0) return;
+    const int row0 = wave * C::R;                                 // rows of a stage this wave loads
+    // the lane's key of a stage: its slot, for the loads and the masks
+    auto entry = [&](int s) __attribute__((always_inline)) -> int {
+        if constexpr (Walk<C, Keys>::PAGED) {
+            const int key = k0 + s * 64 + (threadIdx.x & 63);
+            return key < k1 ? keys.slot(key) : -1;
+        } else {
+            return 0;
         }
     };
-
+    auto issue = [&](uint8_t* kb, uint8_t* vb, int s, int slot) __attribute__((always_inline)) {
+        if constexpr (Walk<C, Keys>::PAGED) {
+            w.template load_paged<false>(kb + row0 * C::RB, row0, slot, row0);
+            w.template load_paged<true>(vb + row0 * C::RB, row0, slot, row0);
+        } else {
+            w.template load_packed<false>(kb + row0 * C::RB, row0, k0 + s * 64 + row0, k1);
+            w.template load_packed<true>(vb + row0 * C::RB, row0, k0 + s * 64 + row0, k1);
+        }
+    };
     auto valid = [&](int slot) __attribute__((always_inline)) -> uint64_t {
-        if constexpr (PAGED) return __ballot(slot >= 0);
+        if constexpr (Walk<C, Keys>::PAGED) return __ballot(slot >= 0);
         else return ~uint64_t(0);
     };
-    // stage s lives in buffer s % 2; its loads are issued while stage s-1 is
+    // stage s lives in buffers s % 2; its loads are issued while stage s-1 is
     // computed, its table entries are read one stage earlier still
-    int slot = table_entry(0);
-    issue(buf0, 0, slot);
+    int slot = entry(0);
+    issue(kb0, vb0, 0, slot);
     uint64_t vcur = valid(slot);
-    slot = n_stages > 1 ? table_entry(1) : 0;
-    auto step = [&](const uint8_t* cur, uint8_t* next, int s) __attribute__((always_inline)) {
+    slot = n_stages > 1 ? entry(1) : 0;
+    auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s) __attribute__((always_inline)) {
         // this wave's loads of stage s have landed and its reads of stage s-1
-        // are done (vmcnt 0, lgkmcnt 0); the barrier says so for every wave
-        __builtin_amdgcn_sched_barrier(0);
-        __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        __builtin_amdgcn_s_waitcnt(0x0070);
+        // are done; the barrier says so for every wave
+        wait_here<kWaitAll>();
         __builtin_amdgcn_s_barrier();
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         __builtin_amdgcn_sched_barrier(0);
         uint64_t vnext = 0;
         if (s + 1 < n_stages) {
-            issue(next, s + 1, slot);
+            issue(kn, vn, s + 1, slot);
             vnext = valid(slot);
-            if (s + 2 < n_stages) slot = table_entry(s + 2);
+            if (s + 2 < n_stages) slot = entry(s + 2);
         }
-        compute(cur, s, vcur);
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const int key0 = k0 + s * 64 + sub * 32;
+            if (key0 >= w.kmax) break;
+            f32x16_t sc = w.scores(kc + sub * 32 * C::RB);
+            w.scale_and_mask(sc, key0, static_cast<uint32_t>(vcur >> (32 * sub)));
+            uint32_t pw[8];
+            w.weights(sc, pw);
+            if (!w.put_off(vc + sub * 32 * C::RB, key0)) w.add(vc + sub * 32 * C::RB, pw);
+        }
         vcur = vnext;
     };
     for (int s = 0; s < n_stages; s += 2) {
-        step(buf0, buf1, s);
-        if (s + 1 < n_stages) step(buf1, buf0, s + 1);
+        step(kb0, vb0, kb1, vb1, s);
+        if (s + 1 < n_stages) step(kb1, vb1, kb0, vb0, s + 1);
     }
     st.l = half_sum(st.l);
+    w.add_late(k1, [&](int key) { return k0 + (key - k0) / 32 * 32; });
 }
 
-// Joins the key waves' partial results into the waves with kw = 0.
-template <class C>
-__device__ __forceinline__ void join_key_waves(uint8_t* buf0, uint8_t* buf1, float c, State<C>& st) {
-    if constexpr (C::KW > 1) {
-        const int lane = threadIdx.x & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        const int qw = wave % C::QW, kw = wave / C::QW;
-        constexpr int PER = 64 * (C::ND * 16 + 2);                // floats per wave
-        constexpr int PERBUF = C::STAGE / (PER * 4);              // waves' states per buffer
-        static_assert(PERBUF >= 1 && 2 * PERBUF >= (C::KW - 1) * C::QW, "room for every joining wave");
-        auto area = [&](int k) -> float* {
-            const int at = (k - 1) * C::QW + qw;
-            return reinterpret_cast<float*>(at < PERBUF ? buf0 : buf1) + (at % PERBUF) * PER + lane;
-        };
-        __syncthreads();                                          // every wave is past its last stage
-        if (kw > 0) {
-            float* a = area(kw);
-#pragma unroll
-            for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) a[(d * 16 + i) * 64] = st.acc[d][i];
-            a[C::ND * 16 * 64] = st.m;
-            a[(C::ND * 16 + 1) * 64] = st.l;
+// Keys k0 .. k1-1 for 32 rows that the four waves share: wave w takes
+// sub-tiles w, w + 4, ...  Each wave's K and V have one place in LDS: K of
+// the next sub-tile is loaded as soon as this one's scores are formed, V as
+// soon as it has been added, so each load has the other half of a sub-tile's
+// work to arrive in and 16 (D <= 64: 8, D > 128: 32) KiB per wave are in flight.
+template <class C, class Keys>
+__device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
+                                           uint8_t* kb, uint8_t* vb, State<C>& st) {
+    constexpr bool PAGED = Walk<C, Keys>::PAGED;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    kb += wave * 32 * C::RB;
+    vb += wave * 32 * C::RB;
+    const int first = k0 + wave * 32;
+    const int n = k1 > first ? (k1 - first + 127) / 128 : 0;
+    auto entry = [&](int t) __attribute__((always_inline)) -> int {
+        if constexpr (PAGED) {
+            const int key = first + t * 128 + (threadIdx.x & 31);
+            return key < k1 ? keys.slot(key) : -1;
+        } else {
+            return 0;
         }
-        __syncthreads();
-        if (kw == 0) {
+    };
+    int slot = n > 0 ? entry(0) : 0;
+    Walk<C, Keys> w(keys, q, klim, D, c, st);
+    if (n <= 0) return;
+    auto load_k = [&](int t, int sl) __attribute__((always_inline)) {
+        if constexpr (PAGED) w.template load_paged<false>(kb, 0, sl, 0);
+        else w.template load_packed<false>(kb, 0, first + t * 128, k1);
+    };
+    auto load_v = [&](int t, int sl) __attribute__((always_inline)) {
+        if constexpr (PAGED) w.template load_paged<true>(vb, 0, sl, 0);
+        else w.template load_packed<true>(vb, 0, first + t * 128, k1);
+    };
+    load_k(0, slot);
+    load_v(0, slot);
+    int next = n > 1 ? entry(1) : 0;
+    for (int t = 0; t < n; ++t) {
+        const int key0 = first + t * 128;
+        const bool more = t + 1 < n;
+        // order of the wave's loads: K(t), entry(t+1), V(t), K(t+1), ...; here
+        // V(t) and an entry are younger than K(t)
+        wait_here<wait_vm(C::NI)>();
+        f32x16_t sc = w.scores(kb);
+        const uint32_t vm = PAGED ? static_cast<uint32_t>(__ballot(slot >= 0)) : 0xFFFFFFFFu;
+        wait_here<kWaitLds>();                                    // K(t) has been read
+        if (more) {
+            slot = next;
+            load_k(t + 1, slot);
+            if (t + 2 < n) next = entry(t + 2);
+        }
+        w.scale_and_mask(sc, key0, vm);
+        uint32_t pw[8];
+        w.weights(sc, pw);
+        if (more) wait_here<wait_vm(C::NI)>();
+        else wait_here<wait_vm(0)>();
+        if (!w.put_off(vb, key0)) w.add(vb, pw);
+        wait_here<kWaitLds>();                                    // V(t) has been read
+        if (more) load_v(t + 1, slot);
+    }
+    st.l = half_sum(st.l);
+    w.add_late(k1, [&](int key) {
+        const int t = key - k0;
+        return (t >> 5 & 3) == wave ? k0 + (t & ~31) : -1;
+    });
+}
+
+// Joins the four waves' results for the same rows: wave w is left with
+// channel blocks d = w, w + 4 of the whole (in acc[d]).
+template <class C>
+__device__ __forceinline__ void join_waves(uint8_t* buf0, uint8_t* buf1, State<C>& st) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    float* const ml = reinterpret_cast<float*>(buf0);             // [wave][m, l][lane]
+    auto place = [&](int d, int from) __attribute__((always_inline)) -> float* {
+        const int at = d * 3 + (from > (d & 3) ? from - 1 : from);
+        uint8_t* const p = at < C::BLOCKS0 ? buf0 + C::ML + at * 4096 : buf1 + (at - C::BLOCKS0) * 4096;
+        return reinterpret_cast<float*>(p) + lane;
+    };
+    __syncthreads();                                              // every wave is past its last sub-tile
+    ml[(2 * wave) * 64 + lane] = st.m;
+    ml[(2 * wave + 1) * 64 + lane] = st.l;
 #pragma unroll
-            for (int k = 1; k < C::KW; ++k) {
-                const float* a = area(k);
-                const float m2 = a[C::ND * 16 * 64], l2 = a[(C::ND * 16 + 1) * 64];
-                const float mn = fmaxf(st.m, m2);
-                const float s1 = st.m == mn ? 1.0f : __builtin_amdgcn_exp2f((st.m - mn) * c);
-                const float s2 = m2 == mn ? 1.0f : __builtin_amdgcn_exp2f((m2 - mn) * c);
-                st.m = mn;
-                st.l = st.l * s1 + l2 * s2;
+    for (int d = 0; d < C::ND; ++d) {
+        if ((d & 3) == wave) continue;
+        float* const at = place(d, wave);
 #pragma unroll
-                for (int d = 0; d < C::ND; ++d)
+        for (int i = 0; i < 16; ++i) at[i * 64] = st.acc[d][i];
+    }
+    __syncthreads();
+    float m = -__builtin_inff(), scale[4], l = 0.0f, own = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) st.acc[d][i] = st.acc[d][i] * s1 + a[(d * 16 + i) * 64] * s2;
-            }
+    for (int w = 0; w < 4; ++w) m = fmaxf(m, ml[(2 * w) * 64 + lane]);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float mw = ml[(2 * w) * 64 + lane];
+        scale[w] = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
+        l += ml[(2 * w + 1) * 64 + lane] * scale[w];
+        own = w == wave ? scale[w] : own;
+    }
+#pragma unroll
+    for (int d = 0; d < C::ND; ++d) {
+        if ((d & 3) != wave) continue;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st.acc[d][i] *= own;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if (w == (d & 3)) continue;
+            const float* const at = place(d, w);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) st.acc[d][i] += at[i * 64] * scale[w];
         }
     }
+    st.m = m;
+    st.l = l;
 }
+
+// Whether this wave holds channel block d of its rows' result.
+template <class C>
+__device__ __forceinline__ bool holds_block(int d) {
+    return C::MANY || (d & 3) == __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+}
+
+// First of this wave's 32 rows in the workgroup's tile.
+template <class C>
+__device__ __forceinline__ int wave_row() {
+    return C::MANY ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 : 0;
+}
+
+template <class C, class Keys>
+__device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
+                                       uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, State<C>& st) {
+    if constexpr (C::MANY) {
+        attend_many<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
+    } else {
+        attend_few<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
+        join_waves<C>(b0, b1, st);
+    }
+}
+
+#define ATTN_BUFFERS                                                                          \
+    __shared__ __attribute__((aligned(16))) uint8_t b0[C::BUF], b1[C::BUF];                   \
+    __shared__ __attribute__((aligned(16))) uint8_t b2[C::MANY ? C::BUF : 16], b3[C::MANY ? C::BUF : 16]
 
 // The row's result, O / l rounded to bf16; a row without keys is 0.
 template <class C>
@@ -417,7 +597,7 @@ __device__ __forceinline__ void store_row(const State<C>& st, uint16_t* out, int
 #pragma unroll
         for (int a = 0; a < 4; ++a) {
             const int ch = 32 * d + 8 * a + 4 * g2;
-            if (ch < D) {
+            if (ch < D && holds_block<C>(d)) {
                 uint2 w;
                 w.x = f32x2_to_bf16x2(st.acc[d][4 * a] * inv, st.acc[d][4 * a + 1] * inv);
                 w.y = f32x2_to_bf16x2(st.acc[d][4 * a + 2] * inv, st.acc[d][4 * a + 3] * inv);
@@ -445,9 +625,9 @@ __device__ __forceinline__ void head_tile(int id, int Hkv, int tiles, int& hk, i
 }
 
 template <class C>
-__global__ __launch_bounds__(kAThreads) void attn_prompt_kernel(PromptArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[C::STAGE];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[C::STAGE];
+__global__ __launch_bounds__(kAThreads) __attribute__((amdgpu_waves_per_eu(C::WAVES, C::WAVES)))
+void attn_prompt_kernel(PromptArgs a) {
+    ATTN_BUFFERS;
     const int lane = threadIdx.x & 63;
     int hk, tile;
     head_tile(blockIdx.x, a.Hkv, a.tiles, hk, tile);
@@ -493,9 +673,8 @@ __global__ __launch_bounds__(kAThreads) void attn_prompt_kernel(PromptArgs a) {
     nk = __builtin_amdgcn_readfirstlane(nk);
     const int rt = tile - __builtin_amdgcn_readfirstlane(first);
 
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t rows = static_cast<int64_t>(nq) * G;
-    const int64_t r = static_cast<int64_t>(rt) * C::TM + (wave % C::QW) * 32 + (lane & 31);
+    const int64_t r = static_cast<int64_t>(rt) * C::TM + wave_row<C>() + (lane & 31);
     const bool live = r < rows;
     const int i = static_cast<int>(r / G), g = static_cast<int>(r - static_cast<int64_t>(i) * G);
     const uint16_t* q = live ? a.q + static_cast<int64_t>(q0 + i) * a.q_stride + static_cast<int64_t>(hk * G + g) * a.D : nullptr;
@@ -509,33 +688,42 @@ __global__ __launch_bounds__(kAThreads) void attn_prompt_kernel(PromptArgs a) {
     PackedKeys keys;
     keys.k = a.k + static_cast<int64_t>(k0) * a.k_stride + static_cast<int64_t>(hk) * a.D;
     keys.v = a.v + static_cast<int64_t>(k0) * a.v_stride + static_cast<int64_t>(hk) * a.D;
-    keys.k_stride = a.k_stride;
-    keys.v_stride = a.v_stride;
+    keys.k_stride = static_cast<int>(a.k_stride) * 2;
+    keys.v_stride = static_cast<int>(a.v_stride) * 2;
     keys.n = nk;
     State<C> st;
-    attend<C>(keys, q, klim, 0, kend, a.D, a.c, buf0, buf1, st);
-    join_key_waves<C>(buf0, buf1, a.c, st);
-    if (wave / C::QW == 0 && live)
+    attend<C>(keys, q, klim, 0, kend, a.D, a.c, b0, b1, b2, b3, st);
+    if (live)
         store_row<C>(st, a.out + static_cast<int64_t>(q0 + i) * a.out_stride + static_cast<int64_t>(hk * G + g) * a.D, a.D);
 }
 
 // ----------------------------------------------------------- shared prefix
 
-// One work item: a row tile of one key/value head against one split of the
-// shared prefix (rows of the whole batch) or of one sequence's suffix.  With
-// one sequence both are one range of keys.  More than one part per row: the
-// parts' unnormalised O, maximum and sum go to the workspace.
+// One workgroup, one work item: a row tile of one key/value head against one
+// split of the shared prefix (rows of the whole batch) or of one sequence's
+// suffix.  With one sequence both are one range of keys.  More than one part
+// per row: the parts' unnormalised O, maximum and sum go to the workspace.
 template <class C>
-__device__ __forceinline__ void shared_item(const SharedArgs& a, int hk, int tile, int split, int splits, int part,
-                                            int b, bool prefix, uint8_t* buf0, uint8_t* buf1) {
+__global__ __launch_bounds__(kAThreads) __attribute__((amdgpu_waves_per_eu(C::WAVES, C::WAVES)))
+void attn_shared_kernel(SharedArgs a) {
+    ATTN_BUFFERS;
+    int id = blockIdx.x;
+    const bool prefix = id < a.prefix_items;
+    if (!prefix) id -= a.prefix_items;
+    // (head, split) fastest: the row tiles that read the same keys are Hkv *
+    // splits apart, on one XCD when that is a multiple of 8
+    const int splits = prefix ? a.prefix_splits : a.suffix_splits;
+    const int pair = id % (a.Hkv * splits), rest = id / (a.Hkv * splits);
+    const int hk = pair / splits, split = pair % splits;
+    const int tile = prefix ? rest : rest % a.suffix_tiles, b = prefix ? 0 : rest / a.suffix_tiles;
+
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int G = a.Hq / a.Hkv;
     const int np = a.prefix_pages ? min(max(a.prefix_len[0], 0), a.prefix_cap) : 0;
     int ns = 0;
     if (!prefix && a.block_table) ns = min(max(a.seq_lens[b], 0), a.suffix_cap);
     PagedKeys keys;
-    keys.stride = static_cast<int64_t>(a.Hkv) * a.D;
+    keys.stride = static_cast<uint32_t>(a.Hkv * a.D * 2);
     keys.k = a.k_cache + static_cast<int64_t>(hk) * a.D;
     keys.v = a.v_cache + static_cast<int64_t>(hk) * a.D;
     keys.prefix = a.prefix_pages;
@@ -545,29 +733,27 @@ __device__ __forceinline__ void shared_item(const SharedArgs& a, int hk, int til
     keys.page_log2 = a.page_log2;
     keys.num_pages = a.num_pages;
 
-    // rows: of the whole batch for the prefix, else of sequence b
     const int rows = (prefix ? a.B : 1) * a.L * G;
-    const int r = tile * C::TM + (wave % C::QW) * 32 + (lane & 31);
+    const int r = tile * C::TM + wave_row<C>() + (lane & 31);
     const bool live = r < rows;
     const int tok = r / G, g = r - tok * G;
-    const int64_t token = static_cast<int64_t>(prefix ? 0 : b) * a.L + tok;       // of B * L
+    const int64_t token = static_cast<int64_t>(b) * a.L + tok;    // of B * L
     const int head = hk * G + g;
     const uint16_t* q = live ? a.q + token * a.q_stride + static_cast<int64_t>(head) * a.D : nullptr;
     int klim = keys.n;
     if (a.causal && !prefix) klim = keys.n_prefix + min(max(tok + 1 + ns - a.L, 0), ns);
-    const int stages = (keys.n + C::ST - 1) / C::ST, per = (stages + splits - 1) / splits;
+    const int steps = (keys.n + C::ST - 1) / C::ST, per = (steps + splits - 1) / splits;
     const int k0 = min(split * per * C::ST, keys.n), k1 = min((split + 1) * per * C::ST, keys.n);
     State<C> st;
-    attend<C>(keys, q, klim, k0, k1, a.D, a.c, buf0, buf1, st);
-    join_key_waves<C>(buf0, buf1, a.c, st);
-    if (wave / C::QW != 0 || !live) return;
+    attend<C>(keys, q, klim, k0, k1, a.D, a.c, b0, b1, b2, b3, st);
+    if (!live) return;
     if (a.parts == 1) {
         store_row<C>(st, a.out + token * a.out_stride + static_cast<int64_t>(head) * a.D, a.D);
         return;
     }
-    const int64_t at = (token * a.Hq + head) * a.parts + part;
+    const int64_t at = (token * a.Hq + head) * a.parts + (prefix ? 0 : a.prefix_splits) + split;
     const int g2 = lane >> 5;
-    if (g2 == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(st.m, st.l);
+    if (g2 == 0 && holds_block<C>(0)) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(st.m, st.l);
     if (st.m == -__builtin_inff()) return;
     float* o = a.part_o + at * a.D;
 #pragma unroll
@@ -575,32 +761,10 @@ __device__ __forceinline__ void shared_item(const SharedArgs& a, int hk, int til
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const int ch = 32 * d + 8 * x + 4 * g2;
-            if (ch < a.D)
+            if (ch < a.D && holds_block<C>(d))
                 *reinterpret_cast<float4*>(o + ch) =
                     make_float4(st.acc[d][4 * x], st.acc[d][4 * x + 1], st.acc[d][4 * x + 2], st.acc[d][4 * x + 3]);
         }
-}
-
-template <class CP, class CS>
-__global__ __launch_bounds__(kAThreads) void attn_shared_kernel(SharedArgs a) {
-    constexpr int STAGE = CP::STAGE > CS::STAGE ? CP::STAGE : CS::STAGE;
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[STAGE];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[STAGE];
-    int id = blockIdx.x;
-    // (head, split) fastest: the row tiles that read the same keys are Hkv *
-    // splits apart, on one XCD when that is a multiple of 8
-    if (id < a.prefix_items) {
-        const int pair = id % (a.Hkv * a.prefix_splits);
-        shared_item<CP>(a, pair / a.prefix_splits, id / (a.Hkv * a.prefix_splits), pair % a.prefix_splits,
-                        a.prefix_splits, pair % a.prefix_splits, 0, true, buf0, buf1);
-    } else {
-        id -= a.prefix_items;
-        const int pair = id % (a.Hkv * a.suffix_splits);
-        const int rest = id / (a.Hkv * a.suffix_splits);
-        const int split = pair % a.suffix_splits;
-        shared_item<CS>(a, pair / a.suffix_splits, rest % a.suffix_tiles, split, a.suffix_splits,
-                        (a.prefix_items ? a.prefix_splits : 0) + split, rest / a.suffix_tiles, false, buf0, buf1);
-    }
 }
 
 // Joins a row's parts: one wave per row, four channels per lane.
@@ -622,7 +786,7 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
             l += ml[2 * p + 1];                                   // 0, or NaN where every score was NaN
             continue;
         }
-        const float w = mp == m ? 1.0f : __builtin_amdgcn_exp2f((mp - m) * a.c);
+        const float w = mp == m ? 1.0f : __builtin_amdgcn_exp2f(mp - m);
         l += ml[2 * p + 1] * w;
         if (ch < a.D) {
             const float4 x = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(p) * a.D);
@@ -638,33 +802,17 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
     *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (row - token * a.Hq) * a.D + ch) = w;
 }
 
-// Tiles by padded head size: many rows (128 x 64 keys a stage) and few rows
-// (32 x 128, or 64 x 64 where 128 keys of 256 channels would not fit LDS twice).
-template <int DP> using Many = ACfg<DP, 4, 1>;
-template <int DP> struct FewOf { using type = ACfg<DP, 1, 4>; };
-template <> struct FewOf<256> { using type = ACfg<256, 2, 2>; };
-template <int DP> using Few = typename FewOf<DP>::type;
-
-int pad_d(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
-int few_rows(int D) { return pad_d(D) == 256 ? 64 : 32; }
-int stage_keys(int D, bool many) { return many || pad_d(D) == 256 ? 64 : 128; }
+template <int DP> using Many = ACfg<DP, true>;
+template <int DP> using Few = ACfg<DP, false>;
 
 constexpr int kComputeUnits = 256;
 
-template <int DP>
-hipError_t prompt_dispatch(const PromptArgs& a, bool many, int grid, hipStream_t s) {
-    if (many) attn_prompt_kernel<Many<DP>><<<grid, kAThreads, 0, s>>>(a);
-    else attn_prompt_kernel<Few<DP>><<<grid, kAThreads, 0, s>>>(a);
-    return hipGetLastError();
-}
-
-template <int DP>
-hipError_t shared_dispatch(const SharedArgs& a, bool pm, bool sm, int grid, hipStream_t s) {
-    if (pm && sm) attn_shared_kernel<Many<DP>, Many<DP>><<<grid, kAThreads, 0, s>>>(a);
-    else if (pm) attn_shared_kernel<Many<DP>, Few<DP>><<<grid, kAThreads, 0, s>>>(a);
-    else if (sm) attn_shared_kernel<Few<DP>, Many<DP>><<<grid, kAThreads, 0, s>>>(a);
-    else attn_shared_kernel<Few<DP>, Few<DP>><<<grid, kAThreads, 0, s>>>(a);
-    return hipGetLastError();
+// D channels run in the kernels of the next padded size.
+template <class F>
+hipError_t by_size(int D, bool many, F&& launch) {
+    if (D <= 64) return many ? launch(Many<64>{}) : launch(Few<64>{});
+    if (D <= 128) return many ? launch(Many<128>{}) : launch(Few<128>{});
+    return many ? launch(Many<256>{}) : launch(Few<256>{});
 }
 
 }  // namespace
@@ -673,16 +821,13 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     // wide tiles once they fill the compute units, else more and narrower ones
     const int64_t rows = static_cast<int64_t>(a.total_q) * (a.Hq / a.Hkv);
     const bool many = a.Hkv * ((rows + 127) / 128) >= kComputeUnits;
-    const int tm = many ? 128 : few_rows(a.D);
+    const int tm = many ? 128 : 32;
     // every sequence ends in at most one partial tile
     a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
-    if (a.tiles == 0) return hipSuccess;
-    const int grid = a.tiles * a.Hkv;
-    switch (pad_d(a.D)) {
-        case 64: return prompt_dispatch<64>(a, many, grid, s);
-        case 128: return prompt_dispatch<128>(a, many, grid, s);
-        default: return prompt_dispatch<256>(a, many, grid, s);
-    }
+    return by_size(a.D, many, [&](auto cfg) {
+        attn_prompt_kernel<decltype(cfg)><<<a.tiles * a.Hkv, kAThreads, 0, s>>>(a);
+        return hipGetLastError();
+    });
 }
 
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
@@ -693,21 +838,20 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     const int64_t rows_p = B * L * G, rows_s = L * G;
     p.prefix_many = rows_p > 64;
     p.suffix_many = rows_s > 64;
-    const int64_t tm_p = p.prefix_many ? 128 : few_rows(static_cast<int>(D));
-    const int64_t tm_s = p.suffix_many ? 128 : few_rows(static_cast<int>(D));
-    const int64_t st_p = stage_keys(static_cast<int>(D), p.prefix_many), st_s = stage_keys(static_cast<int>(D), p.suffix_many);
+    const int64_t tm_p = p.prefix_many ? 128 : 32, tm_s = p.suffix_many ? 128 : 32;
+    const int64_t st_p = p.prefix_many ? 64 : 128, st_s = p.suffix_many ? 64 : 128;
     const int64_t keys_s = suffix_cap + (p.merged ? prefix_cap : 0);
-    const int64_t stages_p = p.merged ? 0 : (prefix_cap + st_p - 1) / st_p;
-    const int64_t stages_s = keys_s > 0 ? (keys_s + st_s - 1) / st_s : 0;
+    const int64_t steps_p = p.merged ? 0 : (prefix_cap + st_p - 1) / st_p;
+    const int64_t steps_s = (keys_s + st_s - 1) / st_s;
     const int64_t tiles_p = p.merged ? 0 : (rows_p + tm_p - 1) / tm_p;
     p.suffix_tiles = (rows_s + tm_s - 1) / tm_s;
-    // stages per work item such that the items of both kinds fill the compute
+    // steps per work item such that the items of both kinds fill the compute
     // units once
-    const int64_t all = Hkv * (tiles_p * stages_p + B * p.suffix_tiles * stages_s);
+    const int64_t all = Hkv * (tiles_p * steps_p + B * p.suffix_tiles * steps_s);
     int64_t per = (all + kComputeUnits - 1) / kComputeUnits;
     if (per < 1) per = 1;
-    p.prefix_splits = stages_p ? (stages_p + per - 1) / per : 0;
-    p.suffix_splits = stages_s ? (stages_s + per - 1) / per : 0;
+    p.prefix_splits = (steps_p + per - 1) / per;
+    p.suffix_splits = (steps_s + per - 1) / per;
     p.prefix_items = Hkv * tiles_p * p.prefix_splits;
     p.suffix_items = Hkv * B * p.suffix_tiles * p.suffix_splits;
     p.parts = p.prefix_splits + p.suffix_splits;
@@ -719,7 +863,6 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
 
 hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipStream_t s) {
     a.merged = p.merged;
-    a.prefix_items = static_cast<int>(p.prefix_items);
     a.prefix_splits = static_cast<int>(p.prefix_splits);
     a.suffix_splits = static_cast<int>(p.suffix_splits);
     a.suffix_tiles = static_cast<int>(p.suffix_tiles);
@@ -727,12 +870,21 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
     a.part_ml = reinterpret_cast<float*>(w);
     a.part_o = reinterpret_cast<float*>(w + p.ml_bytes);
-    const int grid = static_cast<int>(p.prefix_items + p.suffix_items);
+    auto run = [&](bool many, int64_t prefix_items, int64_t suffix_items) {
+        a.prefix_items = static_cast<int>(prefix_items);
+        const int grid = static_cast<int>(prefix_items + suffix_items);
+        if (grid == 0) return hipSuccess;
+        return by_size(a.D, many, [&](auto cfg) {
+            attn_shared_kernel<decltype(cfg)><<<grid, kAThreads, 0, s>>>(a);
+            return hipGetLastError();
+        });
+    };
     hipError_t e;
-    switch (pad_d(a.D)) {
-        case 64: e = shared_dispatch<64>(a, p.prefix_many, p.suffix_many, grid, s); break;
-        case 128: e = shared_dispatch<128>(a, p.prefix_many, p.suffix_many, grid, s); break;
-        default: e = shared_dispatch<256>(a, p.prefix_many, p.suffix_many, grid, s); break;
+    if (p.prefix_many == p.suffix_many) {
+        e = run(p.prefix_many, p.prefix_items, p.suffix_items);
+    } else {
+        e = run(p.prefix_many, p.prefix_items, 0);
+        if (e == hipSuccess) e = run(p.suffix_many, 0, p.suffix_items);
     }
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.L * a.Hq;

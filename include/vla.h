@@ -200,8 +200,8 @@ int vla_gate_residual_ada_norm(const uint16_t *residual, const uint16_t *out, co
  * query head h reads key/value head h / (Hq / Hkv).  A head has D channels, D
  * a multiple of 8, at most 256 (VLA_ESHAPE).  A token's row holds its heads
  * one after another; rows are `*_stride` elements apart (a multiple of 8, at
- * least heads * D, else VLA_ESHAPE), so q, k and v may be the column blocks
- * of one QKV GEMM output.
+ * least heads * D, at most 2^24, else VLA_ESHAPE), so q, k and v may be the
+ * column blocks of one QKV GEMM output.
  *
  * The cache: k_cache and v_cache, device bf16, num_pages pages of page_size
  * rows of Hkv * D elements each; row r of page p is slot p * page_size + r.
