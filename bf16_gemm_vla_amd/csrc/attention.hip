@@ -71,14 +71,8 @@ struct ACfg {
     // LDS buffers: MANY has K and V of two stages of 64 rows, FEW K and V of
     // one sub-tile of 32 rows per wave, each an object of its own: the
     // compiler orders LDS reads after the loads that write the same object
-    static constexpr int BUFS = MANY ? 4 : 2;
     static constexpr int BUF = (MANY ? 64 : 128) * RB;
-    // FEW: the waves' results join through the same buffers, maxima and sums
-    // first, then 4 KiB for each (channel block, wave that gives it away)
-    static constexpr int ML = 4 * 2 * 64 * 4;
-    static constexpr int BLOCKS0 = (BUF - ML) / 4096;        // blocks in the first buffer
     static_assert(R % RPI == 0, "whole load instructions");
-    static_assert(MANY || BLOCKS0 + BUF / 4096 >= 3 * ND, "the waves' results fit the two buffers");
 };
 
 // Position of a row's 16-byte chunks in LDS: chunk ^ swizzle.
@@ -136,7 +130,7 @@ template <class C>
 __device__ __forceinline__ bool has_nonfinite(const uint8_t* v) {
     v += (threadIdx.x & 63) * 16;
     bool bad = false;
-#pragma unroll 1
+#pragma unroll
     for (int i = 0; i < 32 * C::RB / 1024; ++i) {
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + i * 1024);
 #pragma unroll
@@ -151,7 +145,6 @@ template <class C, class Keys>
 struct Walk {
     static constexpr bool PAGED = std::is_same<Keys, PagedKeys>::value;
     const Keys& keys;
-    const uint16_t* q;         // the lane's row, or nullptr
     int klim;                  // the lane's row sees keys below this
     int kfull, kmax;           // every row sees keys below kfull, none one at or past kmax
     int D;
@@ -162,21 +155,14 @@ struct Walk {
     bf16x8_t qf[C::NK];
     State<C>& st;
 
-    __device__ __forceinline__ Walk(const Keys& keys_, const uint16_t* q_, int klim_, int D_, float c_, State<C>& st_)
-        : keys(keys_), q(q_), klim(klim_), D(D_), c(c_), st(st_) {
+    // live: the lane has a row
+    __device__ __forceinline__ Walk(const Keys& keys_, int klim_, int D_, float c_, State<C>& st_, bool live)
+        : keys(keys_), klim(klim_), D(D_), c(c_), st(st_) {
         const int lane = threadIdx.x & 63;
         l32 = lane & 31;
         g2 = lane >> 5;
-        // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
-#pragma unroll
-        for (int kk = 0; kk < C::NK; ++kk) {
-            const int d = 16 * kk + 8 * g2;
-            u32x4_t w = {0, 0, 0, 0};
-            if (q && d < D) w = *reinterpret_cast<const u32x4_t*>(q + d);
-            qf[kk] = as_bf16x8(w);
-        }
-        kfull = q ? klim : INT_MAX;
-        kmax = q ? klim : 0;
+        kfull = live ? klim : INT_MAX;
+        kmax = live ? klim : 0;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) {
             kfull = min(kfull, __shfl_xor(kfull, o, 64));
@@ -198,51 +184,79 @@ struct Walk {
         lrow = lane / C::CH;
         lpos = lane % C::CH;
     }
-
-    // ---- loads of R rows of K or V into LDS at dst; row0: their number in
-    //      the buffer modulo 32 (for the swizzle)
-    template <bool V>
-    __device__ __forceinline__ void load_packed(uint8_t* dst, int row0, int key0, int k1) const {
-        // a buffer that ends with the last key: rows past it load zeros
-        const int stride = V ? keys.v_stride : keys.k_stride;
-        const int left = min(k1 - key0, C::R);
-        const int bytes = left > 0 ? (left - 1) * stride + D * 2 : 0;
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(V ? keys.v : keys.k) + static_cast<int64_t>(key0) * stride), 0,
-            bytes, kBufferWord3);
+    // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
+    __device__ __forceinline__ void load_q(const uint16_t* q) {
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) {
-            const int row = row0 + i * C::RPI + lrow;
-            const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
-            const uint32_t off = ch * 8 < D ? static_cast<uint32_t>(lrow * stride + ch * 16) : 0x80000000u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, off,
-                                                     i * C::RPI * stride, 0, 0);
+        for (int kk = 0; kk < C::NK; ++kk) {
+            const int d = 16 * kk + 8 * g2;
+            u32x4_t w = {0, 0, 0, 0};
+            if (q && d < D) w = *reinterpret_cast<const u32x4_t*>(q + d);
+            qf[kk] = as_bf16x8(w);
         }
     }
+
+    // ---- loads of R rows of K or V into LDS, one instruction (i < C::NI) at a
+    //      time.  row0: the rows' place in the buffer modulo 32 (for the
+    //      swizzle); Source holds what is common to the instructions.
+    struct Source {
+        __amdgpu_buffer_rsrc_t rs;   // packed: a buffer that ends with the last key, rows past it load zeros
+        uint64_t base;               // paged
+        int stride, slot, from;      // slot: of the window's key `lane`; from: the window row of instruction 0
+    };
     template <bool V>
-    __device__ __forceinline__ void load_paged(uint8_t* dst, int row0, int slot, int from) const {
-        const uint16_t* base = V ? keys.v : keys.k;
-#pragma unroll
-        for (int i = 0; i < C::NI; ++i) {
-            const int row = row0 + i * C::RPI + lrow;
-            const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
-            const int sl = __shfl(slot, from + i * C::RPI + lrow, 64);
-            const uint64_t at = reinterpret_cast<uint64_t>(base) + static_cast<uint64_t>(static_cast<uint32_t>(sl)) * keys.stride + ch * 16;
+    __device__ __forceinline__ Source packed_rows(int key0, int k1) const {
+        Source s;
+        s.stride = V ? keys.v_stride : keys.k_stride;
+        const int left = min(k1 - key0, C::R);
+        s.rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(V ? keys.v : keys.k) + static_cast<int64_t>(key0) * s.stride), 0,
+            left > 0 ? (left - 1) * s.stride + D * 2 : 0, kBufferWord3);
+        return s;
+    }
+    template <bool V>
+    __device__ __forceinline__ Source paged_rows(int slot, int from) const {
+        Source s;
+        s.base = reinterpret_cast<uint64_t>(V ? keys.v : keys.k);
+        s.slot = slot;
+        s.from = from;
+        return s;
+    }
+    template <bool V>
+    __device__ __forceinline__ void load(const Source& s, uint8_t* dst, int row0, int i) const {
+        const int row = row0 + i * C::RPI + lrow;
+        const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
+        __attribute__((address_space(3))) void* const to = (__attribute__((address_space(3))) void*)(dst + i * 1024);
+        if constexpr (PAGED) {
+            const int sl = __shfl(s.slot, s.from + i * C::RPI + lrow, 64);
+            const uint64_t at = s.base + static_cast<uint64_t>(static_cast<uint32_t>(sl)) * keys.stride + ch * 16;
             const uint64_t src = (sl >= 0 && ch * 8 < D) ? at : reinterpret_cast<uint64_t>(kZeroChunk);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, to, 16, 0, 0);
+        } else {
+            const uint32_t off = ch * 8 < D ? static_cast<uint32_t>(lrow * s.stride + ch * 16) : 0x80000000u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rs, to, 16, off, i * C::RPI * s.stride, 0, 0);
         }
     }
 
     // ---- one 32-key sub-tile in LDS
-    __device__ __forceinline__ f32x16_t scores(const uint8_t* kt) const {
+    //      N loads, load_one(0 .. N-1), go out between the matrix instructions:
+    //      issued in a block they would hold the wave until the load path has
+    //      taken them all
+    template <int N, class F>
+    __device__ __forceinline__ f32x16_t scores(const uint8_t* kt, F&& load_one) const {
         u32x4_t kf[C::NK];
 #pragma unroll
         for (int kk = 0; kk < C::NK; ++kk) kf[kk] = *reinterpret_cast<const u32x4_t*>(kt + (kaddr ^ (kk << 5)));
         f32x16_t sc = f32x16_t{};
 #pragma unroll
-        for (int kk = 0; kk < C::NK; ++kk)
+        for (int kk = 0; kk < C::NK; ++kk) {
             sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[kk]), qf[kk], sc, 0, 0, 0);
+            if (kk < N) load_one(kk);
+        }
+#pragma unroll
+        for (int kk = 0; kk < C::NK; ++kk) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                    // MFMA
+            if (kk < N) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);        // VMEM
+        }
         return sc;
     }
     // Scores in log2 units; those a row does not see become -inf.
@@ -320,13 +334,13 @@ struct Walk {
     // sub-tile that ends 32 b to 32 b + 31 keys past the last key that every
     // row sees; a tile of at most 128 rows ends at most 128 + 31 keys past it.
     __device__ __forceinline__ bool put_off(const uint8_t* vt, int key0) const {
-        if (key0 + 32 <= kfull || !has_nonfinite<C>(vt)) return false;
+        if (key0 + 32 <= kfull || kfull == kmax || !has_nonfinite<C>(vt)) return false;
         st.late |= 1u << ((key0 + 32 - kfull) >> 5);
         return true;
     }
     // key0_of: first key of this wave's sub-tile that holds a key, or -1 (another wave's)
     template <class F>
-    __device__ __forceinline__ void add_late(int k1, F&& key0_of) const {
+    __device__ __forceinline__ void add_late(const uint16_t* q, int k1, F&& key0_of) const {
         if (!st.late) return;
         for (int key = max(kfull - 31, 0); key < min(kmax, k1); ++key) {
             const int key0 = key0_of(key);
@@ -349,9 +363,14 @@ struct Walk {
 #pragma unroll
             for (int d = 0; d < C::ND; ++d)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int ch = 32 * d + 8 * (i / 4) + 4 * g2 + (i % 4);
-                    if (ch < D) st.acc[d][i] += p * bf16_to_f32(vr[ch]);
+                for (int x = 0; x < 4; ++x) {
+                    const int ch = 32 * d + 8 * x + 4 * g2;
+                    uint2 v = make_uint2(0, 0);
+                    if (ch < D) v = *reinterpret_cast<const uint2*>(vr + ch);
+                    st.acc[d][4 * x] += p * __uint_as_float(v.x << 16);
+                    st.acc[d][4 * x + 1] += p * __uint_as_float(v.x & 0xFFFF0000u);
+                    st.acc[d][4 * x + 2] += p * __uint_as_float(v.y << 16);
+                    st.acc[d][4 * x + 3] += p * __uint_as_float(v.y & 0xFFFF0000u);
                 }
         }
     }
@@ -378,39 +397,51 @@ __device__ __forceinline__ void wait_here() {
 template <class C, class Keys>
 __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                             uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
-    Walk<C, Keys> w(keys, q, klim, D, c, st);
+    using W = Walk<C, Keys>;
+    using Source = typename W::Source;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n_stages = (k1 - k0 + 63) / 64;
-    if (n_stages <= 0) return;
     const int row0 = wave * C::R;                                 // rows of a stage this wave loads
     // the lane's key of a stage: its slot, for the loads and the masks
     auto entry = [&](int s) __attribute__((always_inline)) -> int {
-        if constexpr (Walk<C, Keys>::PAGED) {
+        if constexpr (W::PAGED) {
             const int key = k0 + s * 64 + (threadIdx.x & 63);
             return key < k1 ? keys.slot(key) : -1;
         } else {
             return 0;
         }
     };
-    auto issue = [&](uint8_t* kb, uint8_t* vb, int s, int slot) __attribute__((always_inline)) {
-        if constexpr (Walk<C, Keys>::PAGED) {
-            w.template load_paged<false>(kb + row0 * C::RB, row0, slot, row0);
-            w.template load_paged<true>(vb + row0 * C::RB, row0, slot, row0);
-        } else {
-            w.template load_packed<false>(kb + row0 * C::RB, row0, k0 + s * 64 + row0, k1);
-            w.template load_packed<true>(vb + row0 * C::RB, row0, k0 + s * 64 + row0, k1);
-        }
+    int slot = n_stages > 0 ? entry(0) : 0;
+    W w(keys, klim, D, c, st, q != nullptr);
+    auto source = [&](auto V, int s) __attribute__((always_inline)) -> Source {
+        constexpr bool v = decltype(V)::value;
+        if constexpr (W::PAGED) return w.template paged_rows<v>(slot, row0);
+        else return w.template packed_rows<v>(k0 + s * 64 + row0, k1);
     };
-    auto valid = [&](int slot) __attribute__((always_inline)) -> uint64_t {
-        if constexpr (Walk<C, Keys>::PAGED) return __ballot(slot >= 0);
+    auto valid = [&](int sl) __attribute__((always_inline)) -> uint64_t {
+        if constexpr (W::PAGED) return __ballot(sl >= 0);
         else return ~uint64_t(0);
     };
     // stage s lives in buffers s % 2; its loads are issued while stage s-1 is
     // computed, its table entries are read one stage earlier still
-    int slot = entry(0);
-    issue(kb0, vb0, 0, slot);
     uint64_t vcur = valid(slot);
-    slot = n_stages > 1 ? entry(1) : 0;
+    if (n_stages > 0) {
+        const Source k = source(std::false_type{}, 0), v = source(std::true_type{}, 0);
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb0 + row0 * C::RB, row0, i);
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) w.template load<true>(v, vb0 + row0 * C::RB, row0, i);
+    }
+    w.load_q(q);
+    if (n_stages <= 0) return;
+    slot = n_stages > 1 ? entry(1) : -1;
+    auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& load_one) __attribute__((always_inline)) {
+        f32x16_t sc = w.template scores<C::NI>(kt, load_one);
+        w.scale_and_mask(sc, key0, vm);
+        uint32_t pw[8];
+        w.weights(sc, pw);
+        if (!w.put_off(vt, key0)) w.add(vt, pw);
+    };
     auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s) __attribute__((always_inline)) {
         // this wave's loads of stage s have landed and its reads of stage s-1
         // are done; the barrier says so for every wave
@@ -418,41 +449,36 @@ __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q,
         __builtin_amdgcn_s_barrier();
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         __builtin_amdgcn_sched_barrier(0);
-        uint64_t vnext = 0;
-        if (s + 1 < n_stages) {
-            issue(kn, vn, s + 1, slot);
-            vnext = valid(slot);
-            if (s + 2 < n_stages) slot = entry(s + 2);
-        }
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-            const int key0 = k0 + s * 64 + sub * 32;
-            if (key0 >= w.kmax) break;
-            f32x16_t sc = w.scores(kc + sub * 32 * C::RB);
-            w.scale_and_mask(sc, key0, static_cast<uint32_t>(vcur >> (32 * sub)));
-            uint32_t pw[8];
-            w.weights(sc, pw);
-            if (!w.put_off(vc + sub * 32 * C::RB, key0)) w.add(vc + sub * 32 * C::RB, pw);
-        }
+        const int key0 = k0 + s * 64;
+        // the next stage's K goes out among this one's first scores, its V
+        // among the second ones (past the last stage: zeros)
+        const Source k = source(std::false_type{}, s + 1), v = source(std::true_type{}, s + 1);
+        const uint64_t vnext = valid(slot);
+        sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur),
+                 [&](int i) __attribute__((always_inline)) { w.template load<false>(k, kn + row0 * C::RB, row0, i); });
+        sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32),
+                 [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vn + row0 * C::RB, row0, i); });
         vcur = vnext;
+        slot = s + 2 < n_stages ? entry(s + 2) : -1;
     };
     for (int s = 0; s < n_stages; s += 2) {
         step(kb0, vb0, kb1, vb1, s);
         if (s + 1 < n_stages) step(kb1, vb1, kb0, vb0, s + 1);
     }
     st.l = half_sum(st.l);
-    w.add_late(k1, [&](int key) { return k0 + (key - k0) / 32 * 32; });
+    w.add_late(q, k1, [&](int key) { return k0 + (key - k0) / 32 * 32; });
 }
 
 // Keys k0 .. k1-1 for 32 rows that the four waves share: wave w takes
 // sub-tiles w, w + 4, ...  Each wave's K and V have one place in LDS: K of
-// the next sub-tile is loaded as soon as this one's scores are formed, V as
-// soon as it has been added, so each load has the other half of a sub-tile's
-// work to arrive in and 16 (D <= 64: 8, D > 128: 32) KiB per wave are in flight.
+// the next sub-tile goes out while this one's weights are formed, its V among
+// its scores, so 16 (D <= 64: 8, D > 128: 32) KiB per wave are in flight.
 template <class C, class Keys>
 __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                            uint8_t* kb, uint8_t* vb, State<C>& st) {
-    constexpr bool PAGED = Walk<C, Keys>::PAGED;
+    using W = Walk<C, Keys>;
+    using Source = typename W::Source;
+    constexpr bool PAGED = W::PAGED;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     kb += wave * 32 * C::RB;
     vb += wave * 32 * C::RB;
@@ -467,103 +493,145 @@ __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, 
         }
     };
     int slot = n > 0 ? entry(0) : 0;
-    Walk<C, Keys> w(keys, q, klim, D, c, st);
+    W w(keys, klim, D, c, st, q != nullptr);
+    auto source = [&](auto V, int t, int sl) __attribute__((always_inline)) -> Source {
+        constexpr bool v = decltype(V)::value;
+        if constexpr (PAGED) return w.template paged_rows<v>(sl, 0);
+        else return w.template packed_rows<v>(first + t * 128, k1);
+    };
+    if (n > 0) {
+        const Source k = source(std::false_type{}, 0, slot);
+#pragma unroll
+        for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb, 0, i);
+    }
+    w.load_q(q);
     if (n <= 0) return;
-    auto load_k = [&](int t, int sl) __attribute__((always_inline)) {
-        if constexpr (PAGED) w.template load_paged<false>(kb, 0, sl, 0);
-        else w.template load_packed<false>(kb, 0, first + t * 128, k1);
-    };
-    auto load_v = [&](int t, int sl) __attribute__((always_inline)) {
-        if constexpr (PAGED) w.template load_paged<true>(vb, 0, sl, 0);
-        else w.template load_packed<true>(vb, 0, first + t * 128, k1);
-    };
-    load_k(0, slot);
-    load_v(0, slot);
     int next = n > 1 ? entry(1) : 0;
-    for (int t = 0; t < n; ++t) {
+    auto step = [&](auto MORE, int t) __attribute__((always_inline)) {
         const int key0 = first + t * 128;
-        const bool more = t + 1 < n;
-        // order of the wave's loads: K(t), entry(t+1), V(t), K(t+1), ...; here
-        // V(t) and an entry are younger than K(t)
-        wait_here<wait_vm(C::NI)>();
-        f32x16_t sc = w.scores(kb);
+        wait_here<wait_vm(0)>();                                  // K(t), and the entry of t + 1
+        const Source v = source(std::true_type{}, t, slot);
+        f32x16_t sc = w.template scores<C::NI>(kb, [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vb, 0, i); });
         const uint32_t vm = PAGED ? static_cast<uint32_t>(__ballot(slot >= 0)) : 0xFFFFFFFFu;
         wait_here<kWaitLds>();                                    // K(t) has been read
-        if (more) {
+        if constexpr (decltype(MORE)::value) {
             slot = next;
-            load_k(t + 1, slot);
-            if (t + 2 < n) next = entry(t + 2);
+            const Source k = source(std::false_type{}, t + 1, slot);
+#pragma unroll
+            for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb, 0, i);
+            next = t + 2 < n ? entry(t + 2) : 0;
         }
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
         w.weights(sc, pw);
-        if (more) wait_here<wait_vm(C::NI)>();
+        if constexpr (decltype(MORE)::value) wait_here<wait_vm(C::NI)>();   // V(t); K(t+1) may be on its way
         else wait_here<wait_vm(0)>();
         if (!w.put_off(vb, key0)) w.add(vb, pw);
         wait_here<kWaitLds>();                                    // V(t) has been read
-        if (more) load_v(t + 1, slot);
-    }
+    };
+    for (int t = 0; t + 1 < n; ++t) step(std::true_type{}, t);
+    step(std::false_type{}, n - 1);
     st.l = half_sum(st.l);
-    w.add_late(k1, [&](int key) {
+    w.add_late(q, k1, [&](int key) {
         const int t = key - k0;
         return (t >> 5 & 3) == wave ? k0 + (t & ~31) : -1;
     });
 }
 
-// Joins the four waves' results for the same rows: wave w is left with
-// channel blocks d = w, w + 4 of the whole (in acc[d]).
-template <class C>
-__device__ __forceinline__ void join_waves(uint8_t* buf0, uint8_t* buf1, State<C>& st) {
-    const int lane = threadIdx.x & 63;
+// ------------------------------------------------------------- results
+
+// LDS of one workgroup.
+#define ATTN_LDS                                                                                 \
+    __shared__ __attribute__((aligned(16))) uint8_t b0[C::BUF], b1[C::BUF];                      \
+    __shared__ __attribute__((aligned(16))) uint8_t b2[C::MANY ? C::BUF : 16], b3[C::MANY ? C::BUF : 16]; \
+    __shared__ float ml[4][2][32];                                                               \
+    __shared__ uint64_t row_at[4][32]
+
+// Writes the workgroup's rows: through LDS, so that a row goes out as one run
+// of 16-byte words.  FEW: the four waves' results for the same rows are joined
+// on the way (the first `waves` of them had keys).  PART false: O / l rounded
+// to bf16 (0 for a row without keys) at address `to` of the lane's row; PART
+// true: row number to - 1 of part_ml (maximum, sum) and part_o (O, fp32,
+// nothing for a row without keys).  to 0: the lane has no row.
+template <class C, bool PART>
+__device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, float* part_ml, float* part_o, int waves, int D,
+                                           uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, float (*ml)[2][32],
+                                           uint64_t (*row_at)[32]) {
+    const int lane = threadIdx.x & 63, l32 = lane & 31, g2 = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    float* const ml = reinterpret_cast<float*>(buf0);             // [wave][m, l][lane]
-    auto place = [&](int d, int from) __attribute__((always_inline)) -> float* {
-        const int at = d * 3 + (from > (d & 3) ? from - 1 : from);
-        uint8_t* const p = at < C::BLOCKS0 ? buf0 + C::ML + at * 4096 : buf1 + (at - C::BLOCKS0) * 4096;
-        return reinterpret_cast<float*>(p) + lane;
+    constexpr int ROW = C::DP * 4;                                // bytes; 16-byte chunk c of row r at c ^ r
+    constexpr int SRC = C::MANY ? 1 : 4;                          // results that are joined
+    auto area = [&](int w) __attribute__((always_inline)) -> uint8_t* {
+        if constexpr (C::MANY) return w == 0 ? b0 : (w == 1 ? b1 : (w == 2 ? b2 : b3));
+        else return (w < 2 ? b0 : b1) + (w & 1) * 32 * ROW;
     };
-    __syncthreads();                                              // every wave is past its last sub-tile
-    ml[(2 * wave) * 64 + lane] = st.m;
-    ml[(2 * wave + 1) * 64 + lane] = st.l;
+    wait_here<kWaitAll>();
+    __syncthreads();                                              // every wave is past its last keys
+    {
+        uint8_t* const a = area(wave) + l32 * ROW;
+        if (C::MANY || wave < waves) {
 #pragma unroll
-    for (int d = 0; d < C::ND; ++d) {
-        if ((d & 3) == wave) continue;
-        float* const at = place(d, wave);
+            for (int d = 0; d < C::ND; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) at[i * 64] = st.acc[d][i];
-    }
-    __syncthreads();
-    float m = -__builtin_inff(), scale[4], l = 0.0f, own = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) m = fmaxf(m, ml[(2 * w) * 64 + lane]);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float mw = ml[(2 * w) * 64 + lane];
-        scale[w] = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
-        l += ml[(2 * w + 1) * 64 + lane] * scale[w];
-        own = w == wave ? scale[w] : own;
-    }
-#pragma unroll
-    for (int d = 0; d < C::ND; ++d) {
-        if ((d & 3) != wave) continue;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) st.acc[d][i] *= own;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            if (w == (d & 3)) continue;
-            const float* const at = place(d, w);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) st.acc[d][i] += at[i * 64] * scale[w];
+                for (int x = 0; x < 4; ++x) {
+                    const f32x4_t v = {st.acc[d][4 * x], st.acc[d][4 * x + 1], st.acc[d][4 * x + 2], st.acc[d][4 * x + 3]};
+                    *reinterpret_cast<f32x4_t*>(a + (((8 * d + 2 * x + g2) ^ l32) & (C::DP / 4 - 1)) * 16) = v;
+                }
+        }
+        if (g2 == 0) {
+            ml[wave][0][l32] = st.m;
+            ml[wave][1][l32] = st.l;
+            row_at[wave][l32] = to;
         }
     }
-    st.m = m;
-    st.l = l;
-}
-
-// Whether this wave holds channel block d of its rows' result.
-template <class C>
-__device__ __forceinline__ bool holds_block(int d) {
-    return C::MANY || (d & 3) == __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if constexpr (!C::MANY) __syncthreads();
+    // MANY: a wave writes its own rows; FEW: all waves write the same 32 rows
+    constexpr int GROUPS = C::DP / 8;                             // 8 channels per lane
+    constexpr int ITEMS = 32 * GROUPS / (C::MANY ? 64 : kAThreads);
+    const int at = C::MANY ? lane : static_cast<int>(threadIdx.x);
+    const int mine = C::MANY ? wave : 0;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+        const int item = it * (C::MANY ? 64 : kAThreads) + at;
+        const int row = item / GROUPS, cg = item % GROUPS;
+        const uint64_t dst = row_at[mine][row];
+        if (dst == 0 || cg * 8 >= D) continue;
+        float m = ml[mine][0][row], l = ml[mine][1][row], f[SRC];
+        f[0] = 1.0f;
+        if constexpr (!C::MANY) {
+#pragma unroll
+            for (int w = 1; w < 4; ++w) m = fmaxf(m, ml[w][0][row]);
+            l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float mw = ml[w][0][row];
+                f[w] = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
+                l += ml[w][1][row] * f[w];
+            }
+        }
+        f32x4_t o[2] = {f32x4_t{}, f32x4_t{}};
+#pragma unroll
+        for (int w = 0; w < SRC; ++w) {
+            if (!C::MANY && w >= waves) break;
+            const uint8_t* const a = area(C::MANY ? wave : w) + row * ROW;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                o[x] += *reinterpret_cast<const f32x4_t*>(a + (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16) * f[w];
+        }
+        if constexpr (PART) {
+            const int64_t at_row = static_cast<int64_t>(dst - 1);
+            if (cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at_row) = make_float2(m, l);
+            if (m == -__builtin_inff()) continue;
+            f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at_row * D + cg * 8);
+            p[0] = o[0];
+            p[1] = o[1];
+        } else {
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
+            const u32x4_t w = {f32x2_to_bf16x2(o[0].x * inv, o[0].y * inv), f32x2_to_bf16x2(o[0].z * inv, o[0].w * inv),
+                               f32x2_to_bf16x2(o[1].x * inv, o[1].y * inv), f32x2_to_bf16x2(o[1].z * inv, o[1].w * inv)};
+            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
+        }
+    }
 }
 
 // First of this wave's 32 rows in the workgroup's tile.
@@ -575,35 +643,8 @@ __device__ __forceinline__ int wave_row() {
 template <class C, class Keys>
 __device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                        uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, State<C>& st) {
-    if constexpr (C::MANY) {
-        attend_many<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
-    } else {
-        attend_few<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
-        join_waves<C>(b0, b1, st);
-    }
-}
-
-#define ATTN_BUFFERS                                                                          \
-    __shared__ __attribute__((aligned(16))) uint8_t b0[C::BUF], b1[C::BUF];                   \
-    __shared__ __attribute__((aligned(16))) uint8_t b2[C::MANY ? C::BUF : 16], b3[C::MANY ? C::BUF : 16]
-
-// The row's result, O / l rounded to bf16; a row without keys is 0.
-template <class C>
-__device__ __forceinline__ void store_row(const State<C>& st, uint16_t* out, int D) {
-    const int g2 = (threadIdx.x >> 5) & 1;
-    const float inv = st.l > 0.0f ? 1.0f / st.l : (st.l == 0.0f ? 0.0f : st.l);   // NaN stays NaN
-#pragma unroll
-    for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-        for (int a = 0; a < 4; ++a) {
-            const int ch = 32 * d + 8 * a + 4 * g2;
-            if (ch < D && holds_block<C>(d)) {
-                uint2 w;
-                w.x = f32x2_to_bf16x2(st.acc[d][4 * a] * inv, st.acc[d][4 * a + 1] * inv);
-                w.y = f32x2_to_bf16x2(st.acc[d][4 * a + 2] * inv, st.acc[d][4 * a + 3] * inv);
-                *reinterpret_cast<uint2*>(out + ch) = w;
-            }
-        }
+    if constexpr (C::MANY) attend_many<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
+    else attend_few<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
 }
 
 // ------------------------------------------------------------------ prompt
@@ -627,7 +668,7 @@ __device__ __forceinline__ void head_tile(int id, int Hkv, int tiles, int& hk, i
 template <class C>
 __global__ __launch_bounds__(kAThreads) __attribute__((amdgpu_waves_per_eu(C::WAVES, C::WAVES)))
 void attn_prompt_kernel(PromptArgs a) {
-    ATTN_BUFFERS;
+    ATTN_LDS;
     const int lane = threadIdx.x & 63;
     int hk, tile;
     head_tile(blockIdx.x, a.Hkv, a.tiles, hk, tile);
@@ -639,10 +680,12 @@ void attn_prompt_kernel(PromptArgs a) {
     int q0 = 0, nq = 0, k0 = 0, nk = 0, first = 0, found = 0;
     for (int base = 0; base < a.B && !found; base += 64) {
         const int b = base + lane;
-        int s = 0, n = 0, t = 0;
+        int s = 0, n = 0, t = 0, ks = 0, kn = 0;
         if (b < a.B) {
             s = min(max(a.cu_q[b], 0), a.total_q);
             n = max(min(a.cu_q[b + 1], a.total_q) - s, 0);
+            ks = min(max(a.cu_k[b], 0), a.total_k);
+            kn = max(min(a.cu_k[b + 1], a.total_k) - ks, 0);
             t = static_cast<int>((static_cast<int64_t>(n) * G + C::TM - 1) / C::TM);
         }
         int incl = t;
@@ -657,9 +700,8 @@ void attn_prompt_kernel(PromptArgs a) {
             const int src = __builtin_ctzll(hit);
             q0 = __shfl(s, src, 64);
             nq = __shfl(n, src, 64);
-            const int bb = base + src;
-            k0 = min(max(a.cu_k[bb], 0), a.total_k);
-            nk = max(min(a.cu_k[bb + 1], a.total_k) - k0, 0);
+            k0 = __shfl(ks, src, 64);
+            nk = __shfl(kn, src, 64);
             first = __shfl(first + incl - t, src, 64);
             found = 1;
         } else {
@@ -693,8 +735,9 @@ void attn_prompt_kernel(PromptArgs a) {
     keys.n = nk;
     State<C> st;
     attend<C>(keys, q, klim, 0, kend, a.D, a.c, b0, b1, b2, b3, st);
-    if (live)
-        store_row<C>(st, a.out + static_cast<int64_t>(q0 + i) * a.out_stride + static_cast<int64_t>(hk * G + g) * a.D, a.D);
+    uint16_t* const out = a.out + static_cast<int64_t>(q0 + i) * a.out_stride + static_cast<int64_t>(hk * G + g) * a.D;
+    write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, (kend + 31) / 32, a.D, b0, b1, b2, b3,
+                         ml, row_at);
 }
 
 // ----------------------------------------------------------- shared prefix
@@ -706,7 +749,7 @@ void attn_prompt_kernel(PromptArgs a) {
 template <class C>
 __global__ __launch_bounds__(kAThreads) __attribute__((amdgpu_waves_per_eu(C::WAVES, C::WAVES)))
 void attn_shared_kernel(SharedArgs a) {
-    ATTN_BUFFERS;
+    ATTN_LDS;
     int id = blockIdx.x;
     const bool prefix = id < a.prefix_items;
     if (!prefix) id -= a.prefix_items;
@@ -746,25 +789,14 @@ void attn_shared_kernel(SharedArgs a) {
     const int k0 = min(split * per * C::ST, keys.n), k1 = min((split + 1) * per * C::ST, keys.n);
     State<C> st;
     attend<C>(keys, q, klim, k0, k1, a.D, a.c, b0, b1, b2, b3, st);
-    if (!live) return;
+    const int waves = (k1 - k0 + 31) / 32;
     if (a.parts == 1) {
-        store_row<C>(st, a.out + token * a.out_stride + static_cast<int64_t>(head) * a.D, a.D);
-        return;
+        uint16_t* const out = a.out + token * a.out_stride + static_cast<int64_t>(head) * a.D;
+        write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, waves, a.D, b0, b1, b2, b3, ml, row_at);
+    } else {
+        const int64_t at = (token * a.Hq + head) * a.parts + (prefix ? 0 : a.prefix_splits) + split;
+        write_rows<C, true>(st, live ? static_cast<uint64_t>(at) + 1 : 0, a.part_ml, a.part_o, waves, a.D, b0, b1, b2, b3, ml, row_at);
     }
-    const int64_t at = (token * a.Hq + head) * a.parts + (prefix ? 0 : a.prefix_splits) + split;
-    const int g2 = lane >> 5;
-    if (g2 == 0 && holds_block<C>(0)) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(st.m, st.l);
-    if (st.m == -__builtin_inff()) return;
-    float* o = a.part_o + at * a.D;
-#pragma unroll
-    for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int ch = 32 * d + 8 * x + 4 * g2;
-            if (ch < a.D && holds_block<C>(d))
-                *reinterpret_cast<float4*>(o + ch) =
-                    make_float4(st.acc[d][4 * x], st.acc[d][4 * x + 1], st.acc[d][4 * x + 2], st.acc[d][4 * x + 3]);
-        }
 }
 
 // Joins a row's parts: one wave per row, four channels per lane.
