@@ -129,15 +129,15 @@ __device__ __forceinline__ float half_sum(float x) {
 template <class C>
 __device__ __forceinline__ bool has_nonfinite(const uint8_t* v) {
     v += (threadIdx.x & 63) * 16;
-    bool bad = false;
-#pragma unroll
+    uint32_t top = 0;
+#pragma unroll 4
     for (int i = 0; i < 32 * C::RB / 1024; ++i) {
         const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + i * 1024);
+        // an exponent of all ones plus one carries into the sign's place
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            bad |= (w[j] & 0x7F80u) == 0x7F80u || (w[j] & 0x7F800000u) == 0x7F800000u;
+        for (int j = 0; j < 4; ++j) top |= (w[j] & 0x7F807F80u) + 0x00800080u;
     }
-    return __any(bad);
+    return __any((top & 0x80008000u) != 0);
 }
 
 // What one wave needs to walk keys for its 32 rows.
@@ -252,10 +252,14 @@ struct Walk {
             sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf[kk]), qf[kk], sc, 0, 0, 0);
             if (kk < N) load_one(kk);
         }
+        // LDS reads stay a few steps ahead of the products
+        constexpr int AHEAD = C::NK < 6 ? C::NK : 6;
+        __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);                        // DS reads
 #pragma unroll
         for (int kk = 0; kk < C::NK; ++kk) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                    // MFMA
-            if (kk < N) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);        // VMEM
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                        // MFMA
+            if (kk < N) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);            // VMEM loads
+            if (kk + AHEAD < C::NK) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
         return sc;
     }
@@ -326,6 +330,13 @@ struct Walk {
 #pragma unroll
             for (int d = 0; d < C::ND; ++d)
                 st.acc[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vf[k2][d], as_bf16x8(pv), st.acc[d], 0, 0, 0);
+        }
+        constexpr int AHEAD = 2 * C::ND < 4 ? 2 * C::ND : 4;                          // fragments of two reads each
+        __builtin_amdgcn_sched_group_barrier(0x100, 2 * AHEAD, 0);
+#pragma unroll
+        for (int i = 0; i < 2 * C::ND; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if (i + AHEAD < 2 * C::ND) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
         }
     }
     // A zero weight times an infinity or NaN is not zero: a sub-tile that
@@ -507,14 +518,15 @@ __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, 
     w.load_q(q);
     if (n <= 0) return;
     int next = n > 1 ? entry(1) : 0;
-    auto step = [&](auto MORE, int t) __attribute__((always_inline)) {
+    for (int t = 0; t < n; ++t) {
         const int key0 = first + t * 128;
+        const bool more = t + 1 < n;
         wait_here<wait_vm(0)>();                                  // K(t), and the entry of t + 1
         const Source v = source(std::true_type{}, t, slot);
         f32x16_t sc = w.template scores<C::NI>(kb, [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vb, 0, i); });
         const uint32_t vm = PAGED ? static_cast<uint32_t>(__ballot(slot >= 0)) : 0xFFFFFFFFu;
         wait_here<kWaitLds>();                                    // K(t) has been read
-        if constexpr (decltype(MORE)::value) {
+        if (more) {
             slot = next;
             const Source k = source(std::false_type{}, t + 1, slot);
 #pragma unroll
@@ -524,13 +536,11 @@ __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, 
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
         w.weights(sc, pw);
-        if constexpr (decltype(MORE)::value) wait_here<wait_vm(C::NI)>();   // V(t); K(t+1) may be on its way
+        if (more) wait_here<wait_vm(C::NI)>();                    // V(t); K(t+1) may be on its way
         else wait_here<wait_vm(0)>();
         if (!w.put_off(vb, key0)) w.add(vb, pw);
         wait_here<kWaitLds>();                                    // V(t) has been read
-    };
-    for (int t = 0; t + 1 < n; ++t) step(std::true_type{}, t);
-    step(std::false_type{}, n - 1);
+    }
     st.l = half_sum(st.l);
     w.add_late(q, k1, [&](int key) {
         const int t = key - k0;
@@ -799,33 +809,63 @@ void attn_shared_kernel(SharedArgs a) {
     }
 }
 
-// Joins a row's parts: one wave per row, four channels per lane.
+// Joins a row's parts.  WPR waves per row (1 or 4) take every WPR-th part,
+// eight parts' channels in flight at once (four channels per lane), and meet
+// in LDS.
+template <int WPR>
 __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kAThreads / 64) + (threadIdx.x >> 6);
-    if (row >= static_cast<int64_t>(a.B) * a.L * a.Hq) return;
-    const float* ml = a.part_ml + 2 * row * a.parts;
+    __shared__ f32x4_t o_all[4][64];
+    __shared__ float l_all[4];
+    const int lane = threadIdx.x & 63, ch = 4 * lane;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (4 / WPR) + (WPR == 1 ? wave : 0);
+    if (row >= static_cast<int64_t>(a.B) * a.L * a.Hq) return;    // WPR == 1 alone: no barrier follows
+    const int w0 = WPR == 1 ? 0 : wave;
+    const float* const ml = a.part_ml + 2 * row * a.parts;
+    const float* const po = a.part_o + row * a.parts * a.D + ch;
     float m = -__builtin_inff();
     for (int p = lane; p < a.parts; p += 64) m = fmaxf(m, ml[2 * p]);
     m = wave_max(m);
-    const int ch = 4 * lane;
     float l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float* po = a.part_o + row * a.parts * a.D + ch;
-    for (int p = 0; p < a.parts; ++p) {
-        const float mp = ml[2 * p];
-        if (mp == -__builtin_inff()) {
-            l += ml[2 * p + 1];                                   // 0, or NaN where every score was NaN
-            continue;
+    f32x4_t o = f32x4_t{};
+    const bool live = ch < a.D;
+    // the wave's parts p = w0 + WPR i; lane i holds the weight of part i of a
+    // group of 64
+    for (int base = w0; base < a.parts; base += 64 * WPR) {
+        const int pl = base + WPR * lane;
+        float w = 0.0f;
+        if (pl < a.parts) {
+            const float2 x = *reinterpret_cast<const float2*>(ml + 2 * pl);
+            w = x.x == -__builtin_inff() ? 0.0f : (x.x == m ? 1.0f : __builtin_amdgcn_exp2f(x.x - m));
+            // a part without keys has sum 0, or NaN where every score was NaN
+            l += x.x == -__builtin_inff() ? x.y : x.y * w;
         }
-        const float w = mp == m ? 1.0f : __builtin_amdgcn_exp2f(mp - m);
-        l += ml[2 * p + 1] * w;
-        if (ch < a.D) {
-            const float4 x = *reinterpret_cast<const float4*>(po + static_cast<int64_t>(p) * a.D);
-            o.x += x.x * w; o.y += x.y * w; o.z += x.z * w; o.w += x.w * w;
+        const int n = min(64, (a.parts - base + WPR - 1) / WPR);
+        for (int i = 0; i < n; i += 8) {
+            f32x4_t x[8];
+            float wi[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                wi[j] = i + j < n ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i + j)) : 0.0f;
+                // a part of weight 0 holds nothing that was written
+                x[j] = f32x4_t{};
+                if (wi[j] > 0.0f && live) x[j] = *reinterpret_cast<const f32x4_t*>(po + static_cast<int64_t>(base + WPR * (i + j)) * a.D);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o += x[j] * wi[j];
         }
     }
-    if (ch >= a.D) return;
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) l += __shfl_xor(l, off, 64);
+    if constexpr (WPR == 4) {
+        o_all[wave][lane] = o;
+        if (lane == 0) l_all[wave] = l;
+        __syncthreads();
+        if (wave != 0) return;
+        l = l_all[0] + l_all[1] + l_all[2] + l_all[3];
+        o = o_all[0][lane] + o_all[1][lane] + o_all[2][lane] + o_all[3][lane];
+    }
+    if (!live) return;
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
     uint2 w;
     w.x = f32x2_to_bf16x2(o.x * inv, o.y * inv);
@@ -920,7 +960,10 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     }
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.L * a.Hq;
-    attn_join_kernel<<<static_cast<unsigned>((rows + 3) / 4), kAThreads, 0, s>>>(a);
+    // four waves per row where the parts are many (32 rows of 32 parts: 19 ->
+    // 9 us), one where the rows are
+    if (a.parts > 8) attn_join_kernel<4><<<static_cast<unsigned>(rows), kAThreads, 0, s>>>(a);
+    else attn_join_kernel<1><<<static_cast<unsigned>((rows + 3) / 4), kAThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
