@@ -51,27 +51,30 @@ constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data for
 
 __device__ __attribute__((aligned(16))) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
 
-// MANY: four waves of 32 query rows each share stages of 64 keys; FEW: four
-// waves share 32 query rows and each walks every fourth 32-key sub-tile
-// through LDS of its own, so that no wave waits for another before the end.
-template <int DP_, bool MANY_>
+// KW: waves that share 32 query rows, each with keys of its own; 4 / KW such
+// groups make the workgroup's tile.
+//   KW 1 (128 rows), KW 2 (64 rows): all four waves load and share stages of
+//     64 keys; a wave takes both 32-key sub-tiles, or one of them.
+//   KW 4 (32 rows): each wave walks every fourth 32-key sub-tile through LDS
+//     of its own, so that no wave waits for another before the end.
+template <int DP_, int KW_>
 struct ACfg {
-    static constexpr int DP = DP_;
-    static constexpr bool MANY = MANY_;
+    static constexpr int DP = DP_, KW = KW_;
+    static constexpr bool SHARE = KW < 4;                    // stages shared by all waves
     static constexpr int WAVES = DP <= 128 ? 2 : 1;          // per SIMD: 256 or 512 registers each
-    static constexpr int TM = MANY ? 128 : 32;               // query rows per workgroup
-    static constexpr int ST = MANY ? 64 : 128;               // keys per workgroup step
+    static constexpr int TM = 32 * (4 / KW);                 // query rows per workgroup
+    static constexpr int ST = SHARE ? 64 : 128;              // keys per workgroup step
     static constexpr int CH = DP / 8;                        // 16-byte chunks per row
     static constexpr int RB = DP * 2;                        // bytes per row
-    static constexpr int R = MANY ? 16 : 32;                 // rows of K (and V) a wave loads at once
+    static constexpr int R = SHARE ? 16 : 32;                // rows of K (and V) a wave loads at once
     static constexpr int RPI = 1024 / RB;                    // rows per load instruction
     static constexpr int NI = R / RPI;                       // load instructions for R rows
     static constexpr int NK = DP / 16;                       // MFMA steps of K Q^T
     static constexpr int ND = DP / 32;                       // 32-channel blocks of O^T
-    // LDS buffers: MANY has K and V of two stages of 64 rows, FEW K and V of
-    // one sub-tile of 32 rows per wave, each an object of its own: the
-    // compiler orders LDS reads after the loads that write the same object
-    static constexpr int BUF = (MANY ? 64 : 128) * RB;
+    // LDS buffers: K and V of two shared stages, or of one sub-tile per wave,
+    // each an object of its own: the compiler orders LDS reads after the
+    // loads that write the same object
+    static constexpr int BUF = (SHARE ? 64 : 128) * RB;
     static_assert(R % RPI == 0, "whole load instructions");
 };
 
@@ -184,15 +187,27 @@ struct Walk {
         lrow = lane / C::CH;
         lpos = lane % C::CH;
     }
-    // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
-    __device__ __forceinline__ void load_q(const uint16_t* q) {
+    // Query rows r0 .. r0 + N * RPI - 1 into LDS like rows of K (q: the lane's
+    // row, or nullptr; lane r holds row r): whole rows per instruction, where
+    // operand reads from memory would touch 32 rows each.
+    template <int N>
+    __device__ __forceinline__ void stage_q(const uint16_t* q, uint8_t* dst, int r0) const {
+        const uint64_t mine = reinterpret_cast<uint64_t>(q);
+        const int lo = static_cast<int>(mine), hi = static_cast<int>(mine >> 32);
 #pragma unroll
-        for (int kk = 0; kk < C::NK; ++kk) {
-            const int d = 16 * kk + 8 * g2;
-            u32x4_t w = {0, 0, 0, 0};
-            if (q && d < D) w = *reinterpret_cast<const u32x4_t*>(q + d);
-            qf[kk] = as_bf16x8(w);
+        for (int i = 0; i < N; ++i) {
+            const int row = r0 + i * C::RPI + lrow;
+            const int ch = lpos ^ swz_k<C::DP>(row);
+            const uint64_t p = static_cast<uint32_t>(__shfl(lo, row, 64)) | static_cast<uint64_t>(static_cast<uint32_t>(__shfl(hi, row, 64))) << 32;
+            const uint64_t src = (p != 0 && ch * 8 < D) ? p + ch * 16 : reinterpret_cast<uint64_t>(kZeroChunk);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                             (__attribute__((address_space(3))) void*)(dst + (r0 + i * C::RPI) * C::RB), 16, 0, 0);
         }
+    }
+    // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
+    __device__ __forceinline__ void read_q(const uint8_t* qt) {
+#pragma unroll
+        for (int kk = 0; kk < C::NK; ++kk) qf[kk] = as_bf16x8(*reinterpret_cast<const u32x4_t*>(qt + (kaddr ^ (kk << 5))));
     }
 
     // ---- loads of R rows of K or V into LDS, one instruction (i < C::NI) at a
@@ -279,7 +294,9 @@ struct Walk {
         }
     }
     // Weights, as bf16 pairs in accumulator order; moves the running maximum.
-    __device__ __forceinline__ void weights(const f32x16_t& sc, uint32_t* pw) const {
+    // N loads go out among the exponentials.
+    template <int N, class F>
+    __device__ __forceinline__ void weights(const f32x16_t& sc, uint32_t* pw, F&& load_one) const {
         float mx = fmaxf(sc[0], sc[1]);
 #pragma unroll
         for (int i = 2; i < 16; i += 2) mx = fmaxf(fmaxf(sc[i], sc[i + 1]), mx);
@@ -306,8 +323,17 @@ struct Walk {
             s0 += p0;
             s1 += p1;
             pw[i] = f32x2_to_bf16x2(p0, p1);
+#pragma unroll
+            for (int j = i * N / 8; j < (i + 1) * N / 8; ++j) load_one(j);
         }
         st.l += s0 + s1;
+        if constexpr (N > 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x402, 48 / N, 0);                       // VALU, exponentials
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);                            // VMEM loads
+            }
+        }
     }
     // V^T fragments: 16 keys (step k2) x 32 channels (block d)
     __device__ __forceinline__ bf16x8_t v_frag(const uint8_t* vt, int k2, int d) const {
@@ -406,8 +432,8 @@ __device__ __forceinline__ void wait_here() {
 // Keys k0 .. k1-1 (a uniform range) for the wave's 32 rows, the workgroup's
 // four waves sharing each stage of 64 keys.
 template <class C, class Keys>
-__device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
-                                            uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
+__device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
+                                              uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
     using W = Walk<C, Keys>;
     using Source = typename W::Source;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -434,7 +460,10 @@ __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q,
         else return ~uint64_t(0);
     };
     // stage s lives in buffers s % 2; its loads are issued while stage s-1 is
-    // computed, its table entries are read one stage earlier still
+    // computed, its table entries are read one stage earlier still.  The
+    // query rows come through the buffers of stage 1.
+    uint8_t* const qt = (wave < 2 ? kb1 : vb1) + (wave & 1) * 32 * C::RB;
+    if (n_stages > 0) w.template stage_q<32 / C::RPI>(q, qt, 0);
     uint64_t vcur = valid(slot);
     if (n_stages > 0) {
         const Source k = source(std::false_type{}, 0), v = source(std::true_type{}, 0);
@@ -443,14 +472,15 @@ __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q,
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) w.template load<true>(v, vb0 + row0 * C::RB, row0, i);
     }
-    w.load_q(q);
     if (n_stages <= 0) return;
+    wait_here<wait_vm(2 * C::NI)>();
+    w.read_q(qt);
     slot = n_stages > 1 ? entry(1) : -1;
-    auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& load_one) __attribute__((always_inline)) {
+    auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& load_one, auto&& load_more) __attribute__((always_inline)) {
         f32x16_t sc = w.template scores<C::NI>(kt, load_one);
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
-        w.weights(sc, pw);
+        w.template weights<C::KW == 1 ? 0 : C::NI>(sc, pw, load_more);
         if (!w.put_off(vt, key0)) w.add(vt, pw);
     };
     auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s) __attribute__((always_inline)) {
@@ -461,14 +491,20 @@ __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q,
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         __builtin_amdgcn_sched_barrier(0);
         const int key0 = k0 + s * 64;
-        // the next stage's K goes out among this one's first scores, its V
-        // among the second ones (past the last stage: zeros)
+        // the next stage's loads (past the last stage: zeros) go out among
+        // this one's scores and, with one sub-tile per stage, its weights
         const Source k = source(std::false_type{}, s + 1), v = source(std::true_type{}, s + 1);
         const uint64_t vnext = valid(slot);
-        sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur),
-                 [&](int i) __attribute__((always_inline)) { w.template load<false>(k, kn + row0 * C::RB, row0, i); });
-        sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32),
-                 [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vn + row0 * C::RB, row0, i); });
+        auto load_k = [&](int i) __attribute__((always_inline)) { w.template load<false>(k, kn + row0 * C::RB, row0, i); };
+        auto load_v = [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vn + row0 * C::RB, row0, i); };
+        if constexpr (C::KW == 1) {
+            sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur), load_k, [](int) {});
+            sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32), load_v, [](int) {});
+        } else {
+            const int half = wave >> 1;                           // this wave's sub-tile
+            sub_tile(kc + half * 32 * C::RB, vc + half * 32 * C::RB, key0 + half * 32, static_cast<uint32_t>(vcur >> (32 * half)),
+                     load_k, load_v);
+        }
         vcur = vnext;
         slot = s + 2 < n_stages ? entry(s + 2) : -1;
     };
@@ -477,7 +513,10 @@ __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q,
         if (s + 1 < n_stages) step(kb1, vb1, kb0, vb0, s + 1);
     }
     st.l = half_sum(st.l);
-    w.add_late(q, k1, [&](int key) { return k0 + (key - k0) / 32 * 32; });
+    w.add_late(q, k1, [&](int key) {
+        const int t = key - k0;
+        return C::KW == 1 || (t >> 5 & 1) == wave >> 1 ? k0 + (t & ~31) : -1;
+    });
 }
 
 // Keys k0 .. k1-1 for 32 rows that the four waves share: wave w takes
@@ -485,14 +524,14 @@ __device__ __forceinline__ void attend_many(const Keys& keys, const uint16_t* q,
 // the next sub-tile goes out while this one's weights are formed, its V among
 // its scores, so 16 (D <= 64: 8, D > 128: 32) KiB per wave are in flight.
 template <class C, class Keys>
-__device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
-                                           uint8_t* kb, uint8_t* vb, State<C>& st) {
+__device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
+                                           uint8_t* kb_all, uint8_t* vb_all, State<C>& st) {
     using W = Walk<C, Keys>;
     using Source = typename W::Source;
     constexpr bool PAGED = W::PAGED;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    kb += wave * 32 * C::RB;
-    vb += wave * 32 * C::RB;
+    uint8_t* const kb = kb_all + wave * 32 * C::RB;
+    uint8_t* const vb = vb_all + wave * 32 * C::RB;
     const int first = k0 + wave * 32;
     const int n = k1 > first ? (k1 - first + 127) / 128 : 0;
     auto entry = [&](int t) __attribute__((always_inline)) -> int {
@@ -510,14 +549,24 @@ __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, 
         if constexpr (PAGED) return w.template paged_rows<v>(sl, 0);
         else return w.template packed_rows<v>(first + t * 128, k1);
     };
+    // the query rows come through the place of wave 0's V, eight from each wave
+    w.template stage_q<8 / C::RPI>(q, vb_all, wave * 8);
     if (n > 0) {
         const Source k = source(std::false_type{}, 0, slot);
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb, 0, i);
+        wait_here<wait_vm(C::NI)>();
+    } else {
+        wait_here<wait_vm(0)>();
     }
-    w.load_q(q);
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    w.read_q(vb_all);
+    wait_here<kWaitLds>();
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
     if (n <= 0) return;
-    int next = n > 1 ? entry(1) : 0;
+    int next = n > 1 ? entry(1) : -1;
     for (int t = 0; t < n; ++t) {
         const int key0 = first + t * 128;
         const bool more = t + 1 < n;
@@ -531,11 +580,11 @@ __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, 
             const Source k = source(std::false_type{}, t + 1, slot);
 #pragma unroll
             for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb, 0, i);
-            next = t + 2 < n ? entry(t + 2) : 0;
+            next = t + 2 < n ? entry(t + 2) : -1;
         }
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
-        w.weights(sc, pw);
+        w.template weights<0>(sc, pw, [](int) {});
         if (more) wait_here<wait_vm(C::NI)>();                    // V(t); K(t+1) may be on its way
         else wait_here<wait_vm(0)>();
         if (!w.put_off(vb, key0)) w.add(vb, pw);
@@ -551,35 +600,41 @@ __device__ __forceinline__ void attend_few(const Keys& keys, const uint16_t* q, 
 // ------------------------------------------------------------- results
 
 // LDS of one workgroup.
-#define ATTN_LDS                                                                                 \
-    __shared__ __attribute__((aligned(16))) uint8_t b0[C::BUF], b1[C::BUF];                      \
-    __shared__ __attribute__((aligned(16))) uint8_t b2[C::MANY ? C::BUF : 16], b3[C::MANY ? C::BUF : 16]; \
-    __shared__ float ml[4][2][32];                                                               \
+#define ATTN_LDS                                                                                       \
+    __shared__ __attribute__((aligned(16))) uint8_t b0[C::BUF], b1[C::BUF];                            \
+    __shared__ __attribute__((aligned(16))) uint8_t b2[C::SHARE ? C::BUF : 16], b3[C::SHARE ? C::BUF : 16]; \
+    __shared__ float ml[4][2][32];                                                                     \
     __shared__ uint64_t row_at[4][32]
 
+// First of this wave's 32 rows in the workgroup's tile.
+template <class C>
+__device__ __forceinline__ int wave_row() {
+    return (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % (4 / C::KW)) * 32;
+}
+
 // Writes the workgroup's rows: through LDS, so that a row goes out as one run
-// of 16-byte words.  FEW: the four waves' results for the same rows are joined
-// on the way (the first `waves` of them had keys).  PART false: O / l rounded
-// to bf16 (0 for a row without keys) at address `to` of the lane's row; PART
-// true: row number to - 1 of part_ml (maximum, sum) and part_o (O, fp32,
-// nothing for a row without keys).  to 0: the lane has no row.
+// of 16-byte words; the KW waves' results for the same rows are joined on the
+// way (k-th of them: with_keys > k says that it had keys).  PART false: O / l
+// rounded to bf16 (0 for a row without keys) at address `to` of the lane's
+// row; PART true: row number to - 1 of part_ml (maximum, sum) and part_o (O,
+// fp32, nothing for a row without keys).  to 0: the lane has no row.
 template <class C, bool PART>
-__device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, float* part_ml, float* part_o, int waves, int D,
+__device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, float* part_ml, float* part_o, int with_keys, int D,
                                            uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, float (*ml)[2][32],
                                            uint64_t (*row_at)[32]) {
     const int lane = threadIdx.x & 63, l32 = lane & 31, g2 = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int QW = 4 / C::KW;                                 // groups of 32 rows
     constexpr int ROW = C::DP * 4;                                // bytes; 16-byte chunk c of row r at c ^ r
-    constexpr int SRC = C::MANY ? 1 : 4;                          // results that are joined
     auto area = [&](int w) __attribute__((always_inline)) -> uint8_t* {
-        if constexpr (C::MANY) return w == 0 ? b0 : (w == 1 ? b1 : (w == 2 ? b2 : b3));
+        if constexpr (C::SHARE) return w == 0 ? b0 : (w == 1 ? b1 : (w == 2 ? b2 : b3));
         else return (w < 2 ? b0 : b1) + (w & 1) * 32 * ROW;
     };
     wait_here<kWaitAll>();
     __syncthreads();                                              // every wave is past its last keys
     {
         uint8_t* const a = area(wave) + l32 * ROW;
-        if (C::MANY || wave < waves) {
+        if (wave / QW < with_keys) {
 #pragma unroll
             for (int d = 0; d < C::ND; ++d)
 #pragma unroll
@@ -594,67 +649,72 @@ __device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, floa
             row_at[wave][l32] = to;
         }
     }
-    if constexpr (!C::MANY) __syncthreads();
-    // MANY: a wave writes its own rows; FEW: all waves write the same 32 rows
-    constexpr int GROUPS = C::DP / 8;                             // 8 channels per lane
-    constexpr int ITEMS = 32 * GROUPS / (C::MANY ? 64 : kAThreads);
-    const int at = C::MANY ? lane : static_cast<int>(threadIdx.x);
-    const int mine = C::MANY ? wave : 0;
+    __syncthreads();
+    // the KW waves of a group write its 32 rows: RPW of them per wave and
+    // instruction, 8 channels per lane
+    constexpr int GROUPS = C::DP / 8;
+    constexpr int ITEMS = 32 * GROUPS / (64 * C::KW);
+    const int q = wave % QW, cg = lane % GROUPS;
+    int row[ITEMS];
+    uint64_t dst[ITEMS];
+    float m[ITEMS], l[ITEMS], f[ITEMS][C::KW];
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-        const int item = it * (C::MANY ? 64 : kAThreads) + at;
-        const int row = item / GROUPS, cg = item % GROUPS;
-        const uint64_t dst = row_at[mine][row];
-        if (dst == 0 || cg * 8 >= D) continue;
-        float m = ml[mine][0][row], l = ml[mine][1][row], f[SRC];
-        f[0] = 1.0f;
-        if constexpr (!C::MANY) {
+        row[it] = (it * C::KW + wave / QW) * (64 / GROUPS) + lane / GROUPS;
+        dst[it] = row_at[q][row[it]];
+        float mk[C::KW], lk[C::KW];
 #pragma unroll
-            for (int w = 1; w < 4; ++w) m = fmaxf(m, ml[w][0][row]);
-            l = 0.0f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const float mw = ml[w][0][row];
-                f[w] = mw == m ? 1.0f : __builtin_amdgcn_exp2f(mw - m);
-                l += ml[w][1][row] * f[w];
-            }
+        for (int k = 0; k < C::KW; ++k) {
+            mk[k] = ml[q + k * QW][0][row[it]];
+            lk[k] = ml[q + k * QW][1][row[it]];
         }
-        f32x4_t o[2] = {f32x4_t{}, f32x4_t{}};
+        m[it] = mk[0];
 #pragma unroll
-        for (int w = 0; w < SRC; ++w) {
-            if (!C::MANY && w >= waves) break;
-            const uint8_t* const a = area(C::MANY ? wave : w) + row * ROW;
+        for (int k = 1; k < C::KW; ++k) m[it] = fmaxf(m[it], mk[k]);
+        l[it] = 0.0f;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
-                o[x] += *reinterpret_cast<const f32x4_t*>(a + (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16) * f[w];
-        }
-        if constexpr (PART) {
-            const int64_t at_row = static_cast<int64_t>(dst - 1);
-            if (cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at_row) = make_float2(m, l);
-            if (m == -__builtin_inff()) continue;
-            f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at_row * D + cg * 8);
-            p[0] = o[0];
-            p[1] = o[1];
-        } else {
-            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
-            const u32x4_t w = {f32x2_to_bf16x2(o[0].x * inv, o[0].y * inv), f32x2_to_bf16x2(o[0].z * inv, o[0].w * inv),
-                               f32x2_to_bf16x2(o[1].x * inv, o[1].y * inv), f32x2_to_bf16x2(o[1].z * inv, o[1].w * inv)};
-            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
+        for (int k = 0; k < C::KW; ++k) {
+            f[it][k] = mk[k] == m[it] ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - m[it]);
+            l[it] += lk[k] * f[it][k];
         }
     }
-}
-
-// First of this wave's 32 rows in the workgroup's tile.
-template <class C>
-__device__ __forceinline__ int wave_row() {
-    return C::MANY ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 32 : 0;
+    f32x4_t o[ITEMS][2];
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) o[it][0] = o[it][1] = f32x4_t{};
+#pragma unroll
+    for (int k = 0; k < C::KW; ++k) {
+        if (k >= with_keys) break;
+        const uint8_t* const a = area(q + k * QW);
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                o[it][x] += *reinterpret_cast<const f32x4_t*>(a + row[it] * ROW + (((2 * cg + x) ^ row[it]) & (C::DP / 4 - 1)) * 16) * f[it][k];
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+        if (dst[it] == 0 || cg * 8 >= D) continue;
+        if constexpr (PART) {
+            const int64_t at = static_cast<int64_t>(dst[it] - 1);
+            if (cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m[it], l[it]);
+            if (m[it] == -__builtin_inff()) continue;
+            f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at * D + cg * 8);
+            p[0] = o[it][0];
+            p[1] = o[it][1];
+        } else {
+            const float inv = l[it] > 0.0f ? 1.0f / l[it] : (l[it] == 0.0f ? 0.0f : l[it]);   // NaN stays NaN
+            const f32x4_t x = o[it][0] * inv, y = o[it][1] * inv;
+            const u32x4_t w = {f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w), f32x2_to_bf16x2(y.x, y.y), f32x2_to_bf16x2(y.z, y.w)};
+            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst[it]) + cg * 8) = w;
+        }
+    }
 }
 
 template <class C, class Keys>
 __device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                        uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, State<C>& st) {
-    if constexpr (C::MANY) attend_many<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
-    else attend_few<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
+    if constexpr (C::SHARE) attend_stages<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
+    else attend_streams<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
 }
 
 // ------------------------------------------------------------------ prompt
@@ -874,29 +934,35 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
     *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (row - token * a.Hq) * a.D + ch) = w;
 }
 
-template <int DP> using Many = ACfg<DP, true>;
-template <int DP> using Few = ACfg<DP, false>;
-
 constexpr int kComputeUnits = 256;
 
+// Query rows per workgroup and what goes with them: 128, 64 or 32.
+int key_waves(int tm) { return 128 / tm; }
+int step_keys(int tm) { return tm == 32 ? 128 : 64; }
+
 // D channels run in the kernels of the next padded size.
-template <class F>
-hipError_t by_size(int D, bool many, F&& launch) {
-    if (D <= 64) return many ? launch(Many<64>{}) : launch(Few<64>{});
-    if (D <= 128) return many ? launch(Many<128>{}) : launch(Few<128>{});
-    return many ? launch(Many<256>{}) : launch(Few<256>{});
+template <int DP, class F>
+hipError_t by_rows(int tm, F&& launch) {
+    return tm == 128 ? launch(ACfg<DP, 1>{}) : (tm == 64 ? launch(ACfg<DP, 2>{}) : launch(ACfg<DP, 4>{}));
 }
+template <class F>
+hipError_t by_size(int D, int tm, F&& launch) {
+    return D <= 64 ? by_rows<64>(tm, launch) : (D <= 128 ? by_rows<128>(tm, launch) : by_rows<256>(tm, launch));
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
 hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
-    // wide tiles once they fill the compute units, else more and narrower ones
     const int64_t rows = static_cast<int64_t>(a.total_q) * (a.Hq / a.Hkv);
-    const bool many = a.Hkv * ((rows + 127) / 128) >= kComputeUnits;
-    const int tm = many ? 128 : 32;
+    // the widest tile whose workgroups fill the compute units, as wide tiles
+    // load least; with too few rows for any, the narrowest
+    int tm = 128;
+    while (tm > 32 && a.Hkv * ceil_div(rows, tm) < kComputeUnits) tm /= 2;
     // every sequence ends in at most one partial tile
     a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
-    return by_size(a.D, many, [&](auto cfg) {
+    return by_size(a.D, tm, [&](auto cfg) {
         attn_prompt_kernel<decltype(cfg)><<<a.tiles * a.Hkv, kAThreads, 0, s>>>(a);
         return hipGetLastError();
     });
@@ -905,30 +971,35 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
                             int64_t suffix_cap) {
     SharedPlan p{};
-    const int64_t G = Hq / Hkv;
-    p.merged = B == 1 || prefix_cap == 0;
-    const int64_t rows_p = B * L * G, rows_s = L * G;
-    p.prefix_many = rows_p > 64;
-    p.suffix_many = rows_s > 64;
-    const int64_t tm_p = p.prefix_many ? 128 : 32, tm_s = p.suffix_many ? 128 : 32;
-    const int64_t st_p = p.prefix_many ? 64 : 128, st_s = p.suffix_many ? 64 : 128;
+    const int64_t G = Hq / Hkv, rows_s = L * G, rows_p = B * rows_s;
+    // workgroups that run at once
+    const int64_t slots = D <= 128 ? 2 * kComputeUnits : kComputeUnits;
+    auto tile = [](int64_t rows) { return rows > 64 ? 128 : (rows > 32 ? 64 : 32); };
+    p.prefix_tm = tile(rows_p);
+    p.suffix_tm = tile(rows_s);
+    // A sequence whose rows fill its tiles reads the prefix no more often by
+    // itself than a tile of the whole batch does: then the prefix is the head
+    // of every sequence's range of keys and nothing has to be joined.
+    p.merged = B == 1 || prefix_cap == 0 ||
+               2 * B * ceil_div(rows_s, p.suffix_tm) * p.suffix_tm <= 3 * ceil_div(rows_p, p.prefix_tm) * p.prefix_tm;
     const int64_t keys_s = suffix_cap + (p.merged ? prefix_cap : 0);
-    const int64_t steps_p = p.merged ? 0 : (prefix_cap + st_p - 1) / st_p;
-    const int64_t steps_s = (keys_s + st_s - 1) / st_s;
-    const int64_t tiles_p = p.merged ? 0 : (rows_p + tm_p - 1) / tm_p;
-    p.suffix_tiles = (rows_s + tm_s - 1) / tm_s;
-    // steps per work item such that the items of both kinds fill the compute
-    // units once
-    const int64_t all = Hkv * (tiles_p * steps_p + B * p.suffix_tiles * steps_s);
-    int64_t per = (all + kComputeUnits - 1) / kComputeUnits;
-    if (per < 1) per = 1;
-    p.prefix_splits = (steps_p + per - 1) / per;
-    p.suffix_splits = (steps_s + per - 1) / per;
+    const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(p.prefix_tm));
+    const int64_t steps_s = ceil_div(keys_s, step_keys(p.suffix_tm));
+    const int64_t tiles_p = p.merged ? 0 : ceil_div(rows_p, p.prefix_tm);
+    p.suffix_tiles = ceil_div(rows_s, p.suffix_tm);
+    // keys are split until the workgroups fill the slots once
+    auto splits = [&](int64_t tiles, int64_t steps) {
+        if (tiles == 0 || steps == 0) return int64_t(0);
+        const int64_t per = ceil_div(tiles * steps, slots);
+        return ceil_div(steps, per);
+    };
+    p.prefix_splits = splits(Hkv * tiles_p, steps_p);
+    p.suffix_splits = splits(Hkv * B * p.suffix_tiles, steps_s);
     p.prefix_items = Hkv * tiles_p * p.prefix_splits;
     p.suffix_items = Hkv * B * p.suffix_tiles * p.suffix_splits;
     p.parts = p.prefix_splits + p.suffix_splits;
     const int64_t rows = B * L * Hq;
-    p.ml_bytes = p.parts > 1 ? (rows * p.parts * 8 + 255) / 256 * 256 : 0;
+    p.ml_bytes = p.parts > 1 ? ceil_div(rows * p.parts * 8, 256) * 256 : 0;
     p.ws_bytes = 256 + p.ml_bytes + (p.parts > 1 ? rows * p.parts * D * 4 : 0);
     return p;
 }
@@ -942,21 +1013,21 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
     a.part_ml = reinterpret_cast<float*>(w);
     a.part_o = reinterpret_cast<float*>(w + p.ml_bytes);
-    auto run = [&](bool many, int64_t prefix_items, int64_t suffix_items) {
+    auto run = [&](int tm, int64_t prefix_items, int64_t suffix_items) {
         a.prefix_items = static_cast<int>(prefix_items);
         const int grid = static_cast<int>(prefix_items + suffix_items);
         if (grid == 0) return hipSuccess;
-        return by_size(a.D, many, [&](auto cfg) {
+        return by_size(a.D, tm, [&](auto cfg) {
             attn_shared_kernel<decltype(cfg)><<<grid, kAThreads, 0, s>>>(a);
             return hipGetLastError();
         });
     };
     hipError_t e;
-    if (p.prefix_many == p.suffix_many) {
-        e = run(p.prefix_many, p.prefix_items, p.suffix_items);
+    if (p.prefix_tm == p.suffix_tm) {
+        e = run(p.prefix_tm, p.prefix_items, p.suffix_items);
     } else {
-        e = run(p.prefix_many, p.prefix_items, 0);
-        if (e == hipSuccess) e = run(p.suffix_many, 0, p.suffix_items);
+        e = run(p.prefix_tm, p.prefix_items, 0);
+        if (e == hipSuccess) e = run(p.suffix_tm, 0, p.suffix_items);
     }
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.L * a.Hq;

@@ -70,8 +70,8 @@ struct SharedArgs {
 };
 // Launch plan of a shared-prefix call, from its host sizes alone.
 struct SharedPlan {
-    bool merged;         // prefix and suffix are one range of keys (one sequence, or no prefix)
-    bool prefix_many, suffix_many;
+    bool merged;         // prefix and suffix are one range of keys
+    int prefix_tm, suffix_tm;   // query rows per workgroup
     int64_t prefix_splits, suffix_splits, suffix_tiles, prefix_items, suffix_items, parts;
     int64_t ml_bytes, ws_bytes;
 };
