@@ -215,36 +215,43 @@ struct Walk {
     //      swizzle); Source holds what is common to the instructions.
     struct Source {
         __amdgpu_buffer_rsrc_t rs;   // packed: a buffer that ends with the last key, rows past it load zeros
-        uint64_t base;               // paged
-        int stride, slot, from;      // slot: of the window's key `lane`; from: the window row of instruction 0
+        int stride;
     };
-    template <bool V>
-    __device__ __forceinline__ Source packed_rows(int key0, int k1) const {
-        Source s;
-        s.stride = V ? keys.v_stride : keys.k_stride;
-        const int left = min(k1 - key0, C::R);
-        s.rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(V ? keys.v : keys.k) + static_cast<int64_t>(key0) * s.stride), 0,
-            left > 0 ? (left - 1) * s.stride + D * 2 : 0, kBufferWord3);
+    // Paged: the slots of the rows that this lane loads, taken from the lanes
+    // that read the table (lane l: window key l); from: the window row of
+    // instruction 0.
+    struct Slots {
+        int at[PAGED ? C::NI : 1];
+    };
+    __device__ __forceinline__ Slots slots_of(int slot, int from) const {
+        Slots s;
+        if constexpr (PAGED) {
+#pragma unroll
+            for (int i = 0; i < C::NI; ++i) s.at[i] = __shfl(slot, from + i * C::RPI + lrow, 64);
+        }
         return s;
     }
     template <bool V>
-    __device__ __forceinline__ Source paged_rows(int slot, int from) const {
+    __device__ __forceinline__ Source source(int key0, int k1) const {
         Source s;
-        s.base = reinterpret_cast<uint64_t>(V ? keys.v : keys.k);
-        s.slot = slot;
-        s.from = from;
+        if constexpr (!PAGED) {
+            s.stride = V ? keys.v_stride : keys.k_stride;
+            const int left = min(k1 - key0, C::R);
+            s.rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(V ? keys.v : keys.k) + static_cast<int64_t>(key0) * s.stride), 0,
+                left > 0 ? (left - 1) * s.stride + D * 2 : 0, kBufferWord3);
+        }
         return s;
     }
     template <bool V>
-    __device__ __forceinline__ void load(const Source& s, uint8_t* dst, int row0, int i) const {
+    __device__ __forceinline__ void load(const Source& s, const Slots& sl, uint8_t* dst, int row0, int i) const {
         const int row = row0 + i * C::RPI + lrow;
         const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
         __attribute__((address_space(3))) void* const to = (__attribute__((address_space(3))) void*)(dst + i * 1024);
         if constexpr (PAGED) {
-            const int sl = __shfl(s.slot, s.from + i * C::RPI + lrow, 64);
-            const uint64_t at = s.base + static_cast<uint64_t>(static_cast<uint32_t>(sl)) * keys.stride + ch * 16;
-            const uint64_t src = (sl >= 0 && ch * 8 < D) ? at : reinterpret_cast<uint64_t>(kZeroChunk);
+            const uint64_t at = reinterpret_cast<uint64_t>(V ? keys.v : keys.k) +
+                                static_cast<uint64_t>(static_cast<uint32_t>(sl.at[i])) * keys.stride + ch * 16;
+            const uint64_t src = (sl.at[i] >= 0 && ch * 8 < D) ? at : reinterpret_cast<uint64_t>(kZeroChunk);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, to, 16, 0, 0);
         } else {
             const uint32_t off = ch * 8 < D ? static_cast<uint32_t>(lrow * s.stride + ch * 16) : 0x80000000u;
@@ -436,6 +443,7 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
                                               uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
     using W = Walk<C, Keys>;
     using Source = typename W::Source;
+    using Slots = typename W::Slots;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n_stages = (k1 - k0 + 63) / 64;
     const int row0 = wave * C::R;                                 // rows of a stage this wave loads
@@ -450,11 +458,6 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     };
     int slot = n_stages > 0 ? entry(0) : 0;
     W w(keys, klim, D, c, st, q != nullptr);
-    auto source = [&](auto V, int s) __attribute__((always_inline)) -> Source {
-        constexpr bool v = decltype(V)::value;
-        if constexpr (W::PAGED) return w.template paged_rows<v>(slot, row0);
-        else return w.template packed_rows<v>(k0 + s * 64 + row0, k1);
-    };
     auto valid = [&](int sl) __attribute__((always_inline)) -> uint64_t {
         if constexpr (W::PAGED) return __ballot(sl >= 0);
         else return ~uint64_t(0);
@@ -466,11 +469,12 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     if (n_stages > 0) w.template stage_q<32 / C::RPI>(q, qt, 0);
     uint64_t vcur = valid(slot);
     if (n_stages > 0) {
-        const Source k = source(std::false_type{}, 0), v = source(std::true_type{}, 0);
+        const Source k = w.template source<false>(k0 + row0, k1), v = w.template source<true>(k0 + row0, k1);
+        const Slots sl = w.slots_of(slot, row0);
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb0 + row0 * C::RB, row0, i);
+        for (int i = 0; i < C::NI; ++i) w.template load<false>(k, sl, kb0 + row0 * C::RB, row0, i);
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) w.template load<true>(v, vb0 + row0 * C::RB, row0, i);
+        for (int i = 0; i < C::NI; ++i) w.template load<true>(v, sl, vb0 + row0 * C::RB, row0, i);
     }
     if (n_stages <= 0) return;
     wait_here<wait_vm(2 * C::NI)>();
@@ -493,10 +497,12 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         const int key0 = k0 + s * 64;
         // the next stage's loads (past the last stage: zeros) go out among
         // this one's scores and, with one sub-tile per stage, its weights
-        const Source k = source(std::false_type{}, s + 1), v = source(std::true_type{}, s + 1);
+        const Source k = w.template source<false>(key0 + 64 + row0, k1), v = w.template source<true>(key0 + 64 + row0, k1);
+        const Slots sl = w.slots_of(slot, row0);
+        if constexpr (W::PAGED) __builtin_amdgcn_sched_barrier(0);   // the exchanges together, not one wait among the products each
         const uint64_t vnext = valid(slot);
-        auto load_k = [&](int i) __attribute__((always_inline)) { w.template load<false>(k, kn + row0 * C::RB, row0, i); };
-        auto load_v = [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vn + row0 * C::RB, row0, i); };
+        auto load_k = [&](int i) __attribute__((always_inline)) { w.template load<false>(k, sl, kn + row0 * C::RB, row0, i); };
+        auto load_v = [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vn + row0 * C::RB, row0, i); };
         if constexpr (C::KW == 1) {
             sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur), load_k, [](int) {});
             sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32), load_v, [](int) {});
@@ -528,6 +534,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
                                            uint8_t* kb_all, uint8_t* vb_all, State<C>& st) {
     using W = Walk<C, Keys>;
     using Source = typename W::Source;
+    using Slots = typename W::Slots;
     constexpr bool PAGED = W::PAGED;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     uint8_t* const kb = kb_all + wave * 32 * C::RB;
@@ -544,17 +551,14 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
     };
     int slot = n > 0 ? entry(0) : 0;
     W w(keys, klim, D, c, st, q != nullptr);
-    auto source = [&](auto V, int t, int sl) __attribute__((always_inline)) -> Source {
-        constexpr bool v = decltype(V)::value;
-        if constexpr (PAGED) return w.template paged_rows<v>(sl, 0);
-        else return w.template packed_rows<v>(first + t * 128, k1);
-    };
     // the query rows come through the place of wave 0's V, eight from each wave
     w.template stage_q<8 / C::RPI>(q, vb_all, wave * 8);
+    Slots sl = {};
     if (n > 0) {
-        const Source k = source(std::false_type{}, 0, slot);
+        const Source k = w.template source<false>(first, k1);
+        sl = w.slots_of(slot, 0);
 #pragma unroll
-        for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb, 0, i);
+        for (int i = 0; i < C::NI; ++i) w.template load<false>(k, sl, kb, 0, i);
         wait_here<wait_vm(C::NI)>();
     } else {
         wait_here<wait_vm(0)>();
@@ -571,15 +575,16 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
         const int key0 = first + t * 128;
         const bool more = t + 1 < n;
         wait_here<wait_vm(0)>();                                  // K(t), and the entry of t + 1
-        const Source v = source(std::true_type{}, t, slot);
-        f32x16_t sc = w.template scores<C::NI>(kb, [&](int i) __attribute__((always_inline)) { w.template load<true>(v, vb, 0, i); });
+        const Source v = w.template source<true>(key0, k1);
+        f32x16_t sc = w.template scores<C::NI>(kb, [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vb, 0, i); });
         const uint32_t vm = PAGED ? static_cast<uint32_t>(__ballot(slot >= 0)) : 0xFFFFFFFFu;
         wait_here<kWaitLds>();                                    // K(t) has been read
         if (more) {
             slot = next;
-            const Source k = source(std::false_type{}, t + 1, slot);
+            const Source k = w.template source<false>(key0 + 128, k1);
+            sl = w.slots_of(slot, 0);
 #pragma unroll
-            for (int i = 0; i < C::NI; ++i) w.template load<false>(k, kb, 0, i);
+            for (int i = 0; i < C::NI; ++i) w.template load<false>(k, sl, kb, 0, i);
             next = t + 2 < n ? entry(t + 2) : -1;
         }
         w.scale_and_mask(sc, key0, vm);
@@ -650,62 +655,47 @@ __device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, floa
         }
     }
     __syncthreads();
-    // the KW waves of a group write its 32 rows: RPW of them per wave and
-    // instruction, 8 channels per lane
-    constexpr int GROUPS = C::DP / 8;
-    constexpr int ITEMS = 32 * GROUPS / (64 * C::KW);
+    // the KW waves of a group write its 32 rows, 8 channels per lane.  Many
+    // passes stay a loop: code that runs once per workgroup waits for its
+    // instructions, about 5 cycles each.
+    constexpr int GROUPS = C::DP / 8, RPW = 64 / GROUPS;          // rows per wave and pass
     const int q = wave % QW, cg = lane % GROUPS;
-    int row[ITEMS];
-    uint64_t dst[ITEMS];
-    float m[ITEMS], l[ITEMS], f[ITEMS][C::KW];
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-        row[it] = (it * C::KW + wave / QW) * (64 / GROUPS) + lane / GROUPS;
-        dst[it] = row_at[q][row[it]];
-        float mk[C::KW], lk[C::KW];
+    constexpr int PASSES = 32 / (C::KW * RPW), UNROLL = C::KW == 4 ? PASSES : 2;
+#pragma unroll UNROLL
+    for (int pass = 0; pass < PASSES; ++pass) {
+        const int row = (pass * C::KW + wave / QW) * RPW + lane / GROUPS;
+        const uint64_t dst = row_at[q][row];
+        float mk[C::KW], m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
         for (int k = 0; k < C::KW; ++k) {
-            mk[k] = ml[q + k * QW][0][row[it]];
-            lk[k] = ml[q + k * QW][1][row[it]];
+            mk[k] = ml[q + k * QW][0][row];
+            m = fmaxf(m, mk[k]);
         }
-        m[it] = mk[0];
-#pragma unroll
-        for (int k = 1; k < C::KW; ++k) m[it] = fmaxf(m[it], mk[k]);
-        l[it] = 0.0f;
+        f32x4_t o[2] = {f32x4_t{}, f32x4_t{}};
 #pragma unroll
         for (int k = 0; k < C::KW; ++k) {
-            f[it][k] = mk[k] == m[it] ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - m[it]);
-            l[it] += lk[k] * f[it][k];
+            const float f = mk[k] == m ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - m);
+            l += ml[q + k * QW][1][row] * f;
+            if (k < with_keys) {
+                const uint8_t* const a = area(q + k * QW) + row * ROW;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    o[x] += *reinterpret_cast<const f32x4_t*>(a + (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16) * f;
+            }
         }
-    }
-    f32x4_t o[ITEMS][2];
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) o[it][0] = o[it][1] = f32x4_t{};
-#pragma unroll
-    for (int k = 0; k < C::KW; ++k) {
-        if (k >= with_keys) break;
-        const uint8_t* const a = area(q + k * QW);
-#pragma unroll
-        for (int it = 0; it < ITEMS; ++it)
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                o[it][x] += *reinterpret_cast<const f32x4_t*>(a + row[it] * ROW + (((2 * cg + x) ^ row[it]) & (C::DP / 4 - 1)) * 16) * f[it][k];
-    }
-#pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-        if (dst[it] == 0 || cg * 8 >= D) continue;
+        if (dst == 0 || cg * 8 >= D) continue;
         if constexpr (PART) {
-            const int64_t at = static_cast<int64_t>(dst[it] - 1);
-            if (cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m[it], l[it]);
-            if (m[it] == -__builtin_inff()) continue;
+            const int64_t at = static_cast<int64_t>(dst - 1);
+            if (cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m, l);
+            if (m == -__builtin_inff()) continue;
             f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at * D + cg * 8);
-            p[0] = o[it][0];
-            p[1] = o[it][1];
+            p[0] = o[0];
+            p[1] = o[1];
         } else {
-            const float inv = l[it] > 0.0f ? 1.0f / l[it] : (l[it] == 0.0f ? 0.0f : l[it]);   // NaN stays NaN
-            const f32x4_t x = o[it][0] * inv, y = o[it][1] * inv;
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
+            const f32x4_t x = o[0] * inv, y = o[1] * inv;
             const u32x4_t w = {f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w), f32x2_to_bf16x2(y.x, y.y), f32x2_to_bf16x2(y.z, y.w)};
-            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst[it]) + cg * 8) = w;
+            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
         }
     }
 }
@@ -972,9 +962,11 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
                             int64_t suffix_cap) {
     SharedPlan p{};
     const int64_t G = Hq / Hkv, rows_s = L * G, rows_p = B * rows_s;
-    // workgroups that run at once
-    const int64_t slots = D <= 128 ? 2 * kComputeUnits : kComputeUnits;
-    auto tile = [](int64_t rows) { return rows > 64 ? 128 : (rows > 32 ? 64 : 32); };
+    // Narrow tiles for up to 256 rows per key/value head: each wave streams
+    // keys of its own and fewer splits fill the GPU, so less is joined (64
+    // sequences behind 8195 keys, 32 heads on 8 of 128: 42 us against 50 with
+    // 128-row tiles; 80 rows over 778 keys, 256 channels: 14 against 18).
+    auto tile = [](int64_t rows) { return rows > 256 ? 128 : 32; };
     p.prefix_tm = tile(rows_p);
     p.suffix_tm = tile(rows_s);
     // A sequence whose rows fill its tiles reads the prefix no more often by
@@ -987,10 +979,10 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     const int64_t steps_s = ceil_div(keys_s, step_keys(p.suffix_tm));
     const int64_t tiles_p = p.merged ? 0 : ceil_div(rows_p, p.prefix_tm);
     p.suffix_tiles = ceil_div(rows_s, p.suffix_tm);
-    // keys are split until the workgroups fill the slots once
+    // keys are split until the workgroups fill the compute units once
     auto splits = [&](int64_t tiles, int64_t steps) {
         if (tiles == 0 || steps == 0) return int64_t(0);
-        const int64_t per = ceil_div(tiles * steps, slots);
+        const int64_t per = ceil_div(tiles * steps, kComputeUnits);
         return ceil_div(steps, per);
     };
     p.prefix_splits = splits(Hkv * tiles_p, steps_p);
