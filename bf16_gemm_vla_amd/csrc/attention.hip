@@ -47,6 +47,7 @@ typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 
 constexpr int kAThreads = 256;
 constexpr float kLag = 8.0f;                     // log2 of the largest weight, see weights()
+constexpr uint32_t kNoOffset = 0xFFFFF000u;      // a buffer offset past every cache that takes 32-bit ones
 constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data format
 
 __device__ __attribute__((aligned(16))) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
@@ -91,20 +92,27 @@ struct PackedKeys {
     int k_stride, v_stride;    // bytes
     int n;
 };
+template <bool WIDE_>
 struct PagedKeys {
+    static constexpr bool WIDE = WIDE_;   // byte offsets past 32 bits
     const uint16_t *k, *v;     // slot 0 of this head
+    uint32_t bytes;            // to the end of the last slot's D channels (not WIDE)
     uint32_t stride;           // bytes
     const int32_t *prefix, *suffix;
     int n_prefix, n;           // prefix keys, all keys
     int page_log2;
     uint32_t num_pages;
-    // slot of key j, or -1 where its page does not exist
-    __device__ __forceinline__ int slot(int key) const {
+    // A key's slot in two steps, so that the table is read well before its
+    // entry is needed: the entry (of key 0 <= key < n), then the slot, -1
+    // where the page does not exist.
+    __device__ __forceinline__ int32_t entry(int key) const {
         const bool pre = key < n_prefix;
-        const int j = pre ? key : key - n_prefix;
-        const uint32_t page = static_cast<uint32_t>((pre ? prefix : suffix)[j >> page_log2]);
-        const int at = static_cast<int>((page << page_log2) | (j & ((1 << page_log2) - 1)));
-        return page < num_pages ? at : -1;
+        return (pre ? prefix : suffix)[(pre ? key : key - n_prefix) >> page_log2];
+    }
+    __device__ __forceinline__ int slot(int key, int32_t page) const {
+        const int j = key < n_prefix ? key : key - n_prefix;
+        const int at = static_cast<int>((static_cast<uint32_t>(page) << page_log2) | (j & ((1 << page_log2) - 1)));
+        return static_cast<uint32_t>(page) < num_pages ? at : -1;
     }
 };
 
@@ -146,7 +154,7 @@ __device__ __forceinline__ bool has_nonfinite(const uint8_t* v) {
 // What one wave needs to walk keys for its 32 rows.
 template <class C, class Keys>
 struct Walk {
-    static constexpr bool PAGED = std::is_same<Keys, PagedKeys>::value;
+    static constexpr bool PAGED = !std::is_same<Keys, PackedKeys>::value;
     const Keys& keys;
     int klim;                  // the lane's row sees keys below this
     int kfull, kmax;           // every row sees keys below kfull, none one at or past kmax
@@ -214,20 +222,22 @@ struct Walk {
     //      time.  row0: the rows' place in the buffer modulo 32 (for the
     //      swizzle); Source holds what is common to the instructions.
     struct Source {
-        __amdgpu_buffer_rsrc_t rs;   // packed: a buffer that ends with the last key, rows past it load zeros
+        __amdgpu_buffer_rsrc_t rs;   // packed: ends with the last key, rows past it load zeros; paged: the cache
         int stride;
     };
-    // Paged: the slots of the rows that this lane loads, taken from the lanes
-    // that read the table (lane l: window key l); from: the window row of
-    // instruction 0.
+    // Paged: the rows that this lane loads, taken from the lanes that read the
+    // table (lane l: window key l; from: the window row of instruction 0).
+    // Byte offsets in the cache, past its end where there is no row; WIDE: slots.
     struct Slots {
-        int at[PAGED ? C::NI : 1];
+        uint32_t at[PAGED ? C::NI : 1];
     };
     __device__ __forceinline__ Slots slots_of(int slot, int from) const {
         Slots s;
         if constexpr (PAGED) {
+            int mine = slot;
+            if constexpr (!Keys::WIDE) mine = static_cast<int>(slot >= 0 ? static_cast<uint32_t>(slot) * keys.stride : kNoOffset);
 #pragma unroll
-            for (int i = 0; i < C::NI; ++i) s.at[i] = __shfl(slot, from + i * C::RPI + lrow, 64);
+            for (int i = 0; i < C::NI; ++i) s.at[i] = static_cast<uint32_t>(__shfl(mine, from + i * C::RPI + lrow, 64));
         }
         return s;
     }
@@ -240,6 +250,8 @@ struct Walk {
             s.rs = __builtin_amdgcn_make_buffer_rsrc(
                 const_cast<uint8_t*>(reinterpret_cast<const uint8_t*>(V ? keys.v : keys.k) + static_cast<int64_t>(key0) * s.stride), 0,
                 left > 0 ? (left - 1) * s.stride + D * 2 : 0, kBufferWord3);
+        } else if constexpr (!Keys::WIDE) {
+            s.rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(V ? keys.v : keys.k), 0, keys.bytes, kBufferWord3);
         }
         return s;
     }
@@ -248,14 +260,15 @@ struct Walk {
         const int row = row0 + i * C::RPI + lrow;
         const int ch = lpos ^ (V ? swz_v<C::DP>(row) : swz_k<C::DP>(row));
         __attribute__((address_space(3))) void* const to = (__attribute__((address_space(3))) void*)(dst + i * 1024);
-        if constexpr (PAGED) {
-            const uint64_t at = reinterpret_cast<uint64_t>(V ? keys.v : keys.k) +
-                                static_cast<uint64_t>(static_cast<uint32_t>(sl.at[i])) * keys.stride + ch * 16;
-            const uint64_t src = (sl.at[i] >= 0 && ch * 8 < D) ? at : reinterpret_cast<uint64_t>(kZeroChunk);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, to, 16, 0, 0);
-        } else {
+        if constexpr (!PAGED) {
             const uint32_t off = ch * 8 < D ? static_cast<uint32_t>(lrow * s.stride + ch * 16) : 0x80000000u;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rs, to, 16, off, i * C::RPI * s.stride, 0, 0);
+        } else if constexpr (!Keys::WIDE) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(s.rs, to, 16, ch * 8 < D ? sl.at[i] + ch * 16 : kNoOffset, 0, 0, 0);
+        } else {
+            const uint64_t at = reinterpret_cast<uint64_t>(V ? keys.v : keys.k) + static_cast<uint64_t>(sl.at[i]) * keys.stride + ch * 16;
+            const uint64_t src = (static_cast<int>(sl.at[i]) >= 0 && ch * 8 < D) ? at : reinterpret_cast<uint64_t>(kZeroChunk);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src, to, 16, 0, 0);
         }
     }
 
@@ -391,7 +404,7 @@ struct Walk {
             if (key0 < 0 || key0 + 32 <= kfull || !((st.late >> ((key0 + 32 - kfull) >> 5)) & 1u)) continue;
             const uint16_t *kr, *vr;
             if constexpr (PAGED) {
-                const int sl = keys.slot(key);
+                const int sl = keys.slot(key, keys.entry(key));
                 if (sl < 0) continue;
                 const int64_t at = static_cast<int64_t>(sl) * (keys.stride / 2);
                 kr = keys.k + at;
@@ -447,16 +460,18 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n_stages = (k1 - k0 + 63) / 64;
     const int row0 = wave * C::R;                                 // rows of a stage this wave loads
-    // the lane's key of a stage: its slot, for the loads and the masks
-    auto entry = [&](int s) __attribute__((always_inline)) -> int {
-        if constexpr (W::PAGED) {
-            const int key = k0 + s * 64 + (threadIdx.x & 63);
-            return key < k1 ? keys.slot(key) : -1;
-        } else {
-            return 0;
-        }
+    // the lane's key of a stage: its table entry (of the last key past the
+    // range), then its slot, for the loads and the masks
+    auto entry = [&](int s) __attribute__((always_inline)) -> int32_t {
+        if constexpr (W::PAGED) return keys.entry(min(k0 + s * 64 + static_cast<int>(threadIdx.x & 63), k1 - 1));
+        else return 0;
     };
-    int slot = n_stages > 0 ? entry(0) : 0;
+    auto slot_of = [&](int s, int32_t page) __attribute__((always_inline)) -> int {
+        const int key = k0 + s * 64 + (threadIdx.x & 63);
+        if constexpr (W::PAGED) return key < k1 ? keys.slot(key, page) : -1;
+        else return 0;
+    };
+    int32_t page = n_stages > 0 ? entry(0) : 0;
     W w(keys, klim, D, c, st, q != nullptr);
     auto valid = [&](int sl) __attribute__((always_inline)) -> uint64_t {
         if constexpr (W::PAGED) return __ballot(sl >= 0);
@@ -467,6 +482,7 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     // query rows come through the buffers of stage 1.
     uint8_t* const qt = (wave < 2 ? kb1 : vb1) + (wave & 1) * 32 * C::RB;
     if (n_stages > 0) w.template stage_q<32 / C::RPI>(q, qt, 0);
+    int slot = n_stages > 0 ? slot_of(0, page) : -1;
     uint64_t vcur = valid(slot);
     if (n_stages > 0) {
         const Source k = w.template source<false>(k0 + row0, k1), v = w.template source<true>(k0 + row0, k1);
@@ -479,7 +495,7 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     if (n_stages <= 0) return;
     wait_here<wait_vm(2 * C::NI)>();
     w.read_q(qt);
-    slot = n_stages > 1 ? entry(1) : -1;
+    page = entry(1);
     auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& load_one, auto&& load_more) __attribute__((always_inline)) {
         f32x16_t sc = w.template scores<C::NI>(kt, load_one);
         w.scale_and_mask(sc, key0, vm);
@@ -498,9 +514,11 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         // the next stage's loads (past the last stage: zeros) go out among
         // this one's scores and, with one sub-tile per stage, its weights
         const Source k = w.template source<false>(key0 + 64 + row0, k1), v = w.template source<true>(key0 + 64 + row0, k1);
+        slot = slot_of(s + 1, page);
         const Slots sl = w.slots_of(slot, row0);
         if constexpr (W::PAGED) __builtin_amdgcn_sched_barrier(0);   // the exchanges together, not one wait among the products each
         const uint64_t vnext = valid(slot);
+        page = entry(s + 2);
         auto load_k = [&](int i) __attribute__((always_inline)) { w.template load<false>(k, sl, kn + row0 * C::RB, row0, i); };
         auto load_v = [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vn + row0 * C::RB, row0, i); };
         if constexpr (C::KW == 1) {
@@ -512,7 +530,6 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
                      load_k, load_v);
         }
         vcur = vnext;
-        slot = s + 2 < n_stages ? entry(s + 2) : -1;
     };
     for (int s = 0; s < n_stages; s += 2) {
         step(kb0, vb0, kb1, vb1, s);
@@ -541,21 +558,24 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
     uint8_t* const vb = vb_all + wave * 32 * C::RB;
     const int first = k0 + wave * 32;
     const int n = k1 > first ? (k1 - first + 127) / 128 : 0;
-    auto entry = [&](int t) __attribute__((always_inline)) -> int {
-        if constexpr (PAGED) {
-            const int key = first + t * 128 + (threadIdx.x & 31);
-            return key < k1 ? keys.slot(key) : -1;
-        } else {
-            return 0;
-        }
+    auto entry = [&](int t) __attribute__((always_inline)) -> int32_t {
+        if constexpr (PAGED) return keys.entry(min(first + t * 128 + static_cast<int>(threadIdx.x & 31), k1 - 1));
+        else return 0;
     };
-    int slot = n > 0 ? entry(0) : 0;
+    auto slot_of = [&](int t, int32_t page) __attribute__((always_inline)) -> int {
+        const int key = first + t * 128 + (threadIdx.x & 31);
+        if constexpr (PAGED) return key < k1 ? keys.slot(key, page) : -1;
+        else return 0;
+    };
+    int32_t page = n > 0 ? entry(0) : 0;
     W w(keys, klim, D, c, st, q != nullptr);
     // the query rows come through the place of wave 0's V, eight from each wave
     w.template stage_q<8 / C::RPI>(q, vb_all, wave * 8);
     Slots sl = {};
+    int slot = -1;
     if (n > 0) {
         const Source k = w.template source<false>(first, k1);
+        slot = slot_of(0, page);
         sl = w.slots_of(slot, 0);
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) w.template load<false>(k, sl, kb, 0, i);
@@ -570,7 +590,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     if (n <= 0) return;
-    int next = n > 1 ? entry(1) : -1;
+    page = entry(1);
     for (int t = 0; t < n; ++t) {
         const int key0 = first + t * 128;
         const bool more = t + 1 < n;
@@ -580,12 +600,12 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
         const uint32_t vm = PAGED ? static_cast<uint32_t>(__ballot(slot >= 0)) : 0xFFFFFFFFu;
         wait_here<kWaitLds>();                                    // K(t) has been read
         if (more) {
-            slot = next;
+            slot = slot_of(t + 1, page);
             const Source k = w.template source<false>(key0 + 128, k1);
             sl = w.slots_of(slot, 0);
 #pragma unroll
             for (int i = 0; i < C::NI; ++i) w.template load<false>(k, sl, kb, 0, i);
-            next = t + 2 < n ? entry(t + 2) : -1;
+            page = entry(t + 2);
         }
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
@@ -683,19 +703,20 @@ __device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, floa
                     o[x] += *reinterpret_cast<const f32x4_t*>(a + (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16) * f;
             }
         }
-        if (dst == 0 || cg * 8 >= D) continue;
+        const bool store = dst != 0 && cg * 8 < D;
         if constexpr (PART) {
             const int64_t at = static_cast<int64_t>(dst - 1);
-            if (cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m, l);
-            if (m == -__builtin_inff()) continue;
-            f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at * D + cg * 8);
-            p[0] = o[0];
-            p[1] = o[1];
+            if (store && cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m, l);
+            if (store && m != -__builtin_inff()) {
+                f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at * D + cg * 8);
+                p[0] = o[0];
+                p[1] = o[1];
+            }
         } else {
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
             const f32x4_t x = o[0] * inv, y = o[1] * inv;
             const u32x4_t w = {f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w), f32x2_to_bf16x2(y.x, y.y), f32x2_to_bf16x2(y.z, y.w)};
-            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
+            if (store) *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
         }
     }
 }
@@ -806,7 +827,7 @@ void attn_prompt_kernel(PromptArgs a) {
 // split of the shared prefix (rows of the whole batch) or of one sequence's
 // suffix.  With one sequence both are one range of keys.  More than one part
 // per row: the parts' unnormalised O, maximum and sum go to the workspace.
-template <class C>
+template <class C, bool WIDE>
 __global__ __launch_bounds__(kAThreads) __attribute__((amdgpu_waves_per_eu(C::WAVES, C::WAVES)))
 void attn_shared_kernel(SharedArgs a) {
     ATTN_LDS;
@@ -825,8 +846,9 @@ void attn_shared_kernel(SharedArgs a) {
     const int np = a.prefix_pages ? min(max(a.prefix_len[0], 0), a.prefix_cap) : 0;
     int ns = 0;
     if (!prefix && a.block_table) ns = min(max(a.seq_lens[b], 0), a.suffix_cap);
-    PagedKeys keys;
+    PagedKeys<WIDE> keys;
     keys.stride = static_cast<uint32_t>(a.Hkv * a.D * 2);
+    keys.bytes = static_cast<uint32_t>(((static_cast<uint64_t>(a.num_pages) << a.page_log2) - 1) * keys.stride + a.D * 2);
     keys.k = a.k_cache + static_cast<int64_t>(hk) * a.D;
     keys.v = a.v_cache + static_cast<int64_t>(hk) * a.D;
     keys.prefix = a.prefix_pages;
@@ -1005,12 +1027,17 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
     a.part_ml = reinterpret_cast<float*>(w);
     a.part_o = reinterpret_cast<float*>(w + p.ml_bytes);
+    const bool wide = (static_cast<uint64_t>(a.num_pages) << a.page_log2) * a.Hkv * a.D * 2 > kNoOffset;
     auto run = [&](int tm, int64_t prefix_items, int64_t suffix_items) {
         a.prefix_items = static_cast<int>(prefix_items);
         const int grid = static_cast<int>(prefix_items + suffix_items);
         if (grid == 0) return hipSuccess;
         return by_size(a.D, tm, [&](auto cfg) {
-            attn_shared_kernel<decltype(cfg)><<<grid, kAThreads, 0, s>>>(a);
+            // caches below 4 GiB take one 32-bit offset per row and load, where
+            // 64-bit addresses with a select for missing rows took five
+            // instructions more each
+            if (wide) attn_shared_kernel<decltype(cfg), true><<<grid, kAThreads, 0, s>>>(a);
+            else attn_shared_kernel<decltype(cfg), false><<<grid, kAThreads, 0, s>>>(a);
             return hipGetLastError();
         });
     };
