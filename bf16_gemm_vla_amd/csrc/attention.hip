@@ -139,11 +139,11 @@ __device__ __forceinline__ float half_sum(float x) {
 // all of them are looked at).
 template <class C>
 __device__ __forceinline__ bool has_nonfinite(const uint8_t* v) {
-    v += (threadIdx.x & 63) * 16;
+    const int lane16 = (threadIdx.x & 63) * 16;
     uint32_t top = 0;
 #pragma unroll 4
     for (int i = 0; i < 32 * C::RB / 1024; ++i) {
-        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + i * 1024);
+        const u32x4_t w = *reinterpret_cast<const u32x4_t*>(v + (lane16 + i * 1024));
         // an exponent of all ones plus one carries into the sign's place
 #pragma unroll
         for (int j = 0; j < 4; ++j) top |= (w[j] & 0x7F807F80u) + 0x00800080u;
@@ -161,7 +161,7 @@ struct Walk {
     int D;
     float c;                   // scale * log2(e)
     int l32, g2;
-    int kaddr, vaddr, vswz;    // LDS operand addresses within 32 rows
+    int kaddr, vaddr[C::ND < 4 ? C::ND : 4];   // LDS operand addresses within 32 rows
     int lrow, lpos;            // row and chunk position this lane loads, within one instruction
     bf16x8_t qf[C::NK];
     State<C>& st;
@@ -190,8 +190,9 @@ struct Walk {
         kaddr = l32 * C::RB + ((swz_k<C::DP>(l32) ^ g2) << 4);
         // transpose read: key 4 g2 + i16/4 of an 8-key group, channels 16 g16 + 4 (i16 % 4)
         const int i16 = lane & 15, g16 = (lane >> 4) & 1;
-        vswz = swz_v<C::DP>(i16 >> 2);
-        vaddr = (4 * g2 + (i16 >> 2)) * C::RB + (2 * g16 + ((i16 & 3) >> 1)) * 16 + (i16 & 1) * 8;
+        const int v0 = (4 * g2 + (i16 >> 2)) * C::RB + (2 * g16 + ((i16 & 3) >> 1)) * 16 + (i16 & 1) * 8;
+#pragma unroll
+        for (int d = 0; d < (C::ND < 4 ? C::ND : 4); ++d) vaddr[d] = v0 + ((d * 4) ^ swz_v<C::DP>(i16 >> 2)) * 16;
         lrow = lane / C::CH;
         lpos = lane % C::CH;
     }
@@ -210,6 +211,18 @@ struct Walk {
             const uint64_t src = (p != 0 && ch * 8 < D) ? p + ch * 16 : reinterpret_cast<uint64_t>(kZeroChunk);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                              (__attribute__((address_space(3))) void*)(dst + (r0 + i * C::RPI) * C::RB), 16, 0, 0);
+        }
+    }
+    // Operand addresses from the buffers' starts, `first` bytes on.  They are
+    // made opaque: the compiler follows an address to its LDS object over a few
+    // steps only, and before a read of an object it does not know it waits for
+    // every load into LDS, the next keys' among them.
+    __device__ __forceinline__ void address(int first) {
+        kaddr += first;
+#pragma unroll
+        for (int d = 0; d < (C::ND < 4 ? C::ND : 4); ++d) {
+            vaddr[d] += first;
+            asm volatile("" : "+v"(vaddr[d]));
         }
     }
     // query fragments: B operand, lane = row l32, channels 16 kk + 8 g2 .. +7
@@ -357,9 +370,9 @@ struct Walk {
     }
     // V^T fragments: 16 keys (step k2) x 32 channels (block d)
     __device__ __forceinline__ bf16x8_t v_frag(const uint8_t* vt, int k2, int d) const {
-        const uint8_t* va = vt + vaddr + ((d * 4) ^ vswz) * 16 + 16 * k2 * C::RB;
-        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)va);
-        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(va + 8 * C::RB));
+        const int at = vaddr[d & 3] + (d >> 2) * 256 + 16 * k2 * C::RB;
+        const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(vt + at));
+        const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)(vt + (at + 8 * C::RB)));
         const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
         const u32x4_t vf = {a.x, a.y, b.x, b.y};
         return as_bf16x8(vf);
@@ -495,6 +508,7 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     if (n_stages <= 0) return;
     wait_here<wait_vm(2 * C::NI)>();
     w.read_q(qt);
+    w.address(0);
     page = entry(1);
     auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& load_one, auto&& load_more) __attribute__((always_inline)) {
         f32x16_t sc = w.template scores<C::NI>(kt, load_one);
@@ -586,6 +600,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     w.read_q(vb_all);
+    w.address(wave * 32 * C::RB);
     wait_here<kWaitLds>();
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -596,7 +611,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
         const bool more = t + 1 < n;
         wait_here<wait_vm(0)>();                                  // K(t), and the entry of t + 1
         const Source v = w.template source<true>(key0, k1);
-        f32x16_t sc = w.template scores<C::NI>(kb, [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vb, 0, i); });
+        f32x16_t sc = w.template scores<C::NI>(kb_all, [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vb, 0, i); });
         const uint32_t vm = PAGED ? static_cast<uint32_t>(__ballot(slot >= 0)) : 0xFFFFFFFFu;
         wait_here<kWaitLds>();                                    // K(t) has been read
         if (more) {
@@ -612,7 +627,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
         w.template weights<0>(sc, pw, [](int) {});
         if (more) wait_here<wait_vm(C::NI)>();                    // V(t); K(t+1) may be on its way
         else wait_here<wait_vm(0)>();
-        if (!w.put_off(vb, key0)) w.add(vb, pw);
+        if (!w.put_off(vb, key0)) w.add(vb_all, pw);
         wait_here<kWaitLds>();                                    // V(t) has been read
     }
     st.l = half_sum(st.l);
