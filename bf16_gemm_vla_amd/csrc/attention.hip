@@ -52,31 +52,51 @@ constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data for
 
 __device__ __attribute__((aligned(16))) const uint32_t kZeroChunk[4] = {0, 0, 0, 0};
 
-// KW: waves that share 32 query rows, each with keys of its own; 4 / KW such
-// groups make the workgroup's tile.
-//   KW 1 (128 rows), KW 2 (64 rows): all four waves load and share stages of
-//     64 keys; a wave takes both 32-key sub-tiles, or one of them.
-//   KW 4 (32 rows): each wave walks every fourth 32-key sub-tile through LDS
-//     of its own, so that no wave waits for another before the end.
-template <int DP_, int KW_>
+// How a workgroup's four waves share its work: QG groups of 32 query rows x HV
+// parts of the output channels x KG parts of the keys.
+//   Up to 128 channels, 128 rows (QG 4) and 64 rows (QG 2, KG 2): all waves
+//     load and share stages of 64 keys; a wave takes both 32-key sub-tiles of a
+//     stage, or one of them.
+//   Up to 128 channels, 32 rows (KG 4): each wave walks every fourth 32-key
+//     sub-tile through LDS of its own, so that no wave waits for another
+//     before the end.
+//   256 channels, 64 rows (QG 2, HV 2) and 32 rows (HV 2, KG 2): shared stages
+//     of one sub-tile per key part.  32 rows of queries and output of 256
+//     channels would leave a SIMD one wave; with half of the output channels a
+//     wave fits 256 registers, at the price of forming its scores twice.
+template <int DP_, int TM_>
 struct ACfg {
-    static constexpr int DP = DP_, KW = KW_;
-    static constexpr bool SHARE = KW < 4;                    // stages shared by all waves
-    static constexpr int WAVES = DP <= 128 ? 2 : 1;          // per SIMD: 256 or 512 registers each
-    static constexpr int TM = 32 * (4 / KW);                 // query rows per workgroup
-    static constexpr int ST = SHARE ? 64 : 128;              // keys per workgroup step
+    static constexpr int DP = DP_, TM = TM_;                 // padded channels, query rows per workgroup
+    static constexpr int QG = TM / 32, HV = DP > 128 && TM < 64 ? 2 : 1, KG = 4 / (QG * HV);
+    static_assert(QG * HV * KG == 4, "four waves");
+    static constexpr bool SHARE = KG < 4;                    // stages shared by all waves
+    static constexpr int SUBS = SHARE && QG == 4 ? 2 : 1;    // sub-tiles per wave and stage
+    static constexpr int ST = 32 * KG * SUBS;                // keys per workgroup step
     static constexpr int CH = DP / 8;                        // 16-byte chunks per row
     static constexpr int RB = DP * 2;                        // bytes per row
-    static constexpr int R = SHARE ? 16 : 32;                // rows of K (and V) a wave loads at once
+    static constexpr int R = SHARE ? ST / 4 : 32;            // rows of K (and V) a wave loads at once
     static constexpr int RPI = 1024 / RB;                    // rows per load instruction
     static constexpr int NI = R / RPI;                       // load instructions for R rows
     static constexpr int NK = DP / 16;                       // MFMA steps of K Q^T
-    static constexpr int ND = DP / 32;                       // 32-channel blocks of O^T
+    static constexpr int ND = DP / 32 / HV;                  // 32-channel blocks of O^T per wave
     // LDS buffers: K and V of two shared stages, or of one sub-tile per wave,
     // each an object of its own: the compiler orders LDS reads after the
     // loads that write the same object
-    static constexpr int BUF = (SHARE ? 64 : 128) * RB;
+    static constexpr int BUF = ST * RB;
+    static constexpr int WAVES = (SHARE ? 4 : 2) * BUF > 80 * 1024 ? 1 : 2;   // workgroups per compute unit
     static_assert(R % RPI == 0, "whole load instructions");
+};
+
+// The calling wave's parts.
+template <class C>
+struct Part {
+    int wave, qg, kg, hv;
+    __device__ __forceinline__ Part() {
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        qg = wave % C::QG;
+        kg = wave / C::QG % C::KG;
+        hv = wave / (C::QG * C::KG);
+    }
 };
 
 // Position of a row's 16-byte chunks in LDS: chunk ^ swizzle.
@@ -161,7 +181,10 @@ struct Walk {
     int D;
     float c;                   // scale * log2(e)
     int l32, g2;
-    int kaddr, vaddr[C::ND < 4 ? C::ND : 4];   // LDS operand addresses within 32 rows
+    // the swizzle of V works within 128 channels; the next 128 are 256 bytes on
+    static constexpr int NV = C::ND < 4 ? C::ND : 4;
+    int kaddr, vaddr[NV];      // LDS operand addresses within 32 rows
+    int ch0;                   // first of the wave's output channels
     int lrow, lpos;            // row and chunk position this lane loads, within one instruction
     bf16x8_t qf[C::NK];
     State<C>& st;
@@ -192,7 +215,7 @@ struct Walk {
         const int i16 = lane & 15, g16 = (lane >> 4) & 1;
         const int v0 = (4 * g2 + (i16 >> 2)) * C::RB + (2 * g16 + ((i16 & 3) >> 1)) * 16 + (i16 & 1) * 8;
 #pragma unroll
-        for (int d = 0; d < (C::ND < 4 ? C::ND : 4); ++d) vaddr[d] = v0 + ((d * 4) ^ swz_v<C::DP>(i16 >> 2)) * 16;
+        for (int d = 0; d < NV; ++d) vaddr[d] = v0 + ((d * 4) ^ swz_v<C::DP>(i16 >> 2)) * 16;
         lrow = lane / C::CH;
         lpos = lane % C::CH;
     }
@@ -217,11 +240,12 @@ struct Walk {
     // made opaque: the compiler follows an address to its LDS object over a few
     // steps only, and before a read of an object it does not know it waits for
     // every load into LDS, the next keys' among them.
-    __device__ __forceinline__ void address(int first) {
+    __device__ __forceinline__ void address(int first, int hv) {
         kaddr += first;
+        ch0 = hv * C::ND * 32;
 #pragma unroll
-        for (int d = 0; d < (C::ND < 4 ? C::ND : 4); ++d) {
-            vaddr[d] += first;
+        for (int d = 0; d < NV; ++d) {
+            vaddr[d] += first + ch0 * 2;
             asm volatile("" : "+v"(vaddr[d]));
         }
     }
@@ -434,7 +458,7 @@ struct Walk {
             for (int d = 0; d < C::ND; ++d)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int ch = 32 * d + 8 * x + 4 * g2;
+                    const int ch = ch0 + 32 * d + 8 * x + 4 * g2;
                     uint2 v = make_uint2(0, 0);
                     if (ch < D) v = *reinterpret_cast<const uint2*>(vr + ch);
                     st.acc[d][4 * x] += p * __uint_as_float(v.x << 16);
@@ -463,24 +487,25 @@ __device__ __forceinline__ void wait_here() {
 }
 
 // Keys k0 .. k1-1 (a uniform range) for the wave's 32 rows, the workgroup's
-// four waves sharing each stage of 64 keys.
+// four waves sharing each stage of C::ST keys.
 template <class C, class Keys>
 __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                               uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
     using W = Walk<C, Keys>;
     using Source = typename W::Source;
     using Slots = typename W::Slots;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n_stages = (k1 - k0 + 63) / 64;
-    const int row0 = wave * C::R;                                 // rows of a stage this wave loads
+    const Part<C> part;
+    const int n_stages = (k1 - k0 + C::ST - 1) / C::ST;
+    const int row0 = part.wave * C::R;                            // rows of a stage this wave loads
     // the lane's key of a stage: its table entry (of the last key past the
     // range), then its slot, for the loads and the masks
+    const int mine = k0 + static_cast<int>(threadIdx.x & (C::ST - 1));
     auto entry = [&](int s) __attribute__((always_inline)) -> int32_t {
-        if constexpr (W::PAGED) return keys.entry(min(k0 + s * 64 + static_cast<int>(threadIdx.x & 63), k1 - 1));
+        if constexpr (W::PAGED) return keys.entry(min(mine + s * C::ST, k1 - 1));
         else return 0;
     };
     auto slot_of = [&](int s, int32_t page) __attribute__((always_inline)) -> int {
-        const int key = k0 + s * 64 + (threadIdx.x & 63);
+        const int key = mine + s * C::ST;
         if constexpr (W::PAGED) return key < k1 ? keys.slot(key, page) : -1;
         else return 0;
     };
@@ -490,14 +515,17 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         if constexpr (W::PAGED) return __ballot(sl >= 0);
         else return ~uint64_t(0);
     };
+    if (n_stages <= 0) return;
     // stage s lives in buffers s % 2; its loads are issued while stage s-1 is
     // computed, its table entries are read one stage earlier still.  The
-    // query rows come through the buffers of stage 1.
-    uint8_t* const qt = (wave < 2 ? kb1 : vb1) + (wave & 1) * 32 * C::RB;
-    if (n_stages > 0) w.template stage_q<32 / C::RPI>(q, qt, 0);
-    int slot = n_stages > 0 ? slot_of(0, page) : -1;
+    // query rows come through the buffers of stage 1, each row group's from
+    // the waves that share it.
+    constexpr int PER = C::BUF / (32 * C::RB), WPG = 4 / C::QG;   // row groups per buffer, waves per row group
+    uint8_t* const qt = (part.qg < PER ? kb1 : vb1) + (part.qg % PER) * 32 * C::RB;
+    w.template stage_q<32 / WPG / C::RPI>(q, qt, part.wave / C::QG * (32 / WPG));
+    int slot = slot_of(0, page);
     uint64_t vcur = valid(slot);
-    if (n_stages > 0) {
+    {
         const Source k = w.template source<false>(k0 + row0, k1), v = w.template source<true>(k0 + row0, k1);
         const Slots sl = w.slots_of(slot, row0);
 #pragma unroll
@@ -505,16 +533,19 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
 #pragma unroll
         for (int i = 0; i < C::NI; ++i) w.template load<true>(v, sl, vb0 + row0 * C::RB, row0, i);
     }
-    if (n_stages <= 0) return;
     wait_here<wait_vm(2 * C::NI)>();
+    if constexpr (WPG > 1) {
+        __builtin_amdgcn_s_barrier();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    }
     w.read_q(qt);
-    w.address(0);
+    w.address(0, part.hv);
     page = entry(1);
     auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& load_one, auto&& load_more) __attribute__((always_inline)) {
         f32x16_t sc = w.template scores<C::NI>(kt, load_one);
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
-        w.template weights<C::KW == 1 ? 0 : C::NI>(sc, pw, load_more);
+        w.template weights<C::SUBS == 2 ? 0 : C::NI>(sc, pw, load_more);
         if (!w.put_off(vt, key0)) w.add(vt, pw);
     };
     auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s) __attribute__((always_inline)) {
@@ -524,10 +555,10 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         __builtin_amdgcn_s_barrier();
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         __builtin_amdgcn_sched_barrier(0);
-        const int key0 = k0 + s * 64;
+        const int key0 = k0 + s * C::ST;
         // the next stage's loads (past the last stage: zeros) go out among
         // this one's scores and, with one sub-tile per stage, its weights
-        const Source k = w.template source<false>(key0 + 64 + row0, k1), v = w.template source<true>(key0 + 64 + row0, k1);
+        const Source k = w.template source<false>(key0 + C::ST + row0, k1), v = w.template source<true>(key0 + C::ST + row0, k1);
         slot = slot_of(s + 1, page);
         const Slots sl = w.slots_of(slot, row0);
         if constexpr (W::PAGED) __builtin_amdgcn_sched_barrier(0);   // the exchanges together, not one wait among the products each
@@ -535,13 +566,12 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         page = entry(s + 2);
         auto load_k = [&](int i) __attribute__((always_inline)) { w.template load<false>(k, sl, kn + row0 * C::RB, row0, i); };
         auto load_v = [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vn + row0 * C::RB, row0, i); };
-        if constexpr (C::KW == 1) {
+        if constexpr (C::SUBS == 2) {
             sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur), load_k, [](int) {});
             sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32), load_v, [](int) {});
         } else {
-            const int half = wave >> 1;                           // this wave's sub-tile
-            sub_tile(kc + half * 32 * C::RB, vc + half * 32 * C::RB, key0 + half * 32, static_cast<uint32_t>(vcur >> (32 * half)),
-                     load_k, load_v);
+            const int at = part.kg * 32;
+            sub_tile(kc + at * C::RB, vc + at * C::RB, key0 + at, static_cast<uint32_t>(vcur >> at), load_k, load_v);
         }
         vcur = vnext;
     };
@@ -552,14 +582,14 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
     st.l = half_sum(st.l);
     w.add_late(q, k1, [&](int key) {
         const int t = key - k0;
-        return C::KW == 1 || (t >> 5 & 1) == wave >> 1 ? k0 + (t & ~31) : -1;
+        return (t >> 5 & (C::KG - 1)) == part.kg ? k0 + (t & ~31) : -1;
     });
 }
 
 // Keys k0 .. k1-1 for 32 rows that the four waves share: wave w takes
 // sub-tiles w, w + 4, ...  Each wave's K and V have one place in LDS: K of
 // the next sub-tile goes out while this one's weights are formed, its V among
-// its scores, so 16 (D <= 64: 8, D > 128: 32) KiB per wave are in flight.
+// its scores, so 16 (D <= 64: 8) KiB per wave are in flight.
 template <class C, class Keys>
 __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                            uint8_t* kb_all, uint8_t* vb_all, State<C>& st) {
@@ -600,7 +630,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
     w.read_q(vb_all);
-    w.address(wave * 32 * C::RB);
+    w.address(wave * 32 * C::RB, 0);
     wait_here<kWaitLds>();
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
@@ -649,12 +679,12 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
 // First of this wave's 32 rows in the workgroup's tile.
 template <class C>
 __device__ __forceinline__ int wave_row() {
-    return (__builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % (4 / C::KW)) * 32;
+    return Part<C>().qg * 32;
 }
 
 // Writes the workgroup's rows: through LDS, so that a row goes out as one run
-// of 16-byte words; the KW waves' results for the same rows are joined on the
-// way (k-th of them: with_keys > k says that it had keys).  PART false: O / l
+// of 16-byte words; the KG key parts' results for the same rows are joined on
+// the way (k-th of them: with_keys > k says that it had keys).  PART false: O / l
 // rounded to bf16 (0 for a row without keys) at address `to` of the lane's
 // row; PART true: row number to - 1 of part_ml (maximum, sum) and part_o (O,
 // fp32, nothing for a row without keys).  to 0: the lane has no row.
@@ -663,56 +693,61 @@ __device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, floa
                                            uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, float (*ml)[2][32],
                                            uint64_t (*row_at)[32]) {
     const int lane = threadIdx.x & 63, l32 = lane & 31, g2 = lane >> 5;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int QW = 4 / C::KW;                                 // groups of 32 rows
+    const Part<C> part;
     constexpr int ROW = C::DP * 4;                                // bytes; 16-byte chunk c of row r at c ^ r
-    auto area = [&](int w) __attribute__((always_inline)) -> uint8_t* {
-        if constexpr (C::SHARE) return w == 0 ? b0 : (w == 1 ? b1 : (w == 2 ? b2 : b3));
-        else return (w < 2 ? b0 : b1) + (w & 1) * 32 * ROW;
+    // row r of (row group, key part) a; a buffer holds PER such sets of 32
+    // rows, or half of one
+    constexpr int PER = C::BUF / (32 * ROW);
+    auto place = [&](int a, int r) __attribute__((always_inline)) -> uint8_t* {
+        const int at = PER > 0 ? a / (PER > 0 ? PER : 1) : 2 * a + (r >> 4);
+        const int in = PER > 0 ? a % (PER > 0 ? PER : 1) * 32 + r : r & 15;
+        return (at == 0 ? b0 : (at == 1 ? b1 : (at == 2 ? b2 : b3))) + in * ROW;
     };
+    static_assert(PER > 0 || C::BUF == 16 * ROW, "half a set");
+    const int set = part.qg + part.kg * C::QG;
     wait_here<kWaitAll>();
     __syncthreads();                                              // every wave is past its last keys
     {
-        uint8_t* const a = area(wave) + l32 * ROW;
-        if (wave / QW < with_keys) {
+        uint8_t* const a = place(set, l32);
+        if (part.kg < with_keys) {
 #pragma unroll
             for (int d = 0; d < C::ND; ++d)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const f32x4_t v = {st.acc[d][4 * x], st.acc[d][4 * x + 1], st.acc[d][4 * x + 2], st.acc[d][4 * x + 3]};
-                    *reinterpret_cast<f32x4_t*>(a + (((8 * d + 2 * x + g2) ^ l32) & (C::DP / 4 - 1)) * 16) = v;
+                    *reinterpret_cast<f32x4_t*>(a + (((8 * (d + part.hv * C::ND) + 2 * x + g2) ^ l32) & (C::DP / 4 - 1)) * 16) = v;
                 }
         }
-        if (g2 == 0) {
-            ml[wave][0][l32] = st.m;
-            ml[wave][1][l32] = st.l;
-            row_at[wave][l32] = to;
+        if (g2 == 0 && part.hv == 0) {
+            ml[set][0][l32] = st.m;
+            ml[set][1][l32] = st.l;
+            row_at[set][l32] = to;
         }
     }
     __syncthreads();
-    // the KW waves of a group write its 32 rows, 8 channels per lane.  Many
-    // passes stay a loop: code that runs once per workgroup waits for its
-    // instructions, about 5 cycles each.
+    // the waves of a row group write its 32 rows, 8 channels per lane.  Many
+    // passes stay a loop: code that runs once per workgroup is bound by its
+    // length.
     constexpr int GROUPS = C::DP / 8, RPW = 64 / GROUPS;          // rows per wave and pass
-    const int q = wave % QW, cg = lane % GROUPS;
-    constexpr int PASSES = 32 / (C::KW * RPW), UNROLL = C::KW == 4 ? PASSES : 2;
+    constexpr int WPG = 4 / C::QG, PASSES = 32 / (WPG * RPW), UNROLL = WPG == 4 ? PASSES : 2;
+    const int cg = lane % GROUPS;
 #pragma unroll UNROLL
     for (int pass = 0; pass < PASSES; ++pass) {
-        const int row = (pass * C::KW + wave / QW) * RPW + lane / GROUPS;
-        const uint64_t dst = row_at[q][row];
-        float mk[C::KW], m = -__builtin_inff(), l = 0.0f;
+        const int row = (pass * WPG + part.wave / C::QG) * RPW + lane / GROUPS;
+        const uint64_t dst = row_at[part.qg][row];
+        float mk[C::KG], m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < C::KW; ++k) {
-            mk[k] = ml[q + k * QW][0][row];
+        for (int k = 0; k < C::KG; ++k) {
+            mk[k] = ml[part.qg + k * C::QG][0][row];
             m = fmaxf(m, mk[k]);
         }
         f32x4_t o[2] = {f32x4_t{}, f32x4_t{}};
 #pragma unroll
-        for (int k = 0; k < C::KW; ++k) {
+        for (int k = 0; k < C::KG; ++k) {
             const float f = mk[k] == m ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - m);
-            l += ml[q + k * QW][1][row] * f;
+            l += ml[part.qg + k * C::QG][1][row] * f;
             if (k < with_keys) {
-                const uint8_t* const a = area(q + k * QW) + row * ROW;
+                const uint8_t* const a = place(part.qg + k * C::QG, row);
 #pragma unroll
                 for (int x = 0; x < 2; ++x)
                     o[x] += *reinterpret_cast<const f32x4_t*>(a + (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16) * f;
@@ -963,18 +998,21 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
 
 constexpr int kComputeUnits = 256;
 
-// Query rows per workgroup and what goes with them: 128, 64 or 32.
-int key_waves(int tm) { return 128 / tm; }
-int step_keys(int tm) { return tm == 32 ? 128 : 64; }
+// Query rows per workgroup: 128, 64 or 32, at most 64 with 256 channels; and
+// the keys of a step.
+int most_rows(int64_t D) { return 128; }
+int step_keys(int64_t D, int tm) { return D > 128 ? 64 : (tm == 32 ? 128 : 64); }
 
 // D channels run in the kernels of the next padded size.
 template <int DP, class F>
 hipError_t by_rows(int tm, F&& launch) {
-    return tm == 128 ? launch(ACfg<DP, 1>{}) : (tm == 64 ? launch(ACfg<DP, 2>{}) : launch(ACfg<DP, 4>{}));
+    return tm == 128 ? launch(ACfg<DP, 128>{}) : (tm == 64 ? launch(ACfg<DP, 64>{}) : launch(ACfg<DP, 32>{}));
 }
 template <class F>
 hipError_t by_size(int D, int tm, F&& launch) {
-    return D <= 64 ? by_rows<64>(tm, launch) : (D <= 128 ? by_rows<128>(tm, launch) : by_rows<256>(tm, launch));
+    if (D <= 64) return by_rows<64>(tm, launch);
+    if (D <= 128) return by_rows<128>(tm, launch);
+    return by_rows<256>(tm, launch);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -985,7 +1023,7 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     const int64_t rows = static_cast<int64_t>(a.total_q) * (a.Hq / a.Hkv);
     // the widest tile whose workgroups fill the compute units, as wide tiles
     // load least; with too few rows for any, the narrowest
-    int tm = 128;
+    int tm = most_rows(a.D);
     while (tm > 32 && a.Hkv * ceil_div(rows, tm) < kComputeUnits) tm /= 2;
     // every sequence ends in at most one partial tile
     a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
@@ -1003,7 +1041,7 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // keys of its own and fewer splits fill the GPU, so less is joined (64
     // sequences behind 8195 keys, 32 heads on 8 of 128: 42 us against 50 with
     // 128-row tiles; 80 rows over 778 keys, 256 channels: 14 against 18).
-    auto tile = [](int64_t rows) { return rows > 256 ? 128 : 32; };
+    auto tile = [&](int64_t rows) { return rows > 256 ? most_rows(D) : 32; };
     p.prefix_tm = tile(rows_p);
     p.suffix_tm = tile(rows_s);
     // A sequence whose rows fill its tiles reads the prefix no more often by
@@ -1012,8 +1050,8 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     p.merged = B == 1 || prefix_cap == 0 ||
                2 * B * ceil_div(rows_s, p.suffix_tm) * p.suffix_tm <= 3 * ceil_div(rows_p, p.prefix_tm) * p.prefix_tm;
     const int64_t keys_s = suffix_cap + (p.merged ? prefix_cap : 0);
-    const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(p.prefix_tm));
-    const int64_t steps_s = ceil_div(keys_s, step_keys(p.suffix_tm));
+    const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(D, p.prefix_tm));
+    const int64_t steps_s = ceil_div(keys_s, step_keys(D, p.suffix_tm));
     const int64_t tiles_p = p.merged ? 0 : ceil_div(rows_p, p.prefix_tm);
     p.suffix_tiles = ceil_div(rows_s, p.suffix_tm);
     // keys are split until the workgroups fill the compute units once
