@@ -998,10 +998,8 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
 
 constexpr int kComputeUnits = 256;
 
-// Query rows per workgroup: 128, 64 or 32, at most 64 with 256 channels; and
-// the keys of a step.
-int most_rows(int64_t D) { return 128; }
-int step_keys(int64_t D, int tm) { return D > 128 ? 64 : (tm == 32 ? 128 : 64); }
+// Keys of a workgroup's step.
+int step_keys(int64_t D, int tm) { return D <= 128 && tm == 32 ? 128 : 64; }
 
 // D channels run in the kernels of the next padded size.
 template <int DP, class F>
@@ -1021,10 +1019,21 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     const int64_t rows = static_cast<int64_t>(a.total_q) * (a.Hq / a.Hkv);
-    // the widest tile whose workgroups fill the compute units, as wide tiles
-    // load least; with too few rows for any, the narrowest
-    int tm = most_rows(a.D);
-    while (tm > 32 && a.Hkv * ceil_div(rows, tm) < kComputeUnits) tm /= 2;
+    // Narrow tiles where the GPU runs them all at once, wide ones, which load
+    // less, where not: two workgroups per compute unit, one with 256 channels.
+    // Of a causal prompt's tiles, half as long on average, up to one and a
+    // half (64 rows: two) times as many.  Measured with 128 / 64 / 32 rows:
+    //   32 heads on 8 of 128, all keys: 450 tokens 18.5 / 13.3 / 12.0 us, 1024
+    //   tokens 30 / 27 / 34, 1500 tokens 54 / 55 / 63; causal: 1024 tokens 30 /
+    //   21 / 25, 1500 tokens 42 / 36 / 40
+    //   8 heads on 1 of 256, all keys: 800 tokens 36 / 25 / 21, 2048 tokens 71 /
+    //   50 / 76, 2500 tokens 85 / 104 / 129; causal: 1500 tokens 56 / 37 / 31,
+    //   3900 tokens 124 / 89 / 140
+    // And no tile that the average sequence would not half fill.
+    const int64_t slots = (a.D > 128 ? 1 : 2) * kComputeUnits;
+    auto fits = [&](int tm) { return a.Hkv * ceil_div(rows, tm) <= (a.causal ? (tm == 64 ? 2 * slots : 3 * slots / 2) : slots); };
+    int tm = 128;
+    while (tm > 32 && (2 * rows <= static_cast<int64_t>(a.B) * tm || fits(tm / 2))) tm /= 2;
     // every sequence ends in at most one partial tile
     a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
     return by_size(a.D, tm, [&](auto cfg) {
@@ -1041,7 +1050,7 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // keys of its own and fewer splits fill the GPU, so less is joined (64
     // sequences behind 8195 keys, 32 heads on 8 of 128: 42 us against 50 with
     // 128-row tiles; 80 rows over 778 keys, 256 channels: 14 against 18).
-    auto tile = [&](int64_t rows) { return rows > 256 ? most_rows(D) : 32; };
+    auto tile = [](int64_t rows) { return rows > 256 ? 128 : 32; };
     p.prefix_tm = tile(rows_p);
     p.suffix_tm = tile(rows_s);
     // A sequence whose rows fill its tiles reads the prefix no more often by
