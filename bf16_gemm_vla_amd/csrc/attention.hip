@@ -780,20 +780,117 @@ __device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int 
 
 // ------------------------------------------------------------------ prompt
 
-// Workgroup -> (key/value head, row tile).  Workgroups go to the 8 XCDs round
-// robin: workgroups of one XCD share key/value heads, so a head's keys are
-// fetched into one L2 (or into 8 / Hkv of them), and row tiles come last rows
-// first, so the longest causal tiles do not start last.
-__device__ __forceinline__ void head_tile(int id, int Hkv, int tiles, int& hk, int& tile) {
+// Workgroup -> (key/value head, rank of its row tile).  Workgroups go to the 8
+// XCDs round robin: workgroups of one XCD share key/value heads, so a head's
+// keys are fetched into one L2 (or into 8 / Hkv of them).
+__device__ __forceinline__ void head_rank(int id, int Hkv, int tiles, int& hk, int& rank) {
     if (Hkv % 8 == 0) {
         const int x = id & 7, j = id >> 3;
         hk = (j / tiles) * 8 + x;
-        tile = j % tiles;
+        rank = j % tiles;
     } else {
         hk = id % Hkv;
-        tile = id / Hkv;
+        rank = id / Hkv;
     }
-    tile = tiles - 1 - tile;
+}
+
+// Sum over the wave, the same in every lane.
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
+    auto from = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
+        return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x), ctrl(), rows(), 0xF, false));
+    };
+    x += from(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});   // row_shr:1
+    x += from(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});   // row_shr:2
+    x += from(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});   // row_shr:4
+    x += from(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});   // row_shr:8
+    x += from(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});   // row_bcast:15
+    x += from(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});   // row_bcast:31
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// One sequence's rows and keys, bounded to the tensors: no value in the
+// offsets can lead outside.
+struct Range {
+    int q0, nq, k0, nk;
+    __device__ __forceinline__ Range(const PromptArgs& a, int b) {
+        q0 = min(max(a.cu_q[b], 0), a.total_q);
+        nq = max(min(a.cu_q[b + 1], a.total_q) - q0, 0);
+        k0 = min(max(a.cu_k[b], 0), a.total_k);
+        nk = max(min(a.cu_k[b + 1], a.total_k) - k0, 0);
+    }
+    __device__ __forceinline__ Range() : q0(0), nq(0), k0(0), nk(0) {}
+    __device__ __forceinline__ uint32_t tiles(int G, int tm) const {
+        return static_cast<uint32_t>((static_cast<int64_t>(nq) * G + tm - 1) / tm);
+    }
+    __device__ __forceinline__ void from_lane(int lane) {
+        q0 = __builtin_amdgcn_readlane(q0, lane);
+        nq = __builtin_amdgcn_readlane(nq, lane);
+        k0 = __builtin_amdgcn_readlane(k0, lane);
+        nk = __builtin_amdgcn_readlane(nk, lane);
+    }
+};
+
+// The row tile of rank `rank`: its sequence's range, and its place there as
+// the result, or -1 if there are fewer tiles.
+template <int TM>
+__device__ __forceinline__ int find_tile(const PromptArgs& a, int G, int rank, Range& r) {
+    const int lane = threadIdx.x & 63;
+    if (a.B == 1) {
+        r = Range(a, 0);
+        r.from_lane(0);
+        const uint32_t n = r.tiles(G, TM);
+        return static_cast<uint32_t>(rank) < n ? static_cast<int>(n) - 1 - rank : -1;
+    }
+    if (a.B <= 64) {
+        // One sequence per lane.  Tiles with most keys first, so that none of
+        // them starts last: tile t of a sequence is on level t + `base`, base
+        // being its keys ahead of its first row in units of a tile's rows (16
+        // causal prompts of 1 to 1814 tokens, 28 heads on 4 of 128: 151 us, in
+        // the sequences' order 154).  The level of rank `rank` is the highest
+        // x with more than `rank` tiles on x and above.
+        r = lane < a.B ? Range(a, lane) : Range();
+        const uint32_t n = r.tiles(G, TM);
+        const int64_t ahead = a.causal ? static_cast<int64_t>(r.nk) - r.nq : r.nk;
+        const uint32_t base = n ? static_cast<uint32_t>(min(max(ahead, int64_t(0)) * G / TM, int64_t(1) << 20)) : 0;
+        auto above = [&](uint32_t x) __attribute__((always_inline)) {   // tiles on level x and above
+            return wave_sum(x <= base ? n : (x < base + n ? base + n - x : 0));
+        };
+        if (above(0) <= static_cast<uint32_t>(rank)) return -1;
+        uint32_t lo = 0, size = 1;
+        while (size < 0x80000000u && __any(base + n > size)) size *= 2;
+        for (size /= 2; size; size /= 2)
+            if (above(lo + size) > static_cast<uint32_t>(rank)) lo += size;
+        // the level's tiles, one per sequence, in the sequences' order
+        const uint64_t on = __ballot(lo >= base && lo < base + n);
+        const uint32_t nth = static_cast<uint32_t>(rank) - above(lo + 1);
+        const uint32_t mine = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(on >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(on), 0));
+        const uint64_t hit = __ballot((on >> lane & 1) && mine == nth);
+        const int src = __builtin_ctzll(hit);
+        r.from_lane(src);
+        return static_cast<int>(lo - __builtin_amdgcn_readlane(base, src));
+    }
+    // Many sequences: a scan over their tile counts, 64 at a time, the last
+    // tiles of the batch first.
+    const uint32_t tile = a.tiles - 1 - rank;
+    uint32_t first = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 64) {
+        r = b0 + lane < a.B ? Range(a, b0 + lane) : Range();
+        const uint32_t n = r.tiles(G, TM);
+        uint32_t incl = n;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const uint32_t up = __shfl_up(incl, o, 64);
+            if (lane >= o) incl += up;
+        }
+        const uint64_t hit = __ballot(tile >= first + incl - n && tile < first + incl);
+        if (hit) {
+            const int src = __builtin_ctzll(hit);
+            r.from_lane(src);
+            return static_cast<int>(tile - __builtin_amdgcn_readlane(first + incl - n, src));
+        }
+        first += __builtin_amdgcn_readlane(incl, 63);
+    }
+    return -1;
 }
 
 template <class C>
@@ -801,50 +898,14 @@ __global__ __launch_bounds__(kAThreads) __attribute__((amdgpu_waves_per_eu(C::WA
 void attn_prompt_kernel(PromptArgs a) {
     ATTN_LDS;
     const int lane = threadIdx.x & 63;
-    int hk, tile;
-    head_tile(blockIdx.x, a.Hkv, a.tiles, hk, tile);
-
-    // which sequence holds row tile `tile`: a scan over the sequences' tile
-    // counts, 64 at a time.  Offsets are bounded to the tensors here, so no
-    // value in them can lead outside.
+    int hk, rank;
+    head_rank(blockIdx.x, a.Hkv, a.tiles, hk, rank);
     const int G = a.Hq / a.Hkv;
-    int q0 = 0, nq = 0, k0 = 0, nk = 0, first = 0, found = 0;
-    for (int base = 0; base < a.B && !found; base += 64) {
-        const int b = base + lane;
-        int s = 0, n = 0, t = 0, ks = 0, kn = 0;
-        if (b < a.B) {
-            s = min(max(a.cu_q[b], 0), a.total_q);
-            n = max(min(a.cu_q[b + 1], a.total_q) - s, 0);
-            ks = min(max(a.cu_k[b], 0), a.total_k);
-            kn = max(min(a.cu_k[b + 1], a.total_k) - ks, 0);
-            t = static_cast<int>((static_cast<int64_t>(n) * G + C::TM - 1) / C::TM);
-        }
-        int incl = t;
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int up = __shfl_up(incl, o, 64);
-            if (lane >= o) incl += up;
-        }
-        const bool here = t > 0 && tile >= first + incl - t && tile < first + incl;
-        const uint64_t hit = __ballot(here);
-        if (hit) {
-            const int src = __builtin_ctzll(hit);
-            q0 = __shfl(s, src, 64);
-            nq = __shfl(n, src, 64);
-            k0 = __shfl(ks, src, 64);
-            nk = __shfl(kn, src, 64);
-            first = __shfl(first + incl - t, src, 64);
-            found = 1;
-        } else {
-            first += __shfl(incl, 63, 64);
-        }
-    }
-    if (!found) return;
-    q0 = __builtin_amdgcn_readfirstlane(q0);
-    nq = __builtin_amdgcn_readfirstlane(nq);
-    k0 = __builtin_amdgcn_readfirstlane(k0);
-    nk = __builtin_amdgcn_readfirstlane(nk);
-    const int rt = tile - __builtin_amdgcn_readfirstlane(first);
+    Range at;
+    const int rt = __builtin_amdgcn_readfirstlane(find_tile<C::TM>(a, G, rank, at));
+    if (rt < 0) return;
+    at.from_lane(0);
+    const int q0 = at.q0, nq = at.nq, k0 = at.k0, nk = at.nk;
 
     const int64_t rows = static_cast<int64_t>(nq) * G;
     const int64_t r = static_cast<int64_t>(rt) * C::TM + wave_row<C>() + (lane & 31);
@@ -1002,15 +1063,10 @@ constexpr int kComputeUnits = 256;
 int step_keys(int64_t D, int tm) { return D <= 128 && tm == 32 ? 128 : 64; }
 
 // D channels run in the kernels of the next padded size.
-template <int DP, class F>
-hipError_t by_rows(int tm, F&& launch) {
-    return tm == 128 ? launch(ACfg<DP, 128>{}) : (tm == 64 ? launch(ACfg<DP, 64>{}) : launch(ACfg<DP, 32>{}));
-}
-template <class F>
-hipError_t by_size(int D, int tm, F&& launch) {
-    if (D <= 64) return by_rows<64>(tm, launch);
-    if (D <= 128) return by_rows<128>(tm, launch);
-    return by_rows<256>(tm, launch);
+template <int TM, class F>
+hipError_t by_size(int D, F&& launch) {
+    if (D <= 64) return launch(ACfg<64, TM>{});
+    return D <= 128 ? launch(ACfg<128, TM>{}) : launch(ACfg<256, TM>{});
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1036,10 +1092,11 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     while (tm > 32 && (2 * rows <= static_cast<int64_t>(a.B) * tm || fits(tm / 2))) tm /= 2;
     // every sequence ends in at most one partial tile
     a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
-    return by_size(a.D, tm, [&](auto cfg) {
+    auto run = [&](auto cfg) {
         attn_prompt_kernel<decltype(cfg)><<<a.tiles * a.Hkv, kAThreads, 0, s>>>(a);
         return hipGetLastError();
-    });
+    };
+    return tm == 128 ? by_size<128>(a.D, run) : (tm == 64 ? by_size<64>(a.D, run) : by_size<32>(a.D, run));
 }
 
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
@@ -1094,14 +1151,15 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
         a.prefix_items = static_cast<int>(prefix_items);
         const int grid = static_cast<int>(prefix_items + suffix_items);
         if (grid == 0) return hipSuccess;
-        return by_size(a.D, tm, [&](auto cfg) {
+        auto kernel = [&](auto cfg) {
             // caches below 4 GiB take one 32-bit offset per row and load, where
             // 64-bit addresses with a select for missing rows took five
             // instructions more each
             if (wide) attn_shared_kernel<decltype(cfg), true><<<grid, kAThreads, 0, s>>>(a);
             else attn_shared_kernel<decltype(cfg), false><<<grid, kAThreads, 0, s>>>(a);
             return hipGetLastError();
-        });
+        };
+        return tm == 128 ? by_size<128>(a.D, kernel) : by_size<32>(a.D, kernel);
     };
     hipError_t e;
     if (p.prefix_tm == p.suffix_tm) {

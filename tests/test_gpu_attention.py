@@ -296,6 +296,42 @@ def test_prompt_offsets_are_bounded():
         assert_attention(got[a:e], q[a:e], k[a:e], v[a:e], np.full(e - a, e - a), 0.125)
 
 
+@pytest.mark.parametrize("hq,hkv,D,n,causal", [
+    (32, 8, 64, 1300, False), (40, 8, 128, 900, False), (48, 4, 72, 700, False), (64, 4, 256, 560, False),
+    (64, 8, 64, 1150, True), (64, 8, 128, 1100, True), (64, 4, 256, 200, False), (64, 4, 256, 300, True)])
+def test_prompt_tile_heights(hq, hkv, D, n, causal):
+    """Both tile heights above the smallest, with and without a causal mask,
+    ending inside a tile and behind keys of an earlier chunk."""
+    run_prompt([n, 75], [n, 203], hq, hkv, D, causal, seed=210 + D + n)
+
+
+@pytest.mark.parametrize("hq,hkv,D,n", [(64, 8, 64, 1150), (64, 8, 128, 1100), (64, 4, 256, 560), (64, 4, 200, 300)])
+def test_prompt_unseen_values_in_tall_tiles(hq, hkv, D, n):
+    """NaN in one late key and value stays out of every row before it."""
+    at = n - 40
+    def poison(q, k, v):
+        k[at, :, 3] = v[at, :, 5] = 0x7FC0
+        v[at - 90, :, 0] = 0x7F80
+    got, (q, k, v) = run_prompt([n], [n], hq, hkv, D, True, seed=330 + D, poison=poison, check=False)
+    lim = np.arange(at - 90) + 1
+    assert_attention(got[:at - 90], q[:at - 90], k[:at - 90], v[:at - 90], lim, float(np.float32(1 / math.sqrt(D))))
+    f = bf16_f64(got)
+    assert np.isfinite(f[:at, :, 1:]).all() and np.isnan(f[at:]).all()
+
+
+@pytest.mark.parametrize("B", [2, 63, 64, 65, 130])
+@pytest.mark.parametrize("causal", [False, True])
+def test_prompt_batches(B, causal):
+    """Every tile of every sequence is found once, with sequences of no rows
+    or no keys among them, more rows than keys and more keys than rows."""
+    r = synthetic.rng(9300 + B)
+    nq, nk = r.integers(0, 70, B), r.integers(0, 300, B)
+    nq[::7] = 0
+    nk[3::11] = 0
+    nq[1] = 333
+    run_prompt([int(x) for x in nq], [int(x) for x in nk], 6, 2, 64, causal, pad=(2, 2), seed=340 + B)
+
+
 # --------------------------------------------------------- shared prefix
 
 class Cache:
@@ -464,6 +500,49 @@ def test_shared_cache_past_4_gib():
                                D, pages, page, 0, 7, hq * D, hq * D, True, 0.125)
     o.check()
     assert_attention(o.numpy(np.uint16).reshape(1, hq, D), q, kb, vb, [n], 0.125)
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(4, 2, 128), (8, 1, 256), (2, 2, 64)])
+@pytest.mark.parametrize("rows", [1, 300])
+def test_shared_cache_past_4_gib_in_every_tile(hq, hkv, D, rows):
+    """A prefix and suffixes spread over a cache of 5 GiB, for few rows and for tall tiles."""
+    page, L = 16, rows
+    pages = (5 << 30) // (hkv * D * 2) // page
+    k = torch.zeros(pages * page, hkv, D, dtype=torch.int16, device="cuda")
+    v = torch.zeros_like(k)
+    pre = np.array([pages - 1, 5, pages // 2 + 1, pages // 4 * 3], np.int32)
+    table = np.array([[pages - 3, 7, pages // 5 * 4], [2, pages - 9, pages // 3 * 2]], np.int32)
+    lens, n_pre = [33, 48], 60
+    def slots(p, n):
+        return p[np.arange(n) // page].astype(np.int64) * page + np.arange(n) % page
+    keys = []
+    for b in range(2):
+        at = np.concatenate([slots(pre, n_pre), slots(table[b], lens[b])])
+        keys.append((at, rand(660 + b, len(at), hkv, D), rand(662 + b, len(at), hkv, D)))
+        if b:
+            for x in (1, 2):
+                keys[1][x][:n_pre] = keys[0][x][:n_pre]
+        t = torch.from_numpy(at).cuda()
+        k[t], v[t] = torch.from_numpy(keys[b][1].view(np.int16)).cuda(), torch.from_numpy(keys[b][2].view(np.int16)).cuda()
+    q = rand(664, 2 * L, hq, D, scale=2.0)
+    n = vla.vla_attn_shared_prefix_workspace_bytes(2, L, hq, hkv, D, 4 * page, 3 * page)
+    o, w = Guarded(2 * L * hq * D * 2), zeros_ws(n)
+    vla.vla_attn_shared_prefix(dev(q), k, v, dev(pre), dev(np.array([n_pre], np.int32)), dev(table),
+                               dev(np.array(lens, np.int32)), o.t, w, n, 2, L, hq, hkv, D, pages, page, 4, 3, hq * D, hq * D,
+                               False, 0.1)
+    o.check()
+    got = o.numpy(np.uint16).reshape(2, L, hq, D)
+    for b in range(2):
+        assert_attention(got[b], q.reshape(2, L, hq, D)[b], keys[b][1], keys[b][2], np.full(L, len(keys[b][0])), float(np.float32(0.1)))
+
+
+@pytest.mark.parametrize("hq,hkv,D", [(8, 1, 256), (8, 1, 64), (16, 2, 128), (24, 3, 72)])
+def test_shared_tall_prefix_tiles(hq, hkv, D):
+    """Tall tiles for the prefix beside short ones for the suffixes, and the
+    prefix ahead of every sequence's own keys."""
+    run_shared(41, 1, hq, hkv, D, 16, 333, [1 + 3 * b for b in range(41)], True, seed=580 + D)
+    run_shared(41, 1, hq, hkv, D, 16, 50, [0] * 41, False, pages_per_seq=0, seed=590 + D)
+    run_shared(3, 40, hq, hkv, D, 16, 150, [40, 77, 0], True, seed=595 + D)
 
 
 # ------------------------------------------------------- graphs, streams
