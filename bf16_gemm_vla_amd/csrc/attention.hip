@@ -1103,13 +1103,19 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
                             int64_t suffix_cap) {
     SharedPlan p{};
     const int64_t G = Hq / Hkv, rows_s = L * G, rows_p = B * rows_s;
-    // Narrow tiles for up to 256 rows per key/value head: each wave streams
-    // keys of its own and fewer splits fill the GPU, so less is joined (64
-    // sequences behind 8195 keys, 32 heads on 8 of 128: 42 us against 50 with
-    // 128-row tiles; 80 rows over 778 keys, 256 channels: 14 against 18).
-    auto tile = [](int64_t rows) { return rows > 256 ? 128 : 32; };
-    p.prefix_tm = tile(rows_p);
-    p.suffix_tm = tile(rows_s);
+    // As for prompts: narrow tiles where all of them run at once, and none that
+    // one sequence's rows would not half fill (32 sequences of 50 tokens over
+    // 850 keys, 8 heads on 1 of 256: 31 us with 64 rows, 43 with 128 rows and
+    // the keys in two parts; 100 single tokens behind 4000 keys, 32 heads on 8
+    // of 128: 33 us with 32 rows, 50 with 128).
+    const int64_t slots = (D > 128 ? 1 : 2) * kComputeUnits;
+    auto tile = [&](int64_t batches, int64_t rows) {
+        int tm = 128;
+        while (tm > 32 && (2 * rows <= tm || Hkv * batches * ceil_div(rows, tm / 2) <= slots)) tm /= 2;
+        return tm;
+    };
+    p.prefix_tm = tile(1, rows_p);
+    p.suffix_tm = tile(B, rows_s);
     // A sequence whose rows fill its tiles reads the prefix no more often by
     // itself than a tile of the whole batch does: then the prefix is the head
     // of every sequence's range of keys and nothing has to be joined.
@@ -1120,11 +1126,11 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     const int64_t steps_s = ceil_div(keys_s, step_keys(D, p.suffix_tm));
     const int64_t tiles_p = p.merged ? 0 : ceil_div(rows_p, p.prefix_tm);
     p.suffix_tiles = ceil_div(rows_s, p.suffix_tm);
-    // keys are split until the workgroups fill the compute units once
+    // keys are split as often as the workgroups fit the compute units once
     auto splits = [&](int64_t tiles, int64_t steps) {
         if (tiles == 0 || steps == 0) return int64_t(0);
-        const int64_t per = ceil_div(tiles * steps, kComputeUnits);
-        return ceil_div(steps, per);
+        const int64_t most = kComputeUnits / tiles;
+        return most <= 1 ? int64_t(1) : ceil_div(steps, ceil_div(steps, most));
     };
     p.prefix_splits = splits(Hkv * tiles_p, steps_p);
     p.suffix_splits = splits(Hkv * B * p.suffix_tiles, steps_s);
@@ -1159,7 +1165,7 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
             else attn_shared_kernel<decltype(cfg), false><<<grid, kAThreads, 0, s>>>(a);
             return hipGetLastError();
         };
-        return tm == 128 ? by_size<128>(a.D, kernel) : by_size<32>(a.D, kernel);
+        return tm == 128 ? by_size<128>(a.D, kernel) : (tm == 64 ? by_size<64>(a.D, kernel) : by_size<32>(a.D, kernel));
     };
     hipError_t e;
     if (p.prefix_tm == p.suffix_tm) {

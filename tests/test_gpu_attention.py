@@ -545,6 +545,19 @@ def test_shared_tall_prefix_tiles(hq, hkv, D):
     run_shared(3, 40, hq, hkv, D, 16, 150, [40, 77, 0], True, seed=595 + D)
 
 
+@pytest.mark.parametrize("hq,hkv,D,B,L", [(8, 1, 256, 20, 64), (8, 1, 256, 40, 64), (16, 4, 128, 20, 64), (32, 8, 128, 20, 64),
+                                         (16, 4, 64, 20, 65), (32, 8, 72, 20, 65)])
+def test_shared_tall_suffix_tiles(hq, hkv, D, B, L):
+    """64-row and 128-row tiles for every sequence's rows, the prefix ahead of their own keys."""
+    run_shared(B, L, hq, hkv, D, 16, 70, [(L + 3 * b) if b else 0 for b in range(B)], True, seed=700 + D + B)
+
+
+@pytest.mark.parametrize("hq,hkv,D,B", [(64, 8, 64, 600), (64, 8, 128, 300), (8, 1, 256, 1100), (8, 1, 256, 2100)])
+def test_shared_many_single_tokens(hq, hkv, D, B):
+    """64-row and 128-row tiles for the prefix, 32-row tiles for the suffixes."""
+    run_shared(B, 1, hq, hkv, D, 16, 75, [b % 4 for b in range(B)], True, seed=720 + D + B)
+
+
 # ------------------------------------------------------- graphs, streams
 
 def capture(call):
