@@ -745,7 +745,7 @@ int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, con
     if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
     if (!std::isfinite(scale) || scale <= 0.0f) return fail(VLA_EINVAL, fn, "scale must be finite and > 0");
     // row tiles of at least 32 rows, at most one ragged one per sequence
-    if ((total_q * (Hq / Hkv) / 32 + B) * Hkv >= (int64_t(1) << 31))
+    if (total_q * (Hq / Hkv) >= (int64_t(1) << 31) - 128 || (total_q * (Hq / Hkv) / 32 + B) * Hkv >= (int64_t(1) << 31))
         return fail(VLA_ESHAPE, fn, "total_q=%lld rows of %lld heads are too many", (long long)total_q, (long long)Hq);
     const Region o{out, total_q, Hq * D, out_stride};
     const Region ins[5] = {{q, total_q, Hq * D, q_stride}, {k, total_k, Hkv * D, k_stride}, {v, total_k, Hkv * D, v_stride},

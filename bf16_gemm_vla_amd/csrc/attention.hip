@@ -783,14 +783,11 @@ __device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int 
 // Workgroup -> (key/value head, rank of its row tile).  Workgroups go to the 8
 // XCDs round robin: workgroups of one XCD share key/value heads, so a head's
 // keys are fetched into one L2 (or into 8 / Hkv of them).
-__device__ __forceinline__ void head_rank(int id, int Hkv, int tiles, int& hk, int& rank) {
-    if (Hkv % 8 == 0) {
-        const int x = id & 7, j = id >> 3;
-        hk = (j / tiles) * 8 + x;
-        rank = j % tiles;
+__device__ __forceinline__ void head_rank(const PromptArgs& a, int id, int& hk, int& rank) {
+    if (a.Hkv % 8 == 0) {
+        hk = a.by_heads.divide(id >> 3, rank) * 8 + (id & 7);         // by the tiles
     } else {
-        hk = id % Hkv;
-        rank = id / Hkv;
+        rank = a.by_heads.divide(id, hk);                             // by the key/value heads
     }
 }
 
@@ -820,7 +817,7 @@ struct Range {
     }
     __device__ __forceinline__ Range() : q0(0), nq(0), k0(0), nk(0) {}
     __device__ __forceinline__ uint32_t tiles(int G, int tm) const {
-        return static_cast<uint32_t>((static_cast<int64_t>(nq) * G + tm - 1) / tm);
+        return (static_cast<uint32_t>(nq) * G + tm - 1) / tm;
     }
     __device__ __forceinline__ void from_lane(int lane) {
         q0 = __builtin_amdgcn_readlane(q0, lane);
@@ -899,7 +896,7 @@ void attn_prompt_kernel(PromptArgs a) {
     ATTN_LDS;
     const int lane = threadIdx.x & 63;
     int hk, rank;
-    head_rank(blockIdx.x, a.Hkv, a.tiles, hk, rank);
+    head_rank(a, blockIdx.x, hk, rank);
     const int G = a.Hq / a.Hkv;
     Range at;
     const int rt = __builtin_amdgcn_readfirstlane(find_tile<C::TM>(a, G, rank, at));
@@ -907,17 +904,17 @@ void attn_prompt_kernel(PromptArgs a) {
     at.from_lane(0);
     const int q0 = at.q0, nq = at.nq, k0 = at.k0, nk = at.nk;
 
-    const int64_t rows = static_cast<int64_t>(nq) * G;
-    const int64_t r = static_cast<int64_t>(rt) * C::TM + wave_row<C>() + (lane & 31);
+    const int rows = nq * G, r = rt * C::TM + wave_row<C>() + (lane & 31);
     const bool live = r < rows;
-    const int i = static_cast<int>(r / G), g = static_cast<int>(r - static_cast<int64_t>(i) * G);
+    int g;
+    const int i = a.by_group.divide(r, g);
     const uint16_t* q = live ? a.q + static_cast<int64_t>(q0 + i) * a.q_stride + static_cast<int64_t>(hk * G + g) * a.D : nullptr;
     // ends aligned: row i sees key j <= i + nk - nq
     const int klim = a.causal ? min(max(i + 1 + nk - nq, 0), nk) : nk;
     int kend = nk;
     if (a.causal) {
-        const int64_t lastr = min(static_cast<int64_t>(rt + 1) * C::TM, rows) - 1;
-        kend = min(max(static_cast<int>(lastr / G) + 1 + nk - nq, 0), nk);
+        int rest;
+        kend = min(max(a.by_group.divide(min((rt + 1) * C::TM, rows) - 1, rest) + 1 + nk - nq, 0), nk);
     }
     PackedKeys keys;
     keys.k = a.k + static_cast<int64_t>(k0) * a.k_stride + static_cast<int64_t>(hk) * a.D;
@@ -948,9 +945,11 @@ void attn_shared_kernel(SharedArgs a) {
     // (head, split) fastest: the row tiles that read the same keys are Hkv *
     // splits apart, on one XCD when that is a multiple of 8
     const int splits = prefix ? a.prefix_splits : a.suffix_splits;
-    const int pair = id % (a.Hkv * splits), rest = id / (a.Hkv * splits);
-    const int hk = pair / splits, split = pair % splits;
-    const int tile = prefix ? rest : rest % a.suffix_tiles, b = prefix ? 0 : rest / a.suffix_tiles;
+    int pair, split, tile, b = 0;
+    const int rest = (prefix ? a.by_prefix_pairs : a.by_suffix_pairs).divide(id, pair);
+    const int hk = (prefix ? a.by_prefix_splits : a.by_suffix_splits).divide(pair, split);
+    if (prefix) tile = rest;
+    else b = a.by_suffix_tiles.divide(rest, tile);
 
     const int lane = threadIdx.x & 63;
     const int G = a.Hq / a.Hkv;
@@ -972,13 +971,16 @@ void attn_shared_kernel(SharedArgs a) {
     const int rows = (prefix ? a.B : 1) * a.L * G;
     const int r = tile * C::TM + wave_row<C>() + (lane & 31);
     const bool live = r < rows;
-    const int tok = r / G, g = r - tok * G;
+    int g;
+    const int tok = a.by_group.divide(r, g);
     const int64_t token = static_cast<int64_t>(b) * a.L + tok;    // of B * L
     const int head = hk * G + g;
     const uint16_t* q = live ? a.q + token * a.q_stride + static_cast<int64_t>(head) * a.D : nullptr;
     int klim = keys.n;
     if (a.causal && !prefix) klim = keys.n_prefix + min(max(tok + 1 + ns - a.L, 0), ns);
-    const int steps = (keys.n + C::ST - 1) / C::ST, per = (steps + splits - 1) / splits;
+    int unused;
+    const int steps = (keys.n + C::ST - 1) / C::ST;
+    const int per = (prefix ? a.by_prefix_splits : a.by_suffix_splits).divide(steps + splits - 1, unused);
     const int k0 = min(split * per * C::ST, keys.n), k1 = min((split + 1) * per * C::ST, keys.n);
     State<C> st;
     attend<C>(keys, q, klim, k0, k1, a.D, a.c, b0, b1, b2, b3, st);
@@ -1053,8 +1055,9 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
     uint2 w;
     w.x = f32x2_to_bf16x2(o.x * inv, o.y * inv);
     w.y = f32x2_to_bf16x2(o.z * inv, o.w * inv);
-    const int64_t token = row / a.Hq;
-    *reinterpret_cast<uint2*>(a.out + token * a.out_stride + (row - token * a.Hq) * a.D + ch) = w;
+    int head;
+    const int token = a.by_q_heads.divide(static_cast<int>(row), head);
+    *reinterpret_cast<uint2*>(a.out + token * a.out_stride + head * a.D + ch) = w;
 }
 
 constexpr int kComputeUnits = 256;
@@ -1092,6 +1095,8 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     while (tm > 32 && (2 * rows <= static_cast<int64_t>(a.B) * tm || fits(tm / 2))) tm /= 2;
     // every sequence ends in at most one partial tile
     a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
+    a.by_group = Divisor(a.Hq / a.Hkv);
+    a.by_heads = Divisor(a.Hkv % 8 == 0 ? a.tiles : a.Hkv);
     auto run = [&](auto cfg) {
         attn_prompt_kernel<decltype(cfg)><<<a.tiles * a.Hkv, kAThreads, 0, s>>>(a);
         return hipGetLastError();
@@ -1149,6 +1154,13 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     a.suffix_splits = static_cast<int>(p.suffix_splits);
     a.suffix_tiles = static_cast<int>(p.suffix_tiles);
     a.parts = static_cast<int>(p.parts);
+    a.by_group = Divisor(a.Hq / a.Hkv);
+    a.by_q_heads = Divisor(a.Hq);
+    a.by_prefix_pairs = Divisor(a.Hkv * p.prefix_splits);
+    a.by_prefix_splits = Divisor(p.prefix_splits);
+    a.by_suffix_pairs = Divisor(a.Hkv * p.suffix_splits);
+    a.by_suffix_splits = Divisor(p.suffix_splits);
+    a.by_suffix_tiles = Divisor(p.suffix_tiles);
     uint8_t* w = static_cast<uint8_t*>(ws) + 256;
     a.part_ml = reinterpret_cast<float*>(w);
     a.part_o = reinterpret_cast<float*>(w + p.ml_bytes);

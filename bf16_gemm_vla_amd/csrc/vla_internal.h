@@ -43,6 +43,31 @@ struct RopeArgs {
 };
 hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s);
 
+// Division of 32-bit numbers by a number that the launch knows, in three
+// instructions (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994: the unsigned form, right for every numerator).  The
+// compiler's own division takes about 25, and one that starts a workgroup is
+// bound by its length.
+struct Divisor {
+    uint32_t d, mul, sh1, sh2;
+    Divisor() = default;
+    explicit Divisor(int64_t by) : d(static_cast<uint32_t>(by > 0 ? by : 1)) {
+        uint32_t l = 0;
+        while ((uint64_t(1) << l) < d) ++l;
+        mul = static_cast<uint32_t>(((((uint64_t(1) << l) - d) << 32) / d) + 1);
+        sh1 = l ? 1 : 0;
+        sh2 = l ? l - 1 : 0;
+    }
+#ifdef __HIPCC__
+    __device__ __forceinline__ int divide(int n, int& rest) const {   // n >= 0
+        const uint32_t t = __umulhi(mul, static_cast<uint32_t>(n));
+        const uint32_t q = (t + ((static_cast<uint32_t>(n) - t) >> sh1)) >> sh2;
+        rest = n - static_cast<int>(q * d);
+        return static_cast<int>(q);
+    }
+#endif
+};
+
 struct PromptArgs {
     const uint16_t *q, *k, *v;
     const int32_t *cu_q, *cu_k;
@@ -50,7 +75,9 @@ struct PromptArgs {
     int64_t q_stride, k_stride, v_stride, out_stride;
     int B, total_q, total_k, Hq, Hkv, D, causal;
     float c;                                   // scale * log2(e)
-    int tiles;                                 // set by the launcher: most row tiles per key/value head
+    // set by the launcher
+    int tiles;                                 // most row tiles per key/value head
+    Divisor by_group, by_heads;                // query heads per key/value head; key/value heads, or the tiles
 };
 hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s);
 
@@ -66,6 +93,7 @@ struct SharedArgs {
     uint32_t num_pages;
     // set by the launcher
     int merged, prefix_items, prefix_splits, suffix_splits, suffix_tiles, parts;
+    Divisor by_group, by_q_heads, by_prefix_pairs, by_prefix_splits, by_suffix_pairs, by_suffix_splits, by_suffix_tiles;
     float *part_ml, *part_o;
 };
 // Launch plan of a shared-prefix call, from its host sizes alone.
