@@ -1144,7 +1144,7 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     p.parts = p.prefix_splits + p.suffix_splits;
     const int64_t rows = B * L * Hq;
     p.ml_bytes = p.parts > 1 ? ceil_div(rows * p.parts * 8, 256) * 256 : 0;
-    p.ws_bytes = 256 + p.ml_bytes + (p.parts > 1 ? rows * p.parts * D * 4 : 0);
+    p.ws_bytes = p.parts > 1 ? p.ml_bytes + rows * p.parts * D * 4 : 256;
     return p;
 }
 
@@ -1161,7 +1161,7 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     a.by_suffix_pairs = Divisor(a.Hkv * p.suffix_splits);
     a.by_suffix_splits = Divisor(p.suffix_splits);
     a.by_suffix_tiles = Divisor(p.suffix_tiles);
-    uint8_t* w = static_cast<uint8_t*>(ws) + 256;
+    uint8_t* w = static_cast<uint8_t*>(ws);
     a.part_ml = reinterpret_cast<float*>(w);
     a.part_o = reinterpret_cast<float*>(w + p.ml_bytes);
     const bool wide = (static_cast<uint64_t>(a.num_pages) << a.page_log2) * a.Hkv * a.D * 2 > kNoOffset;

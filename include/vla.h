@@ -221,7 +221,10 @@ int vla_gate_residual_ada_norm(const uint16_t *residual, const uint16_t *out, co
  *   (a, b) -> (a c - b s, b c + a s) for pair j,
  *   c, s = rot_scale * cos, sin (positions[t] * inv_freq[j])
  *   k_cache[slots[t]] = the rotated k row, v_cache[slots[t]] = the v row.
- * fp64 angles, mean squares; fp32 products; each output rounded to bf16 once.
+ * Angles are reduced to one revolution in fp64, their sine and cosine are
+ * fp32 (off by at most 2^-22), as are mean squares and products; a row whose
+ * mean square leaves 1e-30 .. 1e30 has it summed again in fp64.  Each output
+ * is rounded to bf16 once.
  * Scaling for long contexts is in inv_freq and rot_scale.
  *   q, k, v      device bf16, T rows of Hq, Hkv, Hkv heads; v is read only by
  *                the append and must be NULL without it;
@@ -261,15 +264,17 @@ int vla_qk_norm_rope_append(const uint16_t *q, const uint16_t *k, const uint16_t
  *   cu_k      device int32[B + 1], or NULL: the same as cu_q;
  *   out       device bf16, total_q rows; rows in no sequence stay as they were;
  *   scale     finite and > 0, causal 0 or 1 (VLA_EINVAL).
- * B in 1 .. 2^20, total_q and total_k in 1 .. 2^30. */
+ * B in 1 .. 2^20, total_q and total_k in 1 .. 2^30, total_q * Hq / Hkv below
+ * 2^31 - 128 (VLA_ESHAPE). */
 int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                     const int32_t *cu_k, uint16_t *out, int64_t B, int64_t total_q, int64_t total_k, int64_t Hq,
                     int64_t Hkv, int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
                     int64_t out_stride, int causal, float scale, void *stream);
 
 /* Attention of L query rows for each of B sequences over the cache.  Every
- * sequence sees the shared prefix, whose keys are read once for the whole
- * batch, and then its own suffix:
+ * sequence sees the shared prefix (where the sequences have few rows each, its
+ * keys are read for the rows of the whole batch at once) and then its own
+ * suffix:
  *   keys of sequence b = prefix rows 0 .. P-1, suffix rows 0 .. n_b-1,
  * prefix row j in page prefix_pages[j / page_size], suffix row j in page
  * block_table[b][j / page_size].  causal: row i of L sees suffix rows
@@ -287,9 +292,9 @@ int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, con
  *                 pages_per_seq == 0.  One of the two must be there;
  *   ws            device workspace of vla_attn_shared_prefix_workspace_bytes
  *                 (capacities = n_prefix_pages * page_size and pages_per_seq *
- *                 page_size), ZERO-FILLED before its first use; every
- *                 completed call leaves it ready for the next, of any shape.
- *                 Calls that overlap in time must not share it;
+ *                 page_size): parts of rows between the call's launches.
+ *                 What it holds before the call does not matter.  Calls that
+ *                 overlap in time must not share it;
  *   page_size     a power of two, 1 .. 65536 (VLA_ESHAPE).
  * The lengths are read on the device: a captured call follows them.  Results
  * depend on the call's sizes and lengths alone: repeated calls are bitwise

@@ -72,6 +72,12 @@ def test_prompt_refuses(change, code):
     refused("vla_attn_prompt", prompt_args(**change), code)
 
 
+def test_prompt_refuses_rows_past_31_bits():
+    """A key/value head's rows (tokens times query heads per key/value head) are numbered in 31 bits."""
+    few = dict(total_q=(1 << 22), total_k=12, Hq=512, Hkv=1, D=8, q_stride=4096, k_stride=8, v_stride=8, out_stride=4096)
+    refused("vla_attn_prompt", prompt_args(**few), ESHAPE, "too many")
+
+
 def shared_args(**change):
     names = ["q", "k_cache", "v_cache", "prefix_pages", "prefix_len", "block_table", "seq_lens", "out", "ws"]
     a = {n: A + i * GB for i, n in enumerate(names)}

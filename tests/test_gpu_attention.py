@@ -409,6 +409,19 @@ def test_shared_many_rows(hq, hkv, D):
     run_shared(2, 3, hq, hkv, D, 16, 70, [3, 9], True, seed=560 + D)
 
 
+def test_shared_workspace_needs_no_clearing():
+    """What the workspace held before has no part in the result, not even in rows without keys."""
+    for causal, lens in ((True, [0, 600, 3]), (False, [1, 40, 0])):
+        n = vla.vla_attn_shared_prefix_workspace_bytes(3, 2, 8, 2, 128, 304, 608)
+        kw = dict(pages_per_seq=38, n_prefix_pages=19, seed=615)
+        clean, _, _ = run_shared(3, 2, 8, 2, 128, 16, 300, lens, causal, ws=Guarded(n, fill=0), **kw)
+        dirty, _, _ = run_shared(3, 2, 8, 2, 128, 16, 300, lens, causal, ws=Guarded(n, fill=0xFF), **kw)
+        assert np.array_equal(clean, dirty)
+    n = vla.vla_attn_shared_prefix_workspace_bytes(2, 1, 4, 2, 64, 0, 640)
+    got, _, _ = run_shared(2, 1, 4, 2, 64, 16, 0, [0, 640], True, pages_per_seq=40, seed=618, ws=Guarded(n, fill=0xFF))
+    assert not got[0].any()
+
+
 def test_shared_edges():
     # no key at all, rows before the first suffix key, lengths past the capacity, capacity past the lengths
     got, _, _ = run_shared(2, 2, 4, 2, 64, 16, 0, [0, 40], True, pages_per_seq=3, seed=601)
