@@ -1,6 +1,6 @@
 // C ABI of the library: argument validation, status codes and the
-// gated-MLP chain handle (HIP graph capture / replay).  Kernels live in
-// codec.hip and gemm.hip; nothing here allocates device memory.
+// gated-MLP chain handle (HIP graph capture / replay).  Kernels live in the
+// .hip files beside it; nothing here allocates device memory.
 #include <hip/hip_runtime.h>
 
 #include <atomic>

@@ -21,7 +21,11 @@
 // neither overflow nor vanish.  Each output is rounded to bf16 once, from fp32.
 // The kernel is bound by HBM on prompts and by latency on single tokens: a
 // wave's loads of a head go out before the angles, and before the previous
-// head's arithmetic.
+// head's arithmetic.  Measured: 16387 tokens of 32 heads on 8 of 128, appended
+// and kept, 90 us (4.85 TB/s, where a copy reaches 5.14); 2049 tokens of 28 on
+// 4 of 128, normed, 12.7 us (3.1 TB/s: one wave start and one pass over the
+// angles are a good part of it); 50 tokens of 8 on 1 of 256 3.9 us and one
+// token 3.5 us, the time of a launch.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -208,7 +212,8 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
 }  // namespace
 
 hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s) {
-    // 16-byte words where whole pairs of them fit the head and its rotated part
+    // 16-byte words where whole pairs of them fit the head and its rotated
+    // part (16387 tokens as above: 90 us, 8-byte words 97)
     const int vec = (a.D % 16 == 0 && a.rot % 16 == 0) ? 8 : 4;
     const int units = a.D / (2 * vec);
     a.gw_log2 = 0;
@@ -217,7 +222,9 @@ hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s) {
     const int hpw = 64 >> a.gw_log2;
     const int steps = (a.Hq + 2 * a.Hkv + hpw - 1) / hpw;    // wave steps of one token
     // one wave per step while that fills the GPU's 1024 SIMDs some 8 times
-    // over, then one wave per token, which computes its angles once
+    // over, then one wave per token, which computes its angles once (300
+    // tokens of 8 heads on 1 of 256: 3.8 us, one wave per token 5.0; 16387
+    // tokens as above: 90 us, one wave per step 94)
     int64_t chunks = (8192 + a.T - 1) / a.T;
     if (chunks > steps) chunks = steps;
     a.steps = static_cast<int>((steps + chunks - 1) / chunks);
