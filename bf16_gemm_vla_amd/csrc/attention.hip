@@ -693,47 +693,62 @@ __device__ __forceinline__ int wave_row() {
 }
 
 // Writes the workgroup's rows: through LDS, so that a row goes out as one run
-// of 16-byte words; the KG key parts' results for the same rows are joined on
-// the way (k-th of them: with_keys > k says that it had keys).  PART false: O / l
+// of 16-byte words.  The KG key parts' results for the same rows are scaled to
+// their common maximum first and only added on the way.  PART false: O / l
 // rounded to bf16 (0 for a row without keys) at address `to` of the lane's
 // row; PART true: row number to - 1 of part_ml (maximum, sum) and part_o (O,
-// fp32, nothing for a row without keys).  to 0: the lane has no row.
+// fp32).  to 0: the lane has no row.
 template <class C, bool PART>
-__device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, float* part_ml, float* part_o, int with_keys, int D,
+__device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, float* part_ml, float* part_o, int D,
                                            uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, float (*ml)[2][32],
                                            uint64_t (*row_at)[32]) {
     const int lane = threadIdx.x & 63, l32 = lane & 31, g2 = lane >> 5;
     const Part<C> part;
     constexpr int ROW = C::DP * 4;                                // bytes; 16-byte chunk c of row r at c ^ r
-    // row r of (row group, key part) a; a buffer holds PER such sets of 32
-    // rows, or half of one
+    // row r of (row group, key part) a; a buffer holds PER such sets of 32 rows
     constexpr int PER = C::BUF / (32 * ROW);
+    static_assert(PER > 0, "whole sets");
     auto place = [&](int a, int r) __attribute__((always_inline)) -> uint8_t* {
-        const int at = PER > 0 ? a / (PER > 0 ? PER : 1) : 2 * a + (r >> 4);
-        const int in = PER > 0 ? a % (PER > 0 ? PER : 1) * 32 + r : r & 15;
-        return (at == 0 ? b0 : (at == 1 ? b1 : (at == 2 ? b2 : b3))) + in * ROW;
+        const int at = a / PER;
+        return (at == 0 ? b0 : (at == 1 ? b1 : (at == 2 ? b2 : b3))) + (a % PER * 32 + r) * ROW;
     };
-    static_assert(PER > 0 || C::BUF == 16 * ROW, "half a set");
     const int set = part.qg + part.kg * C::QG;
-    wait_here<kWaitAll>();
-    __syncthreads();                                              // every wave is past its last keys
-    {
-        uint8_t* const a = place(set, l32);
-        if (part.kg < with_keys) {
-#pragma unroll
-            for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const f32x4_t v = {st.acc[d][4 * x], st.acc[d][4 * x + 1], st.acc[d][4 * x + 2], st.acc[d][4 * x + 3]};
-                    *reinterpret_cast<f32x4_t*>(a + (((8 * (d + part.hv * C::ND) + 2 * x + g2) ^ l32) & (C::DP / 4 - 1)) * 16) = v;
-                }
-        }
-        if (g2 == 0 && part.hv == 0) {
+    if (g2 == 0 && part.hv == 0) {
+        if constexpr (C::KG > 1) {
             ml[set][0][l32] = st.m;
             ml[set][1][l32] = st.l;
-            row_at[set][l32] = to;
         }
+        if (part.kg == 0) row_at[part.qg][l32] = to;
     }
+    wait_here<kWaitAll>();
+    __syncthreads();                                              // every wave is past its last keys
+    float m = st.m, l = st.l, f = 1.0f;
+    if constexpr (C::KG > 1) {
+        float mk[C::KG];
+#pragma unroll
+        for (int k = 0; k < C::KG; ++k) {
+            mk[k] = ml[part.qg + k * C::QG][0][l32];
+            m = fmaxf(m, mk[k]);
+        }
+        l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C::KG; ++k) l += ml[part.qg + k * C::QG][1][l32] * (mk[k] == m ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - m));
+        f = st.m == m ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
+    }
+    if constexpr (PART) {
+        if (g2 == 0 && part.hv == 0 && part.kg == 0 && to != 0)
+            *reinterpret_cast<float2*>(part_ml + 2 * static_cast<int64_t>(to - 1)) = make_float2(m, l);
+    } else {
+        f *= l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);        // NaN stays NaN
+    }
+    uint8_t* const mine = place(set, l32);
+#pragma unroll
+    for (int d = 0; d < C::ND; ++d)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const f32x4_t v = {st.acc[d][4 * x], st.acc[d][4 * x + 1], st.acc[d][4 * x + 2], st.acc[d][4 * x + 3]};
+            *reinterpret_cast<f32x4_t*>(mine + (((8 * (d + part.hv * C::ND) + 2 * x + g2) ^ l32) & (C::DP / 4 - 1)) * 16) = v * f;
+        }
     __syncthreads();
     // the waves of a row group write its 32 rows, 8 channels per lane.  Many
     // passes stay a loop: code that runs once per workgroup is bound by its
@@ -745,38 +760,23 @@ __device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, floa
     for (int pass = 0; pass < PASSES; ++pass) {
         const int row = (pass * WPG + part.wave / C::QG) * RPW + lane / GROUPS;
         const uint64_t dst = row_at[part.qg][row];
-        float mk[C::KG], m = -__builtin_inff(), l = 0.0f;
+        f32x4_t o[2];
 #pragma unroll
-        for (int k = 0; k < C::KG; ++k) {
-            mk[k] = ml[part.qg + k * C::QG][0][row];
-            m = fmaxf(m, mk[k]);
+        for (int x = 0; x < 2; ++x) {
+            const int at = (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16;
+            o[x] = *reinterpret_cast<const f32x4_t*>(place(part.qg, row) + at);
+#pragma unroll
+            for (int k = 1; k < C::KG; ++k) o[x] += *reinterpret_cast<const f32x4_t*>(place(part.qg + k * C::QG, row) + at);
         }
-        f32x4_t o[2] = {f32x4_t{}, f32x4_t{}};
-#pragma unroll
-        for (int k = 0; k < C::KG; ++k) {
-            const float f = mk[k] == m ? 1.0f : __builtin_amdgcn_exp2f(mk[k] - m);
-            l += ml[part.qg + k * C::QG][1][row] * f;
-            if (k < with_keys) {
-                const uint8_t* const a = place(part.qg + k * C::QG, row);
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    o[x] += *reinterpret_cast<const f32x4_t*>(a + (((2 * cg + x) ^ row) & (C::DP / 4 - 1)) * 16) * f;
-            }
-        }
-        const bool store = dst != 0 && cg * 8 < D;
+        if (dst == 0 || cg * 8 >= D) continue;
         if constexpr (PART) {
-            const int64_t at = static_cast<int64_t>(dst - 1);
-            if (store && cg == 0) *reinterpret_cast<float2*>(part_ml + 2 * at) = make_float2(m, l);
-            if (store && m != -__builtin_inff()) {
-                f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + at * D + cg * 8);
-                p[0] = o[0];
-                p[1] = o[1];
-            }
+            f32x4_t* const p = reinterpret_cast<f32x4_t*>(part_o + static_cast<int64_t>(dst - 1) * D + cg * 8);
+            p[0] = o[0];
+            p[1] = o[1];
         } else {
-            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // NaN stays NaN
-            const f32x4_t x = o[0] * inv, y = o[1] * inv;
-            const u32x4_t w = {f32x2_to_bf16x2(x.x, x.y), f32x2_to_bf16x2(x.z, x.w), f32x2_to_bf16x2(y.x, y.y), f32x2_to_bf16x2(y.z, y.w)};
-            if (store) *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
+            const u32x4_t w = {f32x2_to_bf16x2(o[0].x, o[0].y), f32x2_to_bf16x2(o[0].z, o[0].w),
+                               f32x2_to_bf16x2(o[1].x, o[1].y), f32x2_to_bf16x2(o[1].z, o[1].w)};
+            *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(dst) + cg * 8) = w;
         }
     }
 }
@@ -935,8 +935,7 @@ void attn_prompt_kernel(PromptArgs a) {
     State<C> st;
     attend<C>(keys, q, klim, 0, kend, a.D, a.c, b0, b1, b2, b3, st);
     uint16_t* const out = a.out + static_cast<int64_t>(q0 + i) * a.out_stride + static_cast<int64_t>(hk * G + g) * a.D;
-    write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, (kend + 31) / 32, a.D, b0, b1, b2, b3,
-                         ml, row_at);
+    write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, a.D, b0, b1, b2, b3, ml, row_at);
 }
 
 // ----------------------------------------------------------- shared prefix
@@ -994,13 +993,12 @@ void attn_shared_kernel(SharedArgs a) {
     const int k0 = min(split * per * C::ST, keys.n), k1 = min((split + 1) * per * C::ST, keys.n);
     State<C> st;
     attend<C>(keys, q, klim, k0, k1, a.D, a.c, b0, b1, b2, b3, st);
-    const int waves = (k1 - k0 + 31) / 32;
     if (a.parts == 1) {
         uint16_t* const out = a.out + token * a.out_stride + static_cast<int64_t>(head) * a.D;
-        write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, waves, a.D, b0, b1, b2, b3, ml, row_at);
+        write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, a.D, b0, b1, b2, b3, ml, row_at);
     } else {
         const int64_t at = (token * a.Hq + head) * a.parts + (prefix ? 0 : a.prefix_splits) + split;
-        write_rows<C, true>(st, live ? static_cast<uint64_t>(at) + 1 : 0, a.part_ml, a.part_o, waves, a.D, b0, b1, b2, b3, ml, row_at);
+        write_rows<C, true>(st, live ? static_cast<uint64_t>(at) + 1 : 0, a.part_ml, a.part_o, a.D, b0, b1, b2, b3, ml, row_at);
     }
 }
 
