@@ -205,15 +205,10 @@ struct Walk {
         const int lane = threadIdx.x & 63;
         l32 = lane & 31;
         g2 = lane >> 5;
-        kfull = live ? klim : INT_MAX;
-        kmax = live ? klim : 0;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) {
-            kfull = min(kfull, __shfl_xor(kfull, o, 64));
-            kmax = max(kmax, __shfl_xor(kmax, o, 64));
-        }
-        kfull = __builtin_amdgcn_readfirstlane(kfull);
-        kmax = __builtin_amdgcn_readfirstlane(kmax);
+        // live rows come first, and no row sees fewer keys than the one before
+        const int rows = __builtin_popcount(static_cast<uint32_t>(__ballot(live)));
+        kfull = rows ? __builtin_amdgcn_readlane(klim, 0) : INT_MAX;
+        kmax = rows ? __builtin_amdgcn_readlane(klim, rows - 1) : 0;
 #pragma unroll
         for (int i = 0; i < C::ND; ++i) st.acc[i] = f32x16_t{};
         st.m = -__builtin_inff();
