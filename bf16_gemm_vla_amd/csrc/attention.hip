@@ -38,8 +38,10 @@
 // ms); a sub-tile's exponentials and the exchange of maxima stand between its
 // two products and are covered by the other wave of the SIMD (up to 128
 // channels) or not at all (256).  One token over 131071 keys streams the cache
-// at 4.9 TB/s.  Small calls (50 rows 7.2 us, 10 rows over 778 cached keys 11.5
-// us) are bound by the start and the end of a workgroup.
+// at 4.9 TB/s.  Small calls (50 rows 6.2 us, 10 rows over 778 cached keys 10.4
+// us) are bound by the chain of a workgroup: its arguments and lengths, its
+// first loads, one step, its results.  Two figures beside a rule below were
+// measured side by side when the rule was made.
 #include <hip/hip_runtime.h>
 
 #include <climits>
@@ -553,7 +555,7 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         w.template weights<C::SUBS == 2 ? 0 : C::NI>(sc, pw, load_more);
         if (!w.put_off(vt, key0)) w.add(vt, pw);
     };
-    auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s) __attribute__((always_inline)) {
+    auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s, auto more) __attribute__((always_inline)) {
         // this wave's loads of stage s have landed and its reads of stage s-1
         // are done; the barrier says so for every wave
         wait_here<kWaitAll>();
@@ -561,16 +563,22 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
         __builtin_amdgcn_sched_barrier(0);
         const int key0 = k0 + s * C::ST;
-        // the next stage's loads (past the last stage: zeros) go out among
-        // this one's scores and, with one sub-tile per stage, its weights
-        const Source k = w.template source<false>(key0 + C::ST + row0, k1), v = w.template source<true>(key0 + C::ST + row0, k1);
-        slot = slot_of(s + 1, page);
-        const Slots sl = w.slots_of(slot, row0);
-        if constexpr (W::PAGED) __builtin_amdgcn_sched_barrier(0);   // the exchanges together, not one wait among the products each
-        const uint64_t vnext = valid(slot);
-        page = entry(s + 2);
-        auto load_k = [&](int i) __attribute__((always_inline)) { w.template load<false>(k, sl, kn + row0 * C::RB, row0, i); };
-        auto load_v = [&](int i) __attribute__((always_inline)) { w.template load<true>(v, sl, vn + row0 * C::RB, row0, i); };
+        // the next stage's loads go out among this one's scores and, with one
+        // sub-tile per stage, its weights
+        Source k, v;
+        Slots sl;
+        uint64_t vnext = 0;
+        if constexpr (more()) {
+            k = w.template source<false>(key0 + C::ST + row0, k1);
+            v = w.template source<true>(key0 + C::ST + row0, k1);
+            slot = slot_of(s + 1, page);
+            sl = w.slots_of(slot, row0);
+            if constexpr (W::PAGED) __builtin_amdgcn_sched_barrier(0);   // the exchanges together, not one wait among the products each
+            vnext = valid(slot);
+            page = entry(s + 2);
+        }
+        auto load_k = [&](int i) __attribute__((always_inline)) { if constexpr (more()) w.template load<false>(k, sl, kn + row0 * C::RB, row0, i); };
+        auto load_v = [&](int i) __attribute__((always_inline)) { if constexpr (more()) w.template load<true>(v, sl, vn + row0 * C::RB, row0, i); };
         if constexpr (C::SUBS == 2) {
             sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur), load_k, [](int) {});
             sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32), load_v, [](int) {});
@@ -580,10 +588,11 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         }
         vcur = vnext;
     };
-    for (int s = 0; s < n_stages; s += 2) {
-        step(kb0, vb0, kb1, vb1, s);
-        if (s + 1 < n_stages) step(kb1, vb1, kb0, vb0, s + 1);
+    for (int s = 0; s + 1 < n_stages; s += 2) {
+        step(kb0, vb0, kb1, vb1, s, std::true_type{});
+        if (s + 2 < n_stages) step(kb1, vb1, kb0, vb0, s + 1, std::true_type{});
     }
+    step(n_stages % 2 ? kb0 : kb1, n_stages % 2 ? vb0 : vb1, nullptr, nullptr, n_stages - 1, std::false_type{});
     st.l = half_sum(st.l);
     w.add_late(q, k1, [&](int key) {
         const int t = key - k0;
