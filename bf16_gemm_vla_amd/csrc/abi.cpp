@@ -722,6 +722,15 @@ int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
 }
 
+namespace {
+// The kernels work with scale * log2(e).
+int check_scale(const char* fn, float scale) {
+    if (!std::isfinite(scale) || scale <= 0.0f || !std::isfinite(scale * 1.4426950408889634f))
+        return fail(VLA_EINVAL, fn, "scale must be finite and > 0, and finite times log2(e)");
+    return VLA_OK;
+}
+}  // namespace
+
 int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, const int32_t* cu_q,
                     const int32_t* cu_k, uint16_t* out, int64_t B, int64_t total_q, int64_t total_k, int64_t Hq,
                     int64_t Hkv, int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -743,7 +752,7 @@ int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, con
     if (int rc = check_stride(fn, "v_stride", v_stride, Hkv * D)) return rc;
     if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
     if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
-    if (!std::isfinite(scale) || scale <= 0.0f) return fail(VLA_EINVAL, fn, "scale must be finite and > 0");
+    if (int rc = check_scale(fn, scale)) return rc;
     // row tiles of at least 32 rows, at most one ragged one per sequence
     if (total_q * (Hq / Hkv) >= (int64_t(1) << 31) - 128 || (total_q * (Hq / Hkv) / 32 + B) * Hkv >= (int64_t(1) << 31))
         return fail(VLA_ESHAPE, fn, "total_q=%lld rows of %lld heads are too many", (long long)total_q, (long long)Hq);
@@ -771,8 +780,10 @@ int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, 
     if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
     if (prefix_cap < 0 || suffix_cap < 0 || prefix_cap + suffix_cap == 0)
         return fail(VLA_EINVAL, fn, "a prefix or a suffix must be there");
-    if (B > (int64_t(1) << 20) || L > (int64_t(1) << 20) || B * L * Hq >= (int64_t(1) << 31) ||
-        prefix_cap >= (int64_t(1) << 30) || suffix_cap >= (int64_t(1) << 30))
+    if (B > (int64_t(1) << 20) || L > (int64_t(1) << 20) || B * L * Hq >= (int64_t(1) << 31) - 128 ||
+        prefix_cap >= (int64_t(1) << 30) || suffix_cap >= (int64_t(1) << 30) ||
+        // key numbers, and those of the steps past the last key, stay below 2^31
+        prefix_cap + suffix_cap >= (int64_t(1) << 31) - (int64_t(1) << 16))
         return fail(VLA_ESHAPE, fn, "B=%lld L=%lld Hq=%lld or the capacities %lld, %lld too large", (long long)B, (long long)L,
                     (long long)Hq, (long long)prefix_cap, (long long)suffix_cap);
     return VLA_OK;
@@ -820,7 +831,7 @@ int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uin
     if (int rc = check_stride(fn, "q_stride", q_stride, Hq * D)) return rc;
     if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
     if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
-    if (!std::isfinite(scale) || scale <= 0.0f) return fail(VLA_EINVAL, fn, "scale must be finite and > 0");
+    if (int rc = check_scale(fn, scale)) return rc;
     const vla::SharedPlan p = vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_cap, suffix_cap);
     if (p.prefix_items + p.suffix_items >= (int64_t(1) << 31)) return fail(VLA_ESHAPE, fn, "too many work items");
     if (ws_bytes < static_cast<size_t>(p.ws_bytes))

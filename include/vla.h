@@ -263,7 +263,7 @@ int vla_qk_norm_rope_append(const uint16_t *q, const uint16_t *k, const uint16_t
  *   cu_q      device int32[B + 1], non-decreasing, cu_q[0] >= 0;
  *   cu_k      device int32[B + 1], or NULL: the same as cu_q;
  *   out       device bf16, total_q rows; rows in no sequence stay as they were;
- *   scale     finite and > 0, causal 0 or 1 (VLA_EINVAL).
+ *   scale     > 0, finite also times log2(e); causal 0 or 1 (VLA_EINVAL).
  * B in 1 .. 2^20, total_q and total_k in 1 .. 2^30, total_q * Hq / Hkv below
  * 2^31 - 128 (VLA_ESHAPE). */
 int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
@@ -298,7 +298,8 @@ int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, con
  *   page_size     a power of two, 1 .. 65536 (VLA_ESHAPE).
  * The lengths are read on the device: a captured call follows them.  Results
  * depend on the call's sizes and lengths alone: repeated calls are bitwise
- * equal.  B and L in 1 .. 2^20, B * L * Hq < 2^31, capacities < 2^30. */
+ * equal.  B and L in 1 .. 2^20, B * L * Hq < 2^31 - 128, capacities
+ * < 2^30 and together < 2^31 - 2^16 (VLA_ESHAPE). */
 size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
                                               int64_t prefix_capacity, int64_t suffix_capacity);
 int vla_attn_shared_prefix(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,

@@ -102,6 +102,22 @@ def test_shared_refuses(change, code):
     refused("vla_attn_shared_prefix", shared_args(**change), code)
 
 
+def test_shared_refuses_numbers_past_31_bits():
+    """Rows of a key/value head and keys of a sequence are numbered in 31 bits, steps past the last one included."""
+    half = (1 << 30) - 1
+    refused("vla_attn_shared_prefix", shared_args(page_size=1, n_prefix_pages=half, pages_per_seq=half), ESHAPE, "too large")
+    n = vla.vla_attn_shared_prefix_workspace_bytes
+    assert n(1, 1, 4, 2, 64, half, half) == 0 and n(1, 1, 4, 2, 64, half, 1 << 29) > 0
+    assert n(1 << 10, 1 << 9, 4095, 1, 8, 16, 16) > 0 and n((1 << 20) - 1, 1 << 10, 2, 1, 8, 16, 16) > 0
+    assert n(1 << 20, 1 << 10, 2, 1, 8, 16, 16) == 0
+
+
+@pytest.mark.parametrize("scale", [3e38, float("-inf"), -0.0])
+def test_scales_refused(scale):
+    refused("vla_attn_prompt", prompt_args(scale=scale), EINVAL, "scale")
+    refused("vla_attn_shared_prefix", shared_args(scale=scale), EINVAL, "scale")
+
+
 def test_shared_workspace_query():
     n = vla.vla_attn_shared_prefix_workspace_bytes
     assert n(3, 2, 4, 2, 64, 320, 64) > 0
