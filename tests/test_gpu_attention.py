@@ -565,6 +565,34 @@ def test_shared_tall_suffix_tiles(hq, hkv, D, B, L):
     run_shared(B, L, hq, hkv, D, 16, 70, [(L + 3 * b) if b else 0 for b in range(B)], True, seed=700 + D + B)
 
 
+def test_shared_long_chunk():
+    """A chunk of a prompt over the cache: many rows of few sequences, one of them without keys of its own."""
+    run_shared(2, 600, 32, 8, 72, 16, 45, [0, 650], True, seed=790)
+
+
+@pytest.mark.parametrize("hq,hkv,D,B,prefix", [(8, 1, 256, 20, 70), (8, 1, 256, 40, 0), (32, 8, 128, 20, 70), (16, 4, 64, 20, 33)])
+def test_shared_unseen_values_in_tall_tiles(hq, hkv, D, B, prefix):
+    """NaN in the second to last key and value of every sequence is seen by its last two rows alone."""
+    L, lens = 64, [64 + 5 * b for b in range(B)]
+    c = Cache(B, hkv, D, 16, prefix, lens, seed=650 + D)
+    q = rand(651, B * L, hq, D)
+    for b in range(B):
+        c.k[c.keys[b][-2]] = c.v[c.keys[b][-2]] = 0x7FC0
+    n = vla.vla_attn_shared_prefix_workspace_bytes(B, L, hq, hkv, D, c.npp * 16, c.pps * 16)
+    o, w = Guarded(B * L * hq * D * 2), zeros_ws(n)
+    vla.vla_attn_shared_prefix(dev(q), dev(c.k), dev(c.v), dev(c.prefix_pages) if prefix else None,
+                               dev(np.array([prefix], np.int32)) if prefix else None, dev(c.table),
+                               dev(np.array(lens, np.int32)), o.t, w, n, B, L, hq, hkv, D, c.pages, 16, c.npp,
+                               c.pps, hq * D, hq * D, True, 0.1)
+    o.check()
+    got = o.numpy(np.uint16).reshape(B, L, hq, D)
+    for b in range(B):
+        s, total = c.keys[b], len(c.keys[b])
+        lim = np.arange(L - 2) + 1 + total - L
+        assert_attention(got[b, :L - 2], q.reshape(B, L, hq, D)[b, :L - 2], c.k[s[:-2]], c.v[s[:-2]], lim, float(np.float32(0.1)))
+        assert np.isnan(bf16_f64(got[b, L - 2:])).all()
+
+
 @pytest.mark.parametrize("hq,hkv,D,B", [(64, 8, 64, 600), (64, 8, 128, 300), (8, 1, 256, 1100), (8, 1, 256, 2100)])
 def test_shared_many_single_tokens(hq, hkv, D, B):
     """64-row and 128-row tiles for the prefix, 32-row tiles for the suffixes."""
