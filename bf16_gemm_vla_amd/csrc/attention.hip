@@ -1096,7 +1096,7 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     // half (64 rows: two) times as many.  Measured with 128 / 64 / 32 rows:
     //   32 heads on 8 of 128, all keys: 450 tokens 18.5 / 13.3 / 12.0 us, 1024
     //   tokens 30 / 27 / 34, 1500 tokens 54 / 55 / 63; causal: 1024 tokens 30 /
-    //   21 / 25, 1500 tokens 42 / 36 / 40
+    //   21 / 25, 1500 tokens 42 / 36 / 40, 8191 tokens 575 / 640
     //   8 heads on 1 of 256, all keys: 800 tokens 36 / 25 / 21, 2048 tokens 71 /
     //   50 / 76, 2500 tokens 85 / 104 / 129; causal: 1500 tokens 56 / 37 / 31,
     //   3900 tokens 124 / 89 / 140
