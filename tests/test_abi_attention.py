@@ -135,3 +135,30 @@ def test_shared_workspace_query():
 def test_binding_raises():
     with pytest.raises(RuntimeError, match="vla_attn_prompt: .*scale"):
         vla.vla_attn_prompt(*[A + i * GB for i in range(6)], 1, 1, 1, 1, 1, 8, 8, 8, 8, 8, True, 0.0, stream=0)
+
+
+def test_refusals_under_asan_and_ubsan():
+    """The tests above against a build whose host code is instrumented: the
+    checks and the launch plans neither overflow nor read out of bounds."""
+    import glob
+    import os
+    import subprocess
+    import sys
+
+    from bf16_gemm_vla_amd import build as vla_build
+
+    runtime = sorted(glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so"))
+    if not runtime:
+        pytest.skip("clang's AddressSanitizer runtime is not installed")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    lib = vla_build.build(sanitize=True)
+    runner = ("import sys; sys.path.insert(0, %r)\n"
+              "import bf16_gemm_vla_amd._lib as L; L.LIB_PATH = %r\n"
+              "import pytest; sys.exit(pytest.main(['-q', '-x', '-p', 'no:cacheprovider', '-k', 'not asan', "
+              "'tests/test_abi_attention.py']))\n") % (root, lib)
+    env = dict(os.environ, LD_PRELOAD=runtime[-1], ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-c", runner], cwd=root, env=env, capture_output=True, text=True, timeout=900)
+    tail = (r.stdout + r.stderr)[-4000:]
+    assert r.returncode == 0, tail
+    assert "passed" in r.stdout and "ERROR: AddressSanitizer" not in tail and "runtime error" not in tail, tail
