@@ -150,7 +150,7 @@ struct PagedKeys {
 
 // A wave's partial result for its 32 rows: lane = row l % 32, O^T unnormalised,
 // m the running maximum in log2 units, l the sum of weights (of this lane's
-// keys until finish()).
+// keys until the walk's end).
 template <class C>
 struct State {
     f32x16_t acc[C::ND];
@@ -602,8 +602,8 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
 
 // Keys k0 .. k1-1 for 32 rows that the four waves share: wave w takes
 // sub-tiles w, w + 4, ...  Each wave's K and V have one place in LDS: K of
-// the next sub-tile goes out while this one's weights are formed, its V among
-// its scores, so 16 (D <= 64: 8) KiB per wave are in flight.
+// the next sub-tile goes out before this one's weights are formed, its V among
+// its scores, so up to 16 (D <= 64: 8) KiB per wave are in flight.
 template <class C, class Keys>
 __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                            uint8_t* kb_all, uint8_t* vb_all, State<C>& st) {
