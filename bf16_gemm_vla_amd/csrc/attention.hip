@@ -1140,6 +1140,11 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // tokens behind 8195 shared keys: apart 34 us, merged 114).
     p.merged = B == 1 || prefix_cap == 0 ||
                2 * B * ceil_div(rows_s, p.suffix_tm) * p.suffix_tm <= 3 * ceil_div(rows_p, p.prefix_tm) * p.prefix_tm;
+    // 64-row tiles for the prefix take the suffixes into their launch, 128-row
+    // ones would leave too much of theirs empty (single tokens behind a shared
+    // prefix: 600 of 32 heads on 8 of 128, 64 rows: 87 us, two launches 98;
+    // 2000, 128 rows: 287 us, two launches 241).
+    if (!p.merged && p.prefix_tm == 64) p.suffix_tm = 64;
     const int64_t keys_s = suffix_cap + (p.merged ? prefix_cap : 0);
     const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(D, p.prefix_tm));
     const int64_t steps_s = ceil_div(keys_s, step_keys(D, p.suffix_tm));
