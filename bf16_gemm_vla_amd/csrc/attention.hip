@@ -1143,7 +1143,8 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // 64-row tiles for the prefix take the suffixes into their launch, 128-row
     // ones would leave too much of theirs empty (single tokens behind a shared
     // prefix: 600 of 32 heads on 8 of 128, 64 rows: 87 us, two launches 98;
-    // 2000, 128 rows: 287 us, two launches 241).
+    // 2000, 128 rows: 287 us, two launches 241; 600 with 64 shared and up to
+    // 1500 own keys, 64 rows: 403 us, two launches 396).
     if (!p.merged && p.prefix_tm == 64) p.suffix_tm = 64;
     const int64_t keys_s = suffix_cap + (p.merged ? prefix_cap : 0);
     const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(D, p.prefix_tm));
