@@ -431,10 +431,13 @@ struct Walk {
     }
     // A zero weight times an infinity or NaN is not zero: a sub-tile that
     // some row sees only in part and whose V holds one is left out of the
-    // product and added at the end, key by key.  Bit b of `late` is the
-    // sub-tile that ends 32 b to 32 b + 31 keys past the last key that every
-    // row sees; a tile of at most 128 rows ends at most 128 + 31 keys past it.
+    // product and added at the end, key by key.  So is one that no row sees
+    // (the walk goes on for other waves' rows): there is nothing to add.  Bit b
+    // of `late` is the sub-tile that ends 32 b to 32 b + 31 keys past the last
+    // key that every row sees; 32 rows see at most 31 keys more than that, and
+    // a sub-tile that one of them sees ends at most 31 past those.
     __device__ __forceinline__ bool put_off(const uint8_t* vt, int key0) const {
+        if (key0 >= kmax) return true;
         if (key0 + 32 <= kfull || kfull == kmax || !has_nonfinite<C>(vt)) return false;
         st.late |= 1u << ((key0 + 32 - kfull) >> 5);
         return true;

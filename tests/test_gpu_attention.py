@@ -747,3 +747,81 @@ def test_layer_from_qkv_gemm_to_attention():
         got = out_bits(out, B, hq, D)
         for b in range(B):
             assert_attention(got[b:b + 1], q[b:b + 1], np.array(seen_k[b]), np.array(seen_v[b]), [lens[b]], 0.125, f"step {step}")
+
+
+# ------------------------------------------- infinities and NaN among the keys
+
+KINDS = (0x7FC0, 0x7F80, 0xFF80)          # NaN, +inf, -inf
+
+
+def poison_values(v, at):
+    """Value row at[j] is not finite in channel j; returns the clean copy."""
+    clean = v.copy()
+    assert len(set(int(x) for x in at)) == len(at) <= v.shape[2]
+    for j, key in enumerate(at):
+        v[key, :, j] = KINDS[j % 3]
+    return clean
+
+
+def assert_poisoned(got, q, k, clean, limits, scale, at, what=""):
+    """A row that sees key at[j] has that key's infinity or NaN in channel j;
+    everything else is as if the values were finite."""
+    limits = np.asarray(limits)
+    ref, tol = attention_bound(q, k, clean, limits, scale)
+    g = bf16_f64(got)
+    seen = np.zeros((len(limits), 1, k.shape[2]), bool)
+    for j, key in enumerate(at):
+        seen[:, 0, j] = limits > key
+        x = g[limits > key, :, j]
+        assert (np.isnan(x) if j % 3 == 0 else x == (np.inf if j % 3 == 1 else -np.inf)).all(), f"{what}: seen key {key}"
+    bad = ~(np.abs(g - ref) <= tol) & ~seen
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} outside, first {np.argwhere(bad)[0]}: {g[bad][0]} for {ref[bad][0]}"
+
+
+def poisoned_prompt(n, m, hq, hkv, D, causal, at, every=1, behind=0, seed=0):
+    """One sequence of n rows and m keys, `behind` rows of NaN after its keys."""
+    q, k, v = rand(seed, n, hq, D, scale=2.0), rand(seed + 1, m + behind, hkv, D), rand(seed + 2, m + behind, hkv, D)
+    clean = poison_values(v, at)
+    k[m:] = v[m:] = 0x7FC0
+    scale = float(np.float32(1 / math.sqrt(D)))
+    o = Guarded(n * hq * D * 2, fill=0x5A)
+    vla.vla_attn_prompt(dev(q), dev(k), dev(v), dev(offsets([n])), dev(offsets([m])), o.t, 1, n, m + behind, hq, hkv, D, hq * D,
+                        hkv * D, hkv * D, hq * D, causal, scale)
+    o.check()
+    lim = np.clip(np.arange(n) + 1 + m - n, 0, m) if causal else np.full(n, m)
+    s = slice(None, None, every)
+    assert_poisoned(o.numpy(np.uint16).reshape(n, hq, D)[s], q[s], k[:m], clean[:m], lim[s], scale, at)
+
+
+def poisoned_shared(L, hq, hkv, D, prefix, lens, at, every=1, page=16, seed=0):
+    """Causal rows over the cache; at counts a sequence's own keys, from its end if negative."""
+    B = len(lens)
+    c = Cache(B, hkv, D, page, prefix, lens, seed=seed)
+    q = rand(seed + 5, B * L, hq, D, scale=2.0)
+    clean, where = c.v.copy(), []
+    for b in range(B):
+        where.append([prefix + (a if a >= 0 else lens[b] + a) for a in at if -lens[b] <= a < lens[b]])
+        for j, key in enumerate(where[b]):
+            c.v[c.keys[b][key], :, j] = KINDS[j % 3]
+    scale = float(np.float32(1 / math.sqrt(D)))
+    n = vla.vla_attn_shared_prefix_workspace_bytes(B, L, hq, hkv, D, c.npp * page, c.pps * page)
+    o, w = Guarded(B * L * hq * D * 2, fill=0x5A), zeros_ws(n)
+    vla.vla_attn_shared_prefix(dev(q), dev(c.k), dev(c.v), dev(c.prefix_pages) if prefix else None,
+                               dev(np.array([prefix], np.int32)) if prefix else None, dev(c.table),
+                               dev(np.array(lens, np.int32)), o.t, w, n, B, L, hq, hkv, D, c.pages, page, c.npp, c.pps,
+                               hq * D, hq * D, True, scale)
+    o.check()
+    got, q = o.numpy(np.uint16).reshape(B, L, hq, D), q.reshape(B, L, hq, D)
+    s = slice(None, None, every)
+    for b in range(B):
+        lim = prefix + np.clip(np.arange(L) + 1 + lens[b] - L, 0, lens[b])
+        assert_poisoned(got[b, s], q[b, s], c.k[c.keys[b]], clean[c.keys[b]], lim[s], scale, where[b], f"sequence {b}")
+
+
+@pytest.mark.parametrize("hq,hkv,D,L,prefix", [
+    (8, 8, 64, 1200, 0), (2, 2, 64, 1200, 0), (40, 40, 64, 1200, 0), (4, 4, 256, 1200, 0), (8, 8, 200, 1200, 30),
+    (16, 2, 128, 1200, 0), (2, 2, 72, 2300, 0), (3, 3, 64, 1500, 37)])
+def test_shared_values_far_past_a_row(hq, hkv, D, L, prefix):
+    """NaN and infinities hundreds of keys after what a row sees, in every
+    tile height, with the keys in one part and in several."""
+    poisoned_shared(L, hq, hkv, D, prefix, [L], [100, 511, 700, 1000, 1100, -1], every=3, seed=670)
