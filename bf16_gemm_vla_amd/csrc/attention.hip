@@ -435,10 +435,11 @@ struct Walk {
     // (the walk goes on for other waves' rows): there is nothing to add.  Bit b
     // of `late` is the sub-tile that ends 32 b to 32 b + 31 keys past the last
     // key that every row sees; 32 rows see at most 31 keys more than that, and
-    // a sub-tile that one of them sees ends at most 31 past those.
-    __device__ __forceinline__ bool put_off(const uint8_t* vt, int key0) const {
+    // a sub-tile that one of them sees ends at most 31 past those.  k1: the end
+    // of the walk's keys; past it V holds zeros.
+    __device__ __forceinline__ bool put_off(const uint8_t* vt, int key0, int k1) const {
         if (key0 >= kmax) return true;
-        if (key0 + 32 <= kfull || kfull == kmax || !has_nonfinite<C>(vt)) return false;
+        if (key0 + 32 <= kfull || k1 <= kfull || !has_nonfinite<C>(vt)) return false;
         st.late |= 1u << ((key0 + 32 - kfull) >> 5);
         return true;
     }
@@ -556,7 +557,7 @@ __device__ __forceinline__ void attend_stages(const Keys& keys, const uint16_t* 
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
         w.template weights<C::SUBS == 2 ? 0 : C::NI>(sc, pw, load_more);
-        if (!w.put_off(vt, key0)) w.add(vt, pw);
+        if (!w.put_off(vt, key0, k1)) w.add(vt, pw);
     };
     auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s, auto more) __attribute__((always_inline)) {
         // this wave's loads of stage s have landed and its reads of stage s-1
@@ -674,7 +675,7 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
         w.template weights<0>(sc, pw, [](int) {});
         if (more) wait_here<wait_vm(C::NI)>();                    // V(t); K(t+1) may be on its way
         else wait_here<wait_vm(0)>();
-        if (!w.put_off(vb, key0)) w.add(vb_all, pw);
+        if (!w.put_off(vb, key0, k1)) w.add(vb_all, pw);
         wait_here<kWaitLds>();                                    // V(t) has been read
     }
     st.l = half_sum(st.l);

@@ -825,3 +825,42 @@ def test_shared_values_far_past_a_row(hq, hkv, D, L, prefix):
     """NaN and infinities hundreds of keys after what a row sees, in every
     tile height, with the keys in one part and in several."""
     poisoned_shared(L, hq, hkv, D, prefix, [L], [100, 511, 700, 1000, 1100, -1], every=3, seed=670)
+
+
+def test_shared_values_far_past_a_row_of_a_batch():
+    poisoned_shared(1100, 4, 4, 64, 20, [1100, 1300, 0, 640], [5, 600, 1090, -3], every=5, seed=675)
+
+
+@pytest.mark.parametrize("hq,hkv,D,n", [
+    (32, 1, 128, 300), (32, 1, 128, 1000), (48, 1, 64, 800), (71, 1, 64, 500), (128, 1, 64, 600), (64, 1, 256, 150),
+    (64, 1, 256, 300), (64, 1, 256, 560), (96, 2, 72, 700), (2048, 1, 8, 70)])
+def test_prompt_unseen_values_beside_one_token_of_many_heads(hq, hkv, D, n):
+    """A wave whose rows all belong to one token, in a tile that walks on for later tokens."""
+    at = sorted({min(x, n - 1) for x in (0, 1, 17, 31, 32, n // 2, n - 34)})
+    poisoned_prompt(n, n, hq, hkv, D, True, at, every=max(1, n * hq // 12000), seed=680)
+
+
+@pytest.mark.parametrize("hq,hkv,D,n,m", [
+    (4, 4, 64, 300, 100), (64, 64, 64, 600, 200), (64, 64, 64, 1300, 70), (40, 40, 128, 700, 1), (64, 64, 256, 300, 90),
+    (32, 1, 64, 800, 40)])
+def test_prompt_rows_without_keys_beside_unseen_values(hq, hkv, D, n, m):
+    """Rows that see nothing are 0 in tiles whose later rows see infinities and NaN."""
+    at = sorted({0, m // 2, m - 1})
+    poisoned_prompt(n, m, hq, hkv, D, True, at, every=max(1, n * hq // 12000), seed=690)
+
+
+@pytest.mark.parametrize("hq,hkv,D,L,prefix,lens", [
+    (32, 1, 64, 2, 0, [64]), (32, 1, 128, 2, 0, [2]), (48, 1, 64, 7, 20, [7, 40, 300]), (71, 1, 64, 3, 50, [3, 90]),
+    (32, 1, 256, 40, 0, [40, 3]), (64, 2, 128, 33, 16, [20, 60, 33]), (4, 4, 64, 200, 0, [50, 0, 230]),
+    (64, 64, 64, 300, 10, [60, 300])])
+def test_shared_unseen_values_beside_rows_of_one_limit(hq, hkv, D, L, prefix, lens):
+    """Waves whose rows all see the same keys, or none, over the cache."""
+    poisoned_shared(L, hq, hkv, D, prefix, lens, [0, 1, -1, -2], every=max(1, L * hq // 6000), seed=700)
+
+
+@pytest.mark.parametrize("hq,hkv,D,n,m", [
+    (2, 2, 64, 40, 1), (2, 2, 64, 40, 33), (8, 1, 128, 70, 97), (3, 1, 72, 10, 63), (8, 1, 256, 300, 129), (2, 1, 200, 9, 2),
+    (64, 64, 64, 1300, 65), (40, 40, 128, 700, 45), (64, 64, 256, 300, 66)])
+def test_prompt_nothing_is_read_behind_the_keys(hq, hkv, D, n, m):
+    """All rows see all keys; the rows behind them in the tensors are NaN."""
+    poisoned_prompt(n, m, hq, hkv, D, False, [], every=max(1, n * hq // 6000), behind=128, seed=710)
