@@ -48,6 +48,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "bounded.h"
 #include "vla_device.h"
 #include "vla_internal.h"
 
@@ -828,10 +829,8 @@ __device__ __forceinline__ uint32_t wave_sum(uint32_t x) {
 struct Range {
     int q0, nq, k0, nk;
     __device__ __forceinline__ Range(const PromptArgs& a, int b) {
-        q0 = min(max(a.cu_q[b], 0), a.total_q);
-        nq = max(min(a.cu_q[b + 1], a.total_q) - q0, 0);
-        k0 = min(max(a.cu_k[b], 0), a.total_k);
-        nk = max(min(a.cu_k[b + 1], a.total_k) - k0, 0);
+        bounded_rows(a.cu_q[b], a.cu_q[b + 1], a.total_q, q0, nq);
+        bounded_rows(a.cu_k[b], a.cu_k[b + 1], a.total_k, k0, nk);
     }
     __device__ __forceinline__ Range() : q0(0), nq(0), k0(0), nk(0) {}
     __device__ __forceinline__ uint32_t tiles(int G, int tm) const {

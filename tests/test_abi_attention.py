@@ -162,3 +162,39 @@ def test_refusals_under_asan_and_ubsan():
     tail = (r.stdout + r.stderr)[-4000:]
     assert r.returncode == 0, tail
     assert "passed" in r.stdout and "ERROR: AddressSanitizer" not in tail and "runtime error" not in tail, tail
+
+
+def test_row_offsets_of_any_value_stay_in_the_tensor(tmp_path):
+    """The bounds that the prompt kernel puts on its offsets, compiled for the
+    host with UndefinedBehaviorSanitizer: no difference passes 32 bits, and no
+    pair of offsets leads outside."""
+    import os
+    import shutil
+    import subprocess
+
+    if not shutil.which("g++"):
+        pytest.skip("no host compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src = tmp_path / "rows.cpp"
+    src.write_text('''#include <cstdio>
+#include <algorithm>
+#include "bounded.h"
+int main() {
+    const int32_t values[] = {INT32_MIN, INT32_MIN + 1, -65, -1, 0, 1, 30, 63, 64, 65, 1 << 30, INT32_MAX};
+    for (int32_t total : {1, 64, 1 << 30})
+        for (int32_t begin : values)
+            for (int32_t end : values) {
+                int32_t first, n;
+                vla::bounded_rows(begin, end, total, first, n);
+                const int64_t b = std::min<int64_t>(std::max<int64_t>(begin, 0), total);
+                const int64_t e = std::min<int64_t>(std::max<int64_t>(end, b), total);
+                if (first != b || n != e - b) { printf("%d %d of %d: %d %d\\n", begin, end, total, first, n); return 1; }
+            }
+    return 0;
+}
+''')
+    exe = str(tmp_path / "rows")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=undefined", "-I",
+                    os.path.join(root, "bf16_gemm_vla_amd", "csrc"), str(src), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -864,3 +864,30 @@ def test_shared_unseen_values_beside_rows_of_one_limit(hq, hkv, D, L, prefix, le
 def test_prompt_nothing_is_read_behind_the_keys(hq, hkv, D, n, m):
     """All rows see all keys; the rows behind them in the tensors are NaN."""
     poisoned_prompt(n, m, hq, hkv, D, False, [], every=max(1, n * hq // 6000), behind=128, seed=710)
+
+
+@pytest.mark.parametrize("B", [1, 3, 70])
+@pytest.mark.parametrize("causal", [False, True])
+def test_prompt_offsets_of_any_value(B, causal):
+    """Offsets at the ends of 32 bits: every sequence is its rows and keys cut
+    to the tensors, and only rows of a sequence are written."""
+    total, low, high = 64, -(1 << 31), (1 << 31) - 1
+    q, k, v = rand(730, total, 4, 64), rand(731, total, 2, 64), rand(732, total, 2, 64)
+    some = {1: [10, low], 3: [low, 20, low, high], 70: [20, low] + [low, 5, high, low] * 17 + [low]}[B]
+    for cu_q, cu_k in ((some, some), (some, [0] * (B + 1)), ([0] * B + [total], some)):
+        o = Guarded(total * 4 * 64 * 2, fill=0x5A)
+        vla.vla_attn_prompt(dev(q), dev(k), dev(v), dev(np.array(cu_q, np.int32)), dev(np.array(cu_k, np.int32)), o.t, B,
+                            total, total, 4, 2, 64, 256, 128, 128, 256, causal, 0.125)
+        o.check()
+        written = np.zeros(total, bool)
+        for b in range(B):
+            a = min(max(cu_q[b], 0), total)
+            written[a:max(min(cu_q[b + 1], total), a)] = True
+        got = o.numpy(np.uint16).reshape(total, -1)
+        assert (got[~written] == 0x5A5A).all() and np.isfinite(bf16_f64(got[written])).all()
+        if not all(x <= y for x, y in zip(cu_q, cu_q[1:])):
+            continue                                             # sequences that share rows have no one result
+        s, e = (min(max(x, 0), total) for x in cu_k[-2:])
+        e = max(e, s)
+        lim = np.clip(np.arange(total) + 1 + (e - s) - total, 0, e - s) if causal else np.full(total, e - s)
+        assert_attention(got.reshape(total, 4, 64), q, k[s:e], v[s:e], lim, 0.125)
