@@ -16,9 +16,10 @@
 // at position 2^20 an fp32 product alone would be off by 2^-5 radians.  The
 // sine and cosine instructions take revolutions and are within 2^-22.9 of the
 // exact values over one turn (measured at 2^24 points), 2^-13 of a bf16 step.
-// Mean squares are fp32; rows whose squares leave its range take them in fp64,
-// with the root on the mantissa, so the largest and smallest bf16 values
-// neither overflow nor vanish.  Each output is rounded to bf16 once, from fp32.
+// Mean squares are fp32; heads whose sum of squares leaves its range (1e-30 ..
+// 1e30) take it and the normed values in fp64, with the root on the mantissa, so
+// the largest and smallest bf16 values neither overflow nor vanish.  Each output
+// is rounded to bf16 once, from fp32.
 // The kernel is bound by HBM on prompts and by latency on single tokens: a
 // wave's loads of a head go out before the angles, and before the previous
 // head's arithmetic.  Measured: 16387 tokens of 32 heads on 8 of 128, appended
@@ -140,9 +141,21 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
                 for (int e = 0; e < VEC; ++e) ss += x[e] * x[e] + y[e] * y[e];
             }
             for (int o = a.gw >> 1; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
-            float r = __builtin_amdgcn_rsqf(ss / static_cast<float>(a.D) + a.eps);
-            int k2 = 0;
-            if (!(ss > 1e-30f && ss < 1e30f)) {
+            float wl[VEC], wh[VEC];
+            if (live) {
+                to_f32<VEC>(*reinterpret_cast<const W*>(w + lo), wl);
+                to_f32<VEC>(*reinterpret_cast<const W*>(w + hi), wh);
+            }
+            if (ss > 1e-30f && ss < 1e30f) {
+                const float r = __builtin_amdgcn_rsqf(ss / static_cast<float>(a.D) + a.eps);
+                if (live) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) {
+                        x[e] = x[e] * r * wl[e];
+                        y[e] = y[e] * r * wh[e];
+                    }
+                }
+            } else {
                 double sd = 0.0;
                 if (live) {
 #pragma unroll
@@ -152,20 +165,20 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
                     }
                 }
                 for (int o = a.gw >> 1; o > 0; o >>= 1) sd += __shfl_xor(sd, o, 64);
-                // 1 / sqrt(m 2^(2k)) = rsq(m) 2^-k with m in [1/2, 2)
+                // 1 / sqrt(m 2^(2k)) = rsq(m) 2^-k with m in [1/2, 2); the
+                // products too are fp64: x r alone can leave fp32 on either
+                // side where x r w does not
                 int ex;
                 const double m = frexp(sd / a.D + static_cast<double>(a.eps), &ex);
-                r = __builtin_amdgcn_rsqf(static_cast<float>((ex & 1) ? 2.0 * m : m));
-                k2 = -((ex - (ex & 1)) / 2);
-            }
-            if (live) {
-                float wl[VEC], wh[VEC];
-                to_f32<VEC>(*reinterpret_cast<const W*>(w + lo), wl);
-                to_f32<VEC>(*reinterpret_cast<const W*>(w + hi), wh);
+                const int odd = ex & 1;
+                const double r = ldexp(static_cast<double>(__builtin_amdgcn_rsqf(static_cast<float>(odd ? 2.0 * m : m))),
+                                       -((ex - odd) / 2));
+                if (live) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    x[e] = ldexpf(x[e] * r, k2) * wl[e];
-                    y[e] = ldexpf(y[e] * r, k2) * wh[e];
+                    for (int e = 0; e < VEC; ++e) {
+                        x[e] = static_cast<float>(x[e] * r * wl[e]);
+                        y[e] = static_cast<float>(y[e] * r * wh[e]);
+                    }
                 }
             }
         }

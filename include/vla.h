@@ -222,9 +222,9 @@ int vla_gate_residual_ada_norm(const uint16_t *residual, const uint16_t *out, co
  *   c, s = rot_scale * cos, sin (positions[t] * inv_freq[j])
  *   k_cache[slots[t]] = the rotated k row, v_cache[slots[t]] = the v row.
  * Angles are reduced to one revolution in fp64, their sine and cosine are
- * fp32 (off by at most 2^-22), as are mean squares and products; a row whose
- * mean square leaves 1e-30 .. 1e30 has it summed again in fp64.  Each output
- * is rounded to bf16 once.
+ * fp32 (off by at most 2^-22), as are mean squares and products; a head whose
+ * sum of squares leaves 1e-30 .. 1e30 is summed again and normed in fp64.  Each
+ * output is rounded to bf16 once.
  * Scaling for long contexts is in inv_freq and rot_scale.
  *   q, k, v      device bf16, T rows of Hq, Hkv, Hkv heads; v is read only by
  *                the append and must be NULL without it;

@@ -891,3 +891,28 @@ def test_prompt_offsets_of_any_value(B, causal):
         e = max(e, s)
         lim = np.clip(np.arange(total) + 1 + (e - s) - total, 0, e - s) if causal else np.full(total, e - s)
         assert_attention(got.reshape(total, 4, 64), q, k[s:e], v[s:e], lim, 0.125)
+
+
+@pytest.mark.parametrize("D", [8, 24, 64, 72, 80, 96, 120, 248])
+def test_append_norm_of_the_largest_and_smallest_values(D):
+    """Rows whose mean square leaves fp32: one value at bf16's largest beside
+    small ones that a large weight brings back, and rows of the smallest."""
+    rows = np.zeros((6, 2, D), np.uint16)
+    rows[0, :, 0] = 0x7F7F                       # the largest bf16
+    rows[1, :, D - 1] = 0xFF7F
+    rows[2] = 0x7F7F
+    rows[3, :, :] = 0x3580                       # 2^-20
+    rows[3, :, 3] = 0x7F00                       # beside 2^127
+    rows[4] = 0x0001                             # the smallest
+    rows[5, :, 1] = 0x0001
+    w = np.full(D, 0x3F80, np.uint16)
+    for weight in (w, np.full(D, 0x7180, np.uint16)):            # 1, 2^100
+        for rot in (0, 8):
+            pos, freq = np.arange(6, dtype=np.int32), freqs(rot)
+            go, gk = Guarded(rows.nbytes), Guarded(rows.nbytes)
+            vla.vla_qk_norm_rope_append(dev(rows), dev(rows), None, dev(weight), dev(w), dev(freq) if rot else None,
+                                        dev(pos) if rot else None, None, go.t, gk.t, None, None, 6, 2, 2, D, rot, 2 * D,
+                                        2 * D, 0, 2 * D, 2 * D, 0, vla.VLA_ROPE_HALF, 1.0, 0.0)
+            for g, x in ((go, weight), (gk, w)):
+                g.check()
+                check_rotated(g.numpy(np.uint16).reshape(6, 2, D), rows, x, freq, pos, rot, False, 1.0, 0.0, f"rot {rot}")
