@@ -753,8 +753,8 @@ int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, con
     if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
     if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
     if (int rc = check_scale(fn, scale)) return rc;
-    // row tiles of at least 32 rows, at most one ragged one per sequence
-    if (total_q * (Hq / Hkv) >= (int64_t(1) << 31) - 128 || (total_q * (Hq / Hkv) / 32 + B) * Hkv >= (int64_t(1) << 31))
+    const vla::PromptPlan p = vla::plan_attn_prompt(B, total_q, Hq, Hkv, D, causal != 0);
+    if (total_q * (Hq / Hkv) >= (int64_t(1) << 31) - 128 || p.tiles * Hkv > vla::kMostWorkgroups)
         return fail(VLA_ESHAPE, fn, "total_q=%lld rows of %lld heads are too many", (long long)total_q, (long long)Hq);
     const Region o{out, total_q, Hq * D, out_stride};
     const Region ins[5] = {{q, total_q, Hq * D, q_stride}, {k, total_k, Hkv * D, k_stride}, {v, total_k, Hkv * D, v_stride},
@@ -769,13 +769,14 @@ int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, con
     a.Hq = static_cast<int>(Hq); a.Hkv = static_cast<int>(Hkv); a.D = static_cast<int>(D);
     a.causal = causal;
     a.c = scale * 1.4426950408889634f;
-    hipError_t e = vla::launch_attn_prompt(a, static_cast<hipStream_t>(stream));
+    hipError_t e = vla::launch_attn_prompt(a, p, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
 }
 
 namespace {
-// Sizes of a shared-prefix call that do not depend on its pointers.
-int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap, int64_t suffix_cap) {
+// Sizes of a shared-prefix call that do not depend on its pointers, and their plan.
+int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap, int64_t suffix_cap,
+                 vla::SharedPlan& p) {
     if (B <= 0 || L <= 0) return fail(VLA_EINVAL, fn, "B=%lld L=%lld must be positive", (long long)B, (long long)L);
     if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
     if (prefix_cap < 0 || suffix_cap < 0 || prefix_cap + suffix_cap == 0)
@@ -786,15 +787,20 @@ int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, 
         prefix_cap + suffix_cap >= (int64_t(1) << 31) - (int64_t(1) << 16))
         return fail(VLA_ESHAPE, fn, "B=%lld L=%lld Hq=%lld or the capacities %lld, %lld too large", (long long)B, (long long)L,
                     (long long)Hq, (long long)prefix_cap, (long long)suffix_cap);
+    p = vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_cap, suffix_cap);
+    if (p.workgroups > vla::kMostWorkgroups)
+        return fail(VLA_ESHAPE, fn, "B=%lld L=%lld of %lld heads are too many rows for one launch", (long long)B, (long long)L,
+                    (long long)Hq);
     return VLA_OK;
 }
 }  // namespace
 
 size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
                                               int64_t prefix_capacity, int64_t suffix_capacity) {
-    if (check_shared("vla_attn_shared_prefix_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity) != VLA_OK)
+    vla::SharedPlan p;
+    if (check_shared("vla_attn_shared_prefix_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, p) != VLA_OK)
         return 0;
-    return static_cast<size_t>(vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity).ws_bytes);
+    return static_cast<size_t>(p.ws_bytes);
 }
 
 int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
@@ -827,13 +833,12 @@ int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uin
     if ((block_table != nullptr) != (pages_per_seq > 0) || (seq_lens != nullptr) != (pages_per_seq > 0))
         return fail(VLA_EINVAL, fn, "block_table and seq_lens must be given exactly when pages_per_seq > 0");
     const int64_t prefix_cap = n_prefix_pages * page_size, suffix_cap = pages_per_seq * page_size;
-    if (int rc = check_shared(fn, B, L, Hq, Hkv, D, prefix_cap, suffix_cap)) return rc;
+    vla::SharedPlan p;
+    if (int rc = check_shared(fn, B, L, Hq, Hkv, D, prefix_cap, suffix_cap, p)) return rc;
     if (int rc = check_stride(fn, "q_stride", q_stride, Hq * D)) return rc;
     if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
     if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
     if (int rc = check_scale(fn, scale)) return rc;
-    const vla::SharedPlan p = vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_cap, suffix_cap);
-    if (p.prefix_items + p.suffix_items >= (int64_t(1) << 31)) return fail(VLA_ESHAPE, fn, "too many work items");
     if (ws_bytes < static_cast<size_t>(p.ws_bytes))
         return fail(VLA_EWORKSPACE, fn, "workspace %zu bytes < required %lld", ws_bytes, (long long)p.ws_bytes);
     const size_t cache_bytes = static_cast<size_t>(num_pages) * page_size * Hkv * D * 2;

@@ -44,6 +44,7 @@
 // measured side by side when the rule was made.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cstdint>
 #include <type_traits>
@@ -1091,8 +1092,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
-    const int64_t rows = static_cast<int64_t>(a.total_q) * (a.Hq / a.Hkv);
+PromptPlan plan_attn_prompt(int64_t B, int64_t total_q, int64_t Hq, int64_t Hkv, int64_t D, bool causal) {
+    PromptPlan p{};
+    const int64_t rows = total_q * (Hq / Hkv);
     // Narrow tiles where the GPU runs them all at once, wide ones, which load
     // less, where not: two workgroups per compute unit, one with 256 channels.
     // Of a causal prompt's tiles, half as long on average, up to one and a
@@ -1104,19 +1106,24 @@ hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s) {
     //   50 / 76, 2500 tokens 85 / 104 / 129; causal: 1500 tokens 56 / 37 / 31,
     //   3900 tokens 124 / 89 / 140
     // And no tile that the average sequence would not half fill.
-    const int64_t slots = (a.D > 128 ? 1 : 2) * kComputeUnits;
-    auto fits = [&](int tm) { return a.Hkv * ceil_div(rows, tm) <= (a.causal ? (tm == 64 ? 2 * slots : 3 * slots / 2) : slots); };
-    int tm = 128;
-    while (tm > 32 && (2 * rows <= static_cast<int64_t>(a.B) * tm || fits(tm / 2))) tm /= 2;
+    const int64_t slots = (D > 128 ? 1 : 2) * kComputeUnits;
+    auto fits = [&](int tm) { return Hkv * ceil_div(rows, tm) <= (causal ? (tm == 64 ? 2 * slots : 3 * slots / 2) : slots); };
+    p.tm = 128;
+    while (p.tm > 32 && (2 * rows <= B * p.tm || fits(p.tm / 2))) p.tm /= 2;
     // every sequence ends in at most one partial tile
-    a.tiles = static_cast<int>(rows / tm + (a.B < rows ? a.B : rows));
+    p.tiles = rows / p.tm + (B < rows ? B : rows);
+    return p;
+}
+
+hipError_t launch_attn_prompt(PromptArgs a, const PromptPlan& p, hipStream_t s) {
+    a.tiles = static_cast<int>(p.tiles);
     a.by_group = Divisor(a.Hq / a.Hkv);
     a.by_heads = Divisor(a.Hkv % 8 == 0 ? a.tiles : a.Hkv);
     auto run = [&](auto cfg) {
         attn_prompt_kernel<decltype(cfg)><<<a.tiles * a.Hkv, kAThreads, 0, s>>>(a);
         return hipGetLastError();
     };
-    return tm == 128 ? by_size<128>(a.D, run) : (tm == 64 ? by_size<64>(a.D, run) : by_size<32>(a.D, run));
+    return p.tm == 128 ? by_size<128>(a.D, run) : (p.tm == 64 ? by_size<64>(a.D, run) : by_size<32>(a.D, run));
 }
 
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
@@ -1168,6 +1175,13 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     const int64_t rows = B * L * Hq;
     p.ml_bytes = p.parts > 1 ? ceil_div(rows * p.parts * 8, 256) * 256 : 0;
     p.ws_bytes = p.parts > 1 ? p.ml_bytes + rows * p.parts * D * 4 : 256;
+    // four waves per row where the parts are many (80 rows of 13 parts, the
+    // whole call: 11.5 us, with one wave 12.6), one where they are few (3200
+    // rows of 2 parts: 22 us, with four waves 26)
+    p.join_waves = p.parts > 8 ? 4 : 1;
+    const int64_t join = p.parts > 1 ? ceil_div(rows * p.join_waves, 4) : 0;
+    p.workgroups = std::max(p.prefix_tm == p.suffix_tm ? p.prefix_items + p.suffix_items
+                                                       : std::max(p.prefix_items, p.suffix_items), join);
     return p;
 }
 
@@ -1212,10 +1226,7 @@ hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipSt
     }
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t rows = static_cast<int64_t>(a.B) * a.L * a.Hq;
-    // four waves per row where the parts are many (80 rows of 13 parts, the
-    // whole call: 11.5 us, with one wave 12.6), one where they are few (3200
-    // rows of 2 parts: 22 us, with four waves 26)
-    if (a.parts > 8) attn_join_kernel<4><<<static_cast<unsigned>(rows), kAThreads, 0, s>>>(a);
+    if (p.join_waves == 4) attn_join_kernel<4><<<static_cast<unsigned>(rows), kAThreads, 0, s>>>(a);
     else attn_join_kernel<1><<<static_cast<unsigned>((rows + 3) / 4), kAThreads, 0, s>>>(a);
     return hipGetLastError();
 }

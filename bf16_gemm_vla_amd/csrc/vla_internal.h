@@ -68,6 +68,10 @@ struct Divisor {
 #endif
 };
 
+// Workgroups of one launch of the attention kernels: a launch dimension holds
+// fewer than 2^32 threads, 256 to a workgroup.
+constexpr int64_t kMostWorkgroups = (int64_t(1) << 24) - 1;
+
 struct PromptArgs {
     const uint16_t *q, *k, *v;
     const int32_t *cu_q, *cu_k;
@@ -79,7 +83,13 @@ struct PromptArgs {
     int tiles;                                 // most row tiles per key/value head
     Divisor by_group, by_heads;                // query heads per key/value head; key/value heads, or the tiles
 };
-hipError_t launch_attn_prompt(PromptArgs a, hipStream_t s);
+// Launch plan of a prompt call, from its host sizes alone.
+struct PromptPlan {
+    int tm;              // query rows per workgroup
+    int64_t tiles;       // most row tiles per key/value head
+};
+PromptPlan plan_attn_prompt(int64_t B, int64_t total_q, int64_t Hq, int64_t Hkv, int64_t D, bool causal);
+hipError_t launch_attn_prompt(PromptArgs a, const PromptPlan& p, hipStream_t s);
 
 struct SharedArgs {
     const uint16_t *q, *k_cache, *v_cache;
@@ -101,7 +111,9 @@ struct SharedPlan {
     bool merged;         // prefix and suffix are one range of keys
     int prefix_tm, suffix_tm;   // query rows per workgroup
     int64_t prefix_splits, suffix_splits, suffix_tiles, prefix_items, suffix_items, parts;
+    int join_waves;      // per row, where its parts are joined
     int64_t ml_bytes, ws_bytes;
+    int64_t workgroups;  // of the call's largest launch
 };
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
                             int64_t suffix_cap);

@@ -196,7 +196,8 @@ int vla_gate_residual_ada_norm(const uint16_t *residual, const uint16_t *out, co
  * stable cache addresses; "Real-time VLA inference on AMD hardware", section
  * "The AMD stack", has it decide the whole model's latency.)
  *
- * Heads: Hq query heads share Hkv key/value heads, Hq a multiple of Hkv;
+ * Heads: Hq query heads share Hkv key/value heads, Hq a multiple of Hkv, at most
+ * 4096 (VLA_ESHAPE);
  * query head h reads key/value head h / (Hq / Hkv).  A head has D channels, D
  * a multiple of 8, at most 256 (VLA_ESHAPE).  A token's row holds its heads
  * one after another; rows are `*_stride` elements apart (a multiple of 8, at
@@ -265,7 +266,8 @@ int vla_qk_norm_rope_append(const uint16_t *q, const uint16_t *k, const uint16_t
  *   out       device bf16, total_q rows; rows in no sequence stay as they were;
  *   scale     > 0, finite also times log2(e); causal 0 or 1 (VLA_EINVAL).
  * B in 1 .. 2^20, total_q and total_k in 1 .. 2^30, total_q * Hq / Hkv below
- * 2^31 - 128 (VLA_ESHAPE). */
+ * 2^31 - 128, and what one launch holds: Hkv * (total_q * Hq / Hkv / 32 + B)
+ * below 2^24 always fits (VLA_ESHAPE). */
 int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, const int32_t *cu_q,
                     const int32_t *cu_k, uint16_t *out, int64_t B, int64_t total_q, int64_t total_k, int64_t Hq,
                     int64_t Hkv, int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride,
@@ -299,7 +301,9 @@ int vla_attn_prompt(const uint16_t *q, const uint16_t *k, const uint16_t *v, con
  * The lengths are read on the device: a captured call follows them.  Results
  * depend on the call's sizes and lengths alone: repeated calls are bitwise
  * equal.  B and L in 1 .. 2^20, B * L * Hq < 2^31 - 128, capacities
- * < 2^30 and together < 2^31 - 2^16 (VLA_ESHAPE). */
+ * < 2^30 and together < 2^31 - 2^16, and what one launch holds: Hkv *
+ * (B * L * Hq / Hkv / 32 + 2 * B) below 2^24 and B * L * Hq <= 2^26 - 4 always
+ * fit (VLA_ESHAPE; the workspace query gives 0 for sizes that are refused). */
 size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
                                               int64_t prefix_capacity, int64_t suffix_capacity);
 int vla_attn_shared_prefix(const uint16_t *q, const uint16_t *k_cache, const uint16_t *v_cache,

@@ -198,3 +198,21 @@ int main() {
                     os.path.join(root, "bf16_gemm_vla_amd", "csrc"), str(src), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_sizes_past_one_launch_are_refused():
+    """A launch holds fewer than 2^24 workgroups of 256 threads: row tiles of a
+    prompt, work items and joined rows over the cache."""
+    one = dict(B=1 << 20, total_q=1 << 20, total_k=1 << 20, D=8)
+    for heads in (16, 64):
+        strides = {f"{x}_stride": heads * 8 for x in ("q", "k", "v", "out")}
+        refused("vla_attn_prompt", prompt_args(Hq=heads, Hkv=heads, **one, **strides), ESHAPE, "too many")
+    n = vla.vla_attn_shared_prefix_workspace_bytes
+    most = 1 << 20
+    for heads, kv, prefix, suffix in ((16, 16, 0, 16), (64, 4, 16, 16)):       # items, joined rows
+        assert n(most, 1, heads, kv, 64, prefix, suffix) == 0 and "too many" in vla.last_error()
+        assert n(most - 1, 1, heads, kv, 64, prefix, suffix) > 0
+        refused("vla_attn_shared_prefix", shared_args(
+            B=most, L=1, Hq=heads, Hkv=kv, n_prefix_pages=prefix // 16, prefix_pages=A + 3 * GB if prefix else None,
+            prefix_len=A + 4 * GB if prefix else None, pages_per_seq=1, q_stride=heads * 64, out_stride=heads * 64,
+            ws_bytes=1 << 50), ESHAPE, "too many")
