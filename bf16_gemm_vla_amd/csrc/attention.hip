@@ -1035,12 +1035,15 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
     for (int base = w0; base < a.parts; base += 64 * WPR) {
         const int pl = base + WPR * lane;
         float w = 0.0f;
+        bool has = false;                                         // part pl saw a key
         if (pl < a.parts) {
             const float2 x = *reinterpret_cast<const float2*>(ml + 2 * pl);
+            has = x.x != -__builtin_inff();
             w = x.x == -__builtin_inff() ? 0.0f : (x.x == m ? 1.0f : __builtin_amdgcn_exp2f(x.x - m));
             // a part without keys has sum 0, or NaN where every score was NaN
             l += x.x == -__builtin_inff() ? x.y : x.y * w;
         }
+        const uint64_t there = __ballot(has);
         const int n = min(64, (a.parts - base + WPR - 1) / WPR);
         for (int i = 0; i < n; i += 8) {
             f32x4_t x[8];
@@ -1048,9 +1051,10 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 wi[j] = i + j < n ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i + j)) : 0.0f;
-                // a part of weight 0 holds nothing that was written
+                // a part without keys has nothing to add; one whose weight is
+                // 0 in fp32 has its infinities and NaN
                 x[j] = f32x4_t{};
-                if (wi[j] > 0.0f && live) x[j] = *reinterpret_cast<const f32x4_t*>(po + static_cast<int64_t>(base + WPR * (i + j)) * a.D);
+                if ((there >> (i + j) & 1) && live) x[j] = *reinterpret_cast<const f32x4_t*>(po + static_cast<int64_t>(base + WPR * (i + j)) * a.D);
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) o += x[j] * wi[j];

@@ -916,3 +916,24 @@ def test_append_norm_of_the_largest_and_smallest_values(D):
             for g, x in ((go, weight), (gk, w)):
                 g.check()
                 check_rotated(g.numpy(np.uint16).reshape(6, 2, D), rows, x, freq, pos, rot, False, 1.0, 0.0, f"rot {rot}")
+
+
+@pytest.mark.parametrize("hq,hkv,D,n", [(4, 1, 64, 3000), (8, 1, 256, 1500), (8, 2, 128, 40000)])
+def test_shared_seen_values_of_weights_that_vanish(hq, hkv, D, n):
+    """A visible NaN has its part in the result also where its key's weight, and
+    that of every key in its part of the cache, is 0 in fp32."""
+    c = Cache(1, hkv, D, 16, 0, [n], seed=720)
+    q = np.full((1, hq, D), 0x3F80, np.uint16)                   # ones
+    for lo, hi, x in ((0, n // 2, 0x4180), (n // 2, n, 0xC180)):  # scores +-16 D
+        c.k[c.keys[0][lo:hi]] = x
+    at = [n - 1, n // 2 + 40]
+    for j, key in enumerate(at):
+        c.v[c.keys[0][key], :, 3 * j] = 0x7FC0
+    size = vla.vla_attn_shared_prefix_workspace_bytes(1, 1, hq, hkv, D, 0, c.pps * 16)
+    assert size > 256                                            # the keys are split
+    o, w = Guarded(hq * D * 2), zeros_ws(size)
+    vla.vla_attn_shared_prefix(dev(q), dev(c.k), dev(c.v), None, None, dev(c.table), dev(np.array([n], np.int32)), o.t, w,
+                               size, 1, 1, hq, hkv, D, c.pages, 16, 0, c.pps, hq * D, hq * D, True, 1.0)
+    o.check()
+    g = bf16_f64(o.numpy(np.uint16).reshape(hq, D))
+    assert np.isnan(g[:, [0, 3]]).all() and np.isfinite(np.delete(g, [0, 3], axis=1)).all()
