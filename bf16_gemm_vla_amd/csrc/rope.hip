@@ -134,6 +134,10 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
         to_f32<VEC>(vy, y);
         const uint16_t* w = kind == 0 ? a.q_weight : a.k_weight;
         if (w) {
+            auto weights = [&](float* wl, float* wh) __attribute__((always_inline)) {
+                to_f32<VEC>(*reinterpret_cast<const W*>(w + lo), wl);
+                to_f32<VEC>(*reinterpret_cast<const W*>(w + hi), wh);
+            };
             // the lanes of one head share `kind`: the whole group is here
             float ss = 0.0f;
             if (live) {
@@ -141,21 +145,8 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
                 for (int e = 0; e < VEC; ++e) ss += x[e] * x[e] + y[e] * y[e];
             }
             for (int o = a.gw >> 1; o > 0; o >>= 1) ss += __shfl_xor(ss, o, 64);
-            float wl[VEC], wh[VEC];
-            if (live) {
-                to_f32<VEC>(*reinterpret_cast<const W*>(w + lo), wl);
-                to_f32<VEC>(*reinterpret_cast<const W*>(w + hi), wh);
-            }
-            if (ss > 1e-30f && ss < 1e30f) {
-                const float r = __builtin_amdgcn_rsqf(ss / static_cast<float>(a.D) + a.eps);
-                if (live) {
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        x[e] = x[e] * r * wl[e];
-                        y[e] = y[e] * r * wh[e];
-                    }
-                }
-            } else {
+            const float r = __builtin_amdgcn_rsqf(ss / static_cast<float>(a.D) + a.eps);
+            if (!(ss > 1e-30f && ss < 1e30f)) {
                 double sd = 0.0;
                 if (live) {
 #pragma unroll
@@ -171,14 +162,24 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
                 int ex;
                 const double m = frexp(sd / a.D + static_cast<double>(a.eps), &ex);
                 const int odd = ex & 1;
-                const double r = ldexp(static_cast<double>(__builtin_amdgcn_rsqf(static_cast<float>(odd ? 2.0 * m : m))),
-                                       -((ex - odd) / 2));
+                const double rd = ldexp(static_cast<double>(__builtin_amdgcn_rsqf(static_cast<float>(odd ? 2.0 * m : m))),
+                                        -((ex - odd) / 2));
                 if (live) {
+                    float wl[VEC], wh[VEC];
+                    weights(wl, wh);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) {
-                        x[e] = static_cast<float>(x[e] * r * wl[e]);
-                        y[e] = static_cast<float>(y[e] * r * wh[e]);
+                        x[e] = static_cast<float>(x[e] * rd * wl[e]);
+                        y[e] = static_cast<float>(y[e] * rd * wh[e]);
                     }
+                }
+            } else if (live) {
+                float wl[VEC], wh[VEC];
+                weights(wl, wh);
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    x[e] = x[e] * r * wl[e];
+                    y[e] = y[e] * r * wh[e];
                 }
             }
         }
