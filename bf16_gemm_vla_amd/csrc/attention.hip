@@ -244,6 +244,10 @@ struct Walk {
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
                                              (__attribute__((address_space(3))) void*)(dst + (r0 + i * C::RPI) * C::RB), 16, 0, 0);
         }
+        // the waits for these rows count the loads of keys that go out after
+        // them, and the compiler may reorder loads into different LDS objects
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_sched_barrier(0);
     }
     // Operand addresses from the buffers' starts, `first` bytes on.  They are
     // made opaque: the compiler follows an address to its LDS object over a few
