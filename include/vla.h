@@ -257,9 +257,12 @@ int vla_qk_norm_rope_append(const uint16_t *q, const uint16_t *k, const uint16_t
  *   out_i = sum_j softmax_j(scale q_i . k_j) v_j.
  * causal: with n_q rows and n_k keys, row i sees keys j <= i + n_k - n_q (the
  * ends of rows and keys are aligned; keys of earlier chunks come first).  A
- * row that sees no key gives 0.  What a row does not see has no part in it,
- * whatever its value, infinities and NaN included.  fp32 scores and sums;
- * the weights are rounded to bf16 for the second product.
+ * row that sees no key gives 0, and so does one whose scores are all -inf over
+ * finite values.  What a row does not see has no part in it, whatever its
+ * value, infinities and NaN included.  fp32 scores and sums; the weights, up to
+ * 2^8 each, are rounded to bf16 for the second product, and its result is
+ * divided by their sum (so values of 2^120 over the number of keys and more
+ * can overflow to infinity).
  *   q, k, v   device bf16, total_q, total_k, total_k rows;
  *   cu_q      device int32[B + 1], non-decreasing, cu_q[0] >= 0;
  *   cu_k      device int32[B + 1], or NULL: the same as cu_q;

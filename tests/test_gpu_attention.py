@@ -937,3 +937,55 @@ def test_shared_seen_values_of_weights_that_vanish(hq, hkv, D, n):
     o.check()
     g = bf16_f64(o.numpy(np.uint16).reshape(hq, D))
     assert np.isnan(g[:, [0, 3]]).all() and np.isfinite(np.delete(g, [0, 3], axis=1)).all()
+
+
+def test_scores_of_minus_infinity():
+    """Keys of score -inf weigh nothing; rows that see no others are 0."""
+    n, gone, hq, hkv, D = 100, 60, 4, 2, 64
+    q, k, v = rand(740, n, hq, D), rand(741, n, hkv, D), rand(742, n, hkv, D)
+    q[..., 0], k[:gone, :, 0] = 0x3F80, 0xFF80
+    o = Guarded(n * hq * D * 2)
+    vla.vla_attn_prompt(dev(q), dev(k), dev(v), dev(offsets([n])), None, o.t, 1, n, n, hq, hkv, D, hq * D, hkv * D, hkv * D,
+                        hq * D, True, 0.125)
+    o.check()
+    got = o.numpy(np.uint16).reshape(n, hq, D)
+    assert not (got[:gone] & 0x7FFF).any()
+    assert_attention(got[gone:], q[gone:], k, v, np.arange(gone, n) + 1, 0.125)
+    table = dev(np.arange(1000, dtype=np.int32))
+    for m in (40, 1000):                                         # keys in one part and in several
+        kc, vc = rand(743, m, hkv, D), rand(744, m, hkv, D)
+        kc[:, :, 0] = 0xFF80
+        for keep in (0, 3):
+            kc[m - keep:, :, 0] = 0
+            size = vla.vla_attn_shared_prefix_workspace_bytes(1, 1, hq, hkv, D, 0, m)
+            o, w = Guarded(hq * D * 2, fill=0x5A), zeros_ws(size)
+            vla.vla_attn_shared_prefix(dev(q[:1]), dev(kc), dev(vc), None, None, table, dev(np.array([m], np.int32)), o.t, w,
+                                       size, 1, 1, hq, hkv, D, m, 1, 0, m, hq * D, hq * D, True, 0.125)
+            o.check()
+            got = o.numpy(np.uint16).reshape(1, hq, D)
+            if keep:
+                assert_attention(got, q[:1], kc, vc, [m], 0.125)
+            else:
+                assert not (got & 0x7FFF).any()
+
+
+def test_calls_run_on_the_current_stream():
+    """Without a stream a call takes torch's current one, also under capture."""
+    from bf16_gemm_vla_amd._lib import _stream
+
+    side = torch.cuda.Stream()
+    assert _stream(None) == torch.cuda.current_stream().cuda_stream
+    with torch.cuda.stream(side):
+        assert _stream(None) == side.cuda_stream == torch.cuda.current_stream().cuda_stream
+    q, k, v = (rand(750 + i, 70, n, 64) for i, n in enumerate((4, 2, 2)))
+    d = [dev(x) for x in (q, k, v, offsets([70]))]
+    out = torch.zeros(70 * 4 * 64, dtype=torch.int16, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        assert _stream(None) == torch.cuda.current_stream().cuda_stream
+        vla.vla_attn_prompt(*d, None, out, 1, 70, 70, 4, 2, 64, 256, 128, 128, 256, True, 0.125)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert_attention(out_bits(out, 70, 4, 64), q, k, v, np.arange(70) + 1, 0.125)
