@@ -22,11 +22,10 @@
 // is rounded to bf16 once, from fp32.
 // The kernel is bound by HBM on prompts and by latency on single tokens: a
 // wave's loads of a head go out before the angles, and before the previous
-// head's arithmetic.  Measured: 16387 tokens of 32 heads on 8 of 128, appended
-// and kept, 90 us (4.85 TB/s, where a copy reaches 5.14); 2049 tokens of 28 on
-// 4 of 128, normed, 12.7 us (3.1 TB/s: one wave start and one pass over the
-// angles are a good part of it); 50 tokens of 8 on 1 of 256 3.9 us and one
-// token 3.5 us, the time of a launch.
+// head's arithmetic.  Measured, captured calls one behind another: 16387 tokens
+// of 32 heads on 8 of 128, appended and kept, 91 us (4.8 TB/s, where a copy
+// reaches 5.14); 2049 tokens of 28 on 4 of 128, normed, 12.1 us (3.3 TB/s); 50
+// tokens of 8 on 1 of 256 3.0 us and one token 2.8 us, the time of a launch.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -238,7 +237,9 @@ hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s) {
     // one wave per step while that fills the GPU's 1024 SIMDs some 8 times
     // over, then one wave per token, which computes its angles once (300
     // tokens of 8 heads on 1 of 256: 3.8 us, one wave per token 5.0; 16387
-    // tokens as above: 90 us, one wave per step 94)
+    // tokens as above: 90 us, one wave per step 94).  Between the two the rule
+    // is a compromise: 2049 tokens as above take 12.1 us in its three waves per
+    // token, 11.1 in two, 11.9 in one, 11.7 in one per step
     int64_t chunks = (8192 + a.T - 1) / a.T;
     if (chunks > steps) chunks = steps;
     a.steps = static_cast<int>((steps + chunks - 1) / chunks);
