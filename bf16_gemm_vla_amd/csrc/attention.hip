@@ -36,13 +36,13 @@
 // channels (16384 causal tokens, 32 heads on 8: 2.06 ms), 1060 of 256 (8192 x
 // 8192, 8 heads on 1: 0.52 ms) and 800 of 64 (8192 x 8192, 16 heads on 2: 0.34
 // ms); head sizes between these do the work of the next one (4000 x 4000, 16
-// heads on 16 of 72: 134 us, of 80 131, of 128 141); a sub-tile's exponentials and the exchange of maxima stand between its
-// two products and are covered by the other wave of the SIMD (up to 128
-// channels) or not at all (256).  One token over 131071 keys streams the cache
-// at 5.0 TB/s.  Small calls (50 rows 6.3 us, 10 rows over 778 cached keys 10.6
-// us) are bound by the chain of a workgroup: its arguments and lengths, its
-// first loads, one step, its results.  Two figures beside a rule below were
-// measured side by side when the rule was made.
+// heads on 16 of 72: 134 us, of 80 131, of 128 141); a sub-tile's exponentials
+// and the exchange of maxima stand between its two products and are covered by
+// the other wave of the SIMD (up to 128 channels) or not at all (256).  One token
+// over 131071 keys streams the cache at 5.0 TB/s.  Small calls (50 rows 6.3 us,
+// 10 rows over 778 cached keys 10.6 us) are bound by the chain of a workgroup:
+// its arguments and lengths, its first loads, one step, its results.  Two figures
+// beside a rule below were measured side by side when the rule was made.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1174,10 +1174,10 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // heads on 8 of 128: one token over 131071 keys 108 us, unsplit 1350; 8 and
     // 16 single tokens over up to 32768 own keys 138 and 249 us, unsplit 343
     // and 389; 64 behind 8195 shared and 300 own 31 us, unsplit 72).  Twice as
-    // often, two workgroups to a compute unit, is a little slower at those
-    // (112, 135, 256, 39) but much better from 129 to 256 workgroups, where
-    // this rule does not split: 20 such tokens 436 us, halved 323, the bytes'
-    // time 312.  With 64 of them the sequences fill the GPU (891 us, 860).
+    // often, two workgroups to a compute unit, takes 112, 135, 256 and 39 us
+    // for those, but from 129 to 256 workgroups, where this rule does not
+    // split, it is ahead: 20 such tokens 436 us, halved 323, the bytes' time
+    // 312.  With 64 of them the sequences fill the GPU (891 us, the bytes' 860).
     auto splits = [&](int64_t tiles, int64_t steps) {
         if (tiles == 0 || steps == 0) return int64_t(0);
         const int64_t most = kComputeUnits / tiles;
