@@ -989,3 +989,52 @@ def test_calls_run_on_the_current_stream():
         out.zero_()
         graph.replay()
         assert_attention(out_bits(out, 70, 4, 64), q, k, v, np.arange(70) + 1, 0.125)
+
+
+def test_outputs_with_gaps_between_rows():
+    """Rows of out further apart than their heads: what lies between stays."""
+    n, hq, hkv, D, gap = 75, 6, 2, 72, 24
+    q, k, v = rand(760, n, hq, D), rand(761, n, hkv, D), rand(762, n, hkv, D)
+    stride, d = hq * D + gap, [dev(x) for x in (q, k, v)]
+    def check(o, limits):
+        o.check()
+        rows = np.append(o.numpy(np.uint16), np.full(gap, 0x5A5A, np.uint16)).reshape(n, stride)
+        assert (rows[:, hq * D:] == 0x5A5A).all()
+        assert_attention(rows[:, :hq * D].reshape(n, hq, D), q, k, v, limits, 0.125)
+    o = Guarded((n * stride - gap) * 2, fill=0x5A)
+    vla.vla_attn_prompt(*d, dev(offsets([n])), None, o.t, 1, n, n, hq, hkv, D, hq * D, hkv * D, hkv * D, stride, True, 0.125)
+    check(o, np.arange(n) + 1)
+    size = vla.vla_attn_shared_prefix_workspace_bytes(1, n, hq, hkv, D, 0, n)
+    o, w = Guarded((n * stride - gap) * 2, fill=0x5A), zeros_ws(size)
+    vla.vla_attn_shared_prefix(*d, None, None, dev(np.arange(n, dtype=np.int32)), dev(np.array([n], np.int32)), o.t, w, size, 1, n,
+                               hq, hkv, D, n, 1, 0, n, hq * D, stride, False, 0.125)
+    check(o, np.full(n, n))
+
+
+@pytest.mark.parametrize("D", [8, 128])
+def test_pages_named_more_than_once_and_large_pages(D):
+    """Sequences that name the same pages, the prefix's among them, and pages of
+    65536 rows, two calls at once on streams and workspaces of their own."""
+    hq, hkv, page = 4, 2, 65536
+    k, v = rand(770, 2 * page, hkv, D), rand(771, 2 * page, hkv, D)
+    q = rand(772, 3, hq, D)
+    dk, dv, dq = dev(k), dev(v), dev(q)
+    pre, n_pre = dev(np.array([1], np.int32)), 70
+    table, lens = np.array([[1, 0], [1, 0], [0, 0]], np.int32), [30, page + 5, 90]
+    dt, dl, dn = dev(table), dev(np.array(lens, np.int32)), dev(np.array([n_pre], np.int32))
+    size = vla.vla_attn_shared_prefix_workspace_bytes(3, 1, hq, hkv, D, page, 2 * page)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs, ws = [Guarded(3 * hq * D * 2, fill=0x5A) for _ in streams], [zeros_ws(size) for _ in streams]
+    torch.cuda.synchronize()
+    for s, o, w in zip(streams, outs, ws):
+        for _ in range(3):
+            vla.vla_attn_shared_prefix(dq, dk, dv, pre, dn, dt, dl, o.t, w, size, 3, 1, hq, hkv, D, 2, page, 1, 2, hq * D, hq * D,
+                                       True, 0.125, stream=s)
+    torch.cuda.synchronize()
+    for o in outs:
+        o.check()
+        got = o.numpy(np.uint16).reshape(3, hq, D)
+        for b in range(3):
+            j = np.arange(lens[b])
+            at = np.concatenate([page + np.arange(n_pre), table[b][j // page].astype(np.int64) * page + j % page])
+            assert_attention(got[b:b + 1], q[b:b + 1], k[at], v[at], [len(at)], 0.125, f"sequence {b}")
