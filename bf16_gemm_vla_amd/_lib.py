@@ -54,6 +54,7 @@ SIGNATURES = {
     "vla_quantize_act": (INT, [P, P, P, P, SZ, I64, I64, P]),
     "vla_quantize_act_static": (INT, [P, P, P, I64, I64, P]),
     "vla_qk_norm_rope_append": (INT, [P] * 12 + [I64] * 11 + [INT, ctypes.c_float, ctypes.c_float, P]),
+    "vla_qk_norm_rope_axes_append": (INT, [P] * 13 + [I64] * 12 + [INT, ctypes.c_float, ctypes.c_float, P]),
     "vla_attn_prompt": (INT, [P] * 6 + [I64] * 10 + [INT, ctypes.c_float, P]),
     "vla_attn_shared_prefix_workspace_bytes": (SZ, [I64] * 7),
     "vla_attn_shared_prefix": (INT, [P] * 9 + [SZ] + [I64] * 11 + [INT, ctypes.c_float, P]),
@@ -229,6 +230,16 @@ def vla_qk_norm_rope_append(q, k, v, q_weight, k_weight, inv_freq, positions, sl
                                           _ptr(v_cache), T, Hq, Hkv, D, rot, q_stride, k_stride, v_stride,
                                           q_out_stride, k_out_stride, num_slots, layout, rot_scale, eps,
                                           _stream(stream)), "vla_qk_norm_rope_append")
+
+
+def vla_qk_norm_rope_axes_append(q, k, v, q_weight, k_weight, inv_freq, axis_of, positions, slots, q_out, k_out, k_cache,
+                                 v_cache, T, Hq, Hkv, D, rot, axes, q_stride, k_stride, v_stride, q_out_stride,
+                                 k_out_stride, num_slots, layout, rot_scale, eps, stream=None):
+    _check(load().vla_qk_norm_rope_axes_append(_ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(inv_freq),
+                                               _ptr(axis_of), _ptr(positions), _ptr(slots), _ptr(q_out), _ptr(k_out),
+                                               _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D, rot, axes, q_stride, k_stride,
+                                               v_stride, q_out_stride, k_out_stride, num_slots, layout, rot_scale, eps,
+                                               _stream(stream)), "vla_qk_norm_rope_axes_append")
 
 
 def vla_attn_prompt(q, k, v, cu_q, cu_k, out, B, total_q, total_k, Hq, Hkv, D, q_stride, k_stride, v_stride,

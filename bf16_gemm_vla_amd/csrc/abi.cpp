@@ -651,14 +651,14 @@ int vla_gate_residual_ada_norm(const uint16_t* residual, const uint16_t* out, co
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
 }
 
-int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* q_weight,
-                            const uint16_t* k_weight, const float* inv_freq, const int32_t* positions,
-                            const int64_t* slots, uint16_t* q_out, uint16_t* k_out, uint16_t* k_cache,
-                            uint16_t* v_cache, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot,
-                            int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
-                            int64_t k_out_stride, int64_t num_slots, int layout, float rot_scale, float eps,
-                            void* stream) {
-    const char* fn = "vla_qk_norm_rope_append";
+namespace {
+// Both forms of the append; with `several`, a token has positions on `axes` axes.
+int rope_append(const char* fn, bool several, const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* q_weight,
+                const uint16_t* k_weight, const float* inv_freq, const uint8_t* axis_of, const int32_t* positions,
+                const int64_t* slots, uint16_t* q_out, uint16_t* k_out, uint16_t* k_cache, uint16_t* v_cache, int64_t T,
+                int64_t Hq, int64_t Hkv, int64_t D, int64_t rot, int64_t axes, int64_t q_stride, int64_t k_stride,
+                int64_t v_stride, int64_t q_out_stride, int64_t k_out_stride, int64_t num_slots, int layout,
+                float rot_scale, float eps, void* stream) {
     REQUIRE_PTR(q);
     REQUIRE_PTR(k);
     REQUIRE_PTR(q_out);
@@ -666,6 +666,7 @@ int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t
     OPTIONAL_PTR(q_weight);
     OPTIONAL_PTR(k_weight);
     OPTIONAL_PTR(inv_freq);
+    OPTIONAL_PTR(axis_of);
     OPTIONAL_PTR(positions);
     OPTIONAL_PTR(slots);
     OPTIONAL_PTR(k_out);
@@ -676,11 +677,15 @@ int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t
     if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
     if (rot < 0 || rot > D || rot % 8 != 0)
         return fail(VLA_ESHAPE, fn, "rot=%lld must be a multiple of 8 in 0..D", (long long)rot);
+    if (axes <= 0) return fail(VLA_EINVAL, fn, "axes=%lld must be positive", (long long)axes);
+    if (axes > vla::kMostAxes) return fail(VLA_ESHAPE, fn, "axes=%lld must be at most %d", (long long)axes, vla::kMostAxes);
     if (layout != VLA_ROPE_HALF && layout != VLA_ROPE_INTERLEAVED) return fail(VLA_EINVAL, fn, "unknown layout %d", layout);
     if (!std::isfinite(rot_scale)) return fail(VLA_EINVAL, fn, "rot_scale must be finite");
     if (!std::isfinite(eps) || eps < 0.0f) return fail(VLA_EINVAL, fn, "eps must be finite and >= 0");
     if ((inv_freq != nullptr) != (rot > 0) || (positions != nullptr) != (rot > 0))
         return fail(VLA_EINVAL, fn, "inv_freq and positions must be given exactly when rot > 0");
+    if (several && (axis_of != nullptr) != (rot > 0))
+        return fail(VLA_EINVAL, fn, "axis_of must be given exactly when rot > 0");
     const bool append = k_cache != nullptr;
     if ((v_cache != nullptr) != append || (slots != nullptr) != append || (v != nullptr) != append || (num_slots != 0) != append)
         return fail(VLA_EINVAL, fn, "v, slots, k_cache, v_cache and num_slots must be given together");
@@ -694,13 +699,13 @@ int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t
     if (int rc = check_stride(fn, "q_out_stride", q_out_stride, Hq * D)) return rc;
     if (k_out)
         if (int rc = check_stride(fn, "k_out_stride", k_out_stride, Hkv * D)) return rc;
-    const Region ins[8] = {{q, T, Hq * D, q_stride}, {k, T, Hkv * D, k_stride}, {v, T, Hkv * D, v_stride},
+    const Region ins[9] = {{q, T, Hq * D, q_stride}, {k, T, Hkv * D, k_stride}, {v, T, Hkv * D, v_stride},
                            flat(q_weight, D * 2), flat(k_weight, D * 2), flat(inv_freq, rot * 2),
-                           flat(positions, T * 4), flat(slots, T * 8)};
+                           flat(positions, T * axes * 4), flat(slots, T * 8), flat(axis_of, rot / 2)};
     const Region outs[4] = {{q_out, T, Hq * D, q_out_stride}, {k_out, T, Hkv * D, k_out_stride},
                             {k_cache, num_slots, Hkv * D, Hkv * D}, {v_cache, num_slots, Hkv * D, Hkv * D}};
     for (int i = 0; i < 4; ++i) {
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 9; ++j) {
             const bool in_place = i == j && i < 2 && outs[i].p == ins[j].p && outs[i].stride == ins[j].stride;
             if (!in_place && regions_overlap(outs[i], ins[j])) return fail(VLA_EINVAL, fn, "output %d overlaps input %d", i, j);
         }
@@ -710,16 +715,42 @@ int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t
     vla::RopeArgs a{};
     a.q = q; a.k = k; a.v = v;
     a.q_weight = q_weight; a.k_weight = k_weight;
-    a.inv_freq = inv_freq; a.positions = positions; a.slots = slots;
+    a.inv_freq = inv_freq; a.positions = positions; a.axis_of = axis_of; a.slots = slots;
     a.q_out = q_out; a.k_out = k_out; a.k_cache = k_cache; a.v_cache = v_cache;
     a.T = T; a.num_slots = num_slots;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
     a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
     a.Hq = static_cast<int>(Hq); a.Hkv = static_cast<int>(Hkv); a.D = static_cast<int>(D); a.rot = static_cast<int>(rot);
+    a.axes = static_cast<int>(axes);
     a.interleaved = layout == VLA_ROPE_INTERLEAVED;
     a.rot_scale = rot_scale; a.eps = eps;
     hipError_t e = vla::launch_qk_norm_rope_append(a, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+}  // namespace
+
+int vla_qk_norm_rope_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* q_weight,
+                            const uint16_t* k_weight, const float* inv_freq, const int32_t* positions,
+                            const int64_t* slots, uint16_t* q_out, uint16_t* k_out, uint16_t* k_cache,
+                            uint16_t* v_cache, int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t rot,
+                            int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t q_out_stride,
+                            int64_t k_out_stride, int64_t num_slots, int layout, float rot_scale, float eps,
+                            void* stream) {
+    return rope_append("vla_qk_norm_rope_append", false, q, k, v, q_weight, k_weight, inv_freq, nullptr, positions, slots,
+                       q_out, k_out, k_cache, v_cache, T, Hq, Hkv, D, rot, 1, q_stride, k_stride, v_stride, q_out_stride,
+                       k_out_stride, num_slots, layout, rot_scale, eps, stream);
+}
+
+int vla_qk_norm_rope_axes_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* q_weight,
+                                 const uint16_t* k_weight, const float* inv_freq, const uint8_t* axis_of,
+                                 const int32_t* positions, const int64_t* slots, uint16_t* q_out, uint16_t* k_out,
+                                 uint16_t* k_cache, uint16_t* v_cache, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t rot, int64_t axes, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 int64_t q_out_stride, int64_t k_out_stride, int64_t num_slots, int layout,
+                                 float rot_scale, float eps, void* stream) {
+    return rope_append("vla_qk_norm_rope_axes_append", true, q, k, v, q_weight, k_weight, inv_freq, axis_of, positions,
+                       slots, q_out, k_out, k_cache, v_cache, T, Hq, Hkv, D, rot, axes, q_stride, k_stride, v_stride,
+                       q_out_stride, k_out_stride, num_slots, layout, rot_scale, eps, stream);
 }
 
 namespace {

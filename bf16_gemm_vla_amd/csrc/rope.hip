@@ -3,7 +3,9 @@
 //   n = x * w / sqrt(mean(x^2) + eps)                  (q and k, with a weight)
 //   (a, b) -> (a c - b s, b c + a s),  c, s = rot_scale * (cos, sin)(position * inv_freq[j])
 // with (a, b) = (n_j, n_{j + rot/2}) or (n_2j, n_2j+1); channels rot .. D-1
-// pass.  The rotated k row and the v row also go to their cache slot.
+// pass.  The rotated k row and the v row also go to their cache slot.  With
+// AXES a token has a position on each of up to four axes (time, height, width)
+// and pair j turns by the one that axis_of[j] names.
 //
 // A head is cut into units of 2 VEC channels that hold whole pairs: in the
 // rotated part of the half layout VEC channels and their VEC partners rot/2
@@ -46,6 +48,13 @@ template <>
 struct Words<4> { using type = uint2; };
 
 template <int VEC>
+struct Axes;    // the axis bytes of VEC pairs
+template <>
+struct Axes<8> { using type = uint64_t; };
+template <>
+struct Axes<4> { using type = uint32_t; };
+
+template <int VEC>
 __device__ __forceinline__ void to_f32(typename Words<VEC>::type w, float* x) {
     uint32_t u[VEC / 2];
     __builtin_memcpy(u, &w, sizeof(w));
@@ -67,7 +76,7 @@ __device__ __forceinline__ typename Words<VEC>::type to_words(const float* x) {
     return w;
 }
 
-template <int VEC>
+template <int VEC, bool AXES>
 __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs a) {
     using W = typename Words<VEC>::type;
     const int lane = threadIdx.x & 63;
@@ -104,9 +113,30 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
 #pragma unroll
     for (int e = 0; e < VEC; ++e) { c[e] = 1.0f; s[e] = 0.0f; }
     if (turned) {
-        const double pos = static_cast<double>(a.positions[t]) * 0.15915494309189533577;   // 1 / (2 pi)
+        constexpr double kPerTurn = 0.15915494309189533577;   // 1 / (2 pi)
+        int at[AXES ? kMostAxes : 1] = {};                    // the token's positions
+        typename Axes<VEC>::type axis = 0;                    // one byte per pair
+        if constexpr (AXES) {
+            // the pairs' axes and every axis's position in flight together,
+            // then a choice: an indexed load would wait for the first
+            axis = *reinterpret_cast<const typename Axes<VEC>::type*>(a.axis_of + u * VEC);
+#pragma unroll
+            for (int x = 0; x < kMostAxes; ++x)
+                if (x < a.axes) at[x] = a.positions[x * a.T + t];
+        } else {
+            at[0] = a.positions[t];
+        }
+        const double first = static_cast<double>(at[0]) * kPerTurn;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
+            double pos = first;
+            if constexpr (AXES) {
+                const uint32_t x = static_cast<uint32_t>(axis >> (8 * e)) & 0xFFu;
+                int p = 0;                                    // an axis that the token does not have
+#pragma unroll
+                for (int i = 0; i < kMostAxes; ++i) p = x == static_cast<uint32_t>(i) ? at[i] : p;
+                pos = static_cast<double>(p) * kPerTurn;
+            }
             const double rev = pos * static_cast<double>(a.inv_freq[u * VEC + e]);
             const float f = static_cast<float>(rev - __builtin_rint(rev));
             s[e] = __builtin_amdgcn_sinf(f) * a.rot_scale;
@@ -246,8 +276,13 @@ hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s) {
     a.chunks = (steps + a.steps - 1) / a.steps;
     const int64_t blocks = (a.T * a.chunks + kRThreads / 64 - 1) / (kRThreads / 64);
     const dim3 grid(static_cast<unsigned>(blocks));
-    if (vec == 8) qk_norm_rope_append_kernel<8><<<grid, kRThreads, 0, s>>>(a);
-    else qk_norm_rope_append_kernel<4><<<grid, kRThreads, 0, s>>>(a);
+    if (a.axis_of) {
+        if (vec == 8) qk_norm_rope_append_kernel<8, true><<<grid, kRThreads, 0, s>>>(a);
+        else qk_norm_rope_append_kernel<4, true><<<grid, kRThreads, 0, s>>>(a);
+    } else {
+        if (vec == 8) qk_norm_rope_append_kernel<8, false><<<grid, kRThreads, 0, s>>>(a);
+        else qk_norm_rope_append_kernel<4, false><<<grid, kRThreads, 0, s>>>(a);
+    }
     return hipGetLastError();
 }
 

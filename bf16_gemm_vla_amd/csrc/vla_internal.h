@@ -29,15 +29,17 @@ hipError_t launch_gate_residual_ada_norm(const uint16_t* resid, const uint16_t* 
 bool boundary_width_ok(int64_t D);   // D a positive multiple of 4, at most 8192
 
 // ------------------------------------------------------------ attention
+constexpr int kMostAxes = 4;                   // positions per token
 struct RopeArgs {
     const uint16_t *q, *k, *v;
     const uint16_t *q_weight, *k_weight;       // nullable
     const float* inv_freq;
-    const int32_t* positions;
+    const int32_t* positions;                  // axes rows of T
+    const uint8_t* axis_of;                    // nullable: one axis
     const int64_t* slots;                      // nullable with the caches
     uint16_t *q_out, *k_out, *k_cache, *v_cache;   // k_out, caches nullable
     int64_t T, q_stride, k_stride, v_stride, q_out_stride, k_out_stride, num_slots;
-    int Hq, Hkv, D, rot, interleaved;
+    int Hq, Hkv, D, rot, interleaved, axes;
     float rot_scale, eps;
     int gw, gw_log2, chunks, steps;            // set by the launcher
 };

@@ -252,6 +252,22 @@ int vla_qk_norm_rope_append(const uint16_t *q, const uint16_t *k, const uint16_t
                             int64_t k_out_stride, int64_t num_slots, int layout, float rot_scale, float eps,
                             void *stream);
 
+/* The same with positions on several axes, as the tokens of images and videos
+ * have them (time, height, width): pair j turns by positions[axis_of[j]][t].
+ *   axis_of    device uint8[rot / 2], NULL when rot == 0; a pair whose axis is
+ *              not in 0 .. axes - 1 turns as at position 0;
+ *   positions  device int32[axes][T] (axis after axis), any sign;
+ *   axes       1 .. 4 (VLA_EINVAL below, VLA_ESHAPE above).
+ * Everything else is vla_qk_norm_rope_append's; with one axis, or where a
+ * token's positions are equal, the results are bit for bit the same. */
+int vla_qk_norm_rope_axes_append(const uint16_t* q, const uint16_t* k, const uint16_t* v, const uint16_t* q_weight,
+                                 const uint16_t* k_weight, const float* inv_freq, const uint8_t* axis_of,
+                                 const int32_t* positions, const int64_t* slots, uint16_t* q_out, uint16_t* k_out,
+                                 uint16_t* k_cache, uint16_t* v_cache, int64_t T, int64_t Hq, int64_t Hkv, int64_t D,
+                                 int64_t rot, int64_t axes, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                 int64_t q_out_stride, int64_t k_out_stride, int64_t num_slots, int layout,
+                                 float rot_scale, float eps, void* stream);
+
 /* Attention over B packed sequences: rows cu_q[b] .. cu_q[b+1]-1 of q attend
  * to rows cu_k[b] .. cu_k[b+1]-1 of k and v,
  *   out_i = sum_j softmax_j(scale q_i . k_j) v_j.
