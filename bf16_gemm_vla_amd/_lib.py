@@ -28,6 +28,7 @@ VLA_WFMT_BF16 = 0
 VLA_WFMT_E4M3_OCP = 1
 VLA_WFMT_E4M3_FNUZ = 2
 VLA_WFMT_MXFP4 = 3
+VLA_WFMT_INT8 = 4
 VLA_LAYOUT_ROWMAJOR = 0
 VLA_LAYOUT_MFMA = 1
 VLA_ROPE_HALF = 0
@@ -53,6 +54,7 @@ SIGNATURES = {
     "vla_quantize_act_workspace_bytes": (SZ, [I64, I64]),
     "vla_quantize_act": (INT, [P, P, P, P, SZ, I64, I64, P]),
     "vla_quantize_act_static": (INT, [P, P, P, I64, I64, P]),
+    "vla_quantize_tokens_int8": (INT, [P, P, P, I64, I64, P]),
     "vla_qk_norm_rope_append": (INT, [P] * 12 + [I64] * 11 + [INT, ctypes.c_float, ctypes.c_float, P]),
     "vla_qk_norm_rope_axes_append": (INT, [P] * 13 + [I64] * 12 + [INT, ctypes.c_float, ctypes.c_float, P]),
     "vla_attn_prompt": (INT, [P] * 6 + [I64] * 10 + [INT, ctypes.c_float, P]),
@@ -67,6 +69,7 @@ SIGNATURES = {
     "vla_gemm_fp8w_noalloc": (INT, [P, P, P, P, P, P, P, I64, I64, I64, P]),
     "vla_gemm_bf16": (INT, [P, P, P, P, P, P, SZ, I64, I64, I64, P]),
     "vla_gemm_mxfp4w": (INT, [P, P, P, P, P, P, SZ, I64, I64, I64, P]),
+    "vla_gemm_int8": (INT, [P, P, P, P, P, P, P, P, SZ, I64, I64, I64, P]),
     "vla_gemm_fp8w_gelu_mul": (INT, [P, P, P, P, P, P, P, SZ, I64, I64, I64, P]),
     "vla_mlp_chain_scratch_bytes": (SZ, [I64, I64, I64]),
     "vla_mlp_chain_fused_supported": (INT, [I64, I64, I64, INT]),
@@ -212,6 +215,10 @@ def vla_quantize_act(A, qa, s_a, ws, ws_bytes, M, K, stream=None):
                                    _stream(stream)), "vla_quantize_act")
 
 
+def vla_quantize_tokens_int8(A, qa, s_a, M, K, stream=None):
+    _check(load().vla_quantize_tokens_int8(_ptr(A), _ptr(qa), _ptr(s_a), M, K, _stream(stream)), "vla_quantize_tokens_int8")
+
+
 def vla_gate_residual_ada_norm(residual, out, gate, style, style_per_row, eps, residual_out, normalized,
                                next_gate, M, D, stream=None):
     _check(load().vla_gate_residual_ada_norm(_ptr(residual), _ptr(out), _ptr(gate), _ptr(style),
@@ -303,6 +310,11 @@ def vla_gemm_bf16(A, Wq, bias, residual, Y, ws, ws_bytes, M, N, K, stream=None):
 def vla_gemm_mxfp4w(A, Wq, bias, residual, Y, ws, ws_bytes, M, N, K, stream=None):
     _check(load().vla_gemm_mxfp4w(_ptr(A), _ptr(Wq), _ptr(bias), _ptr(residual), _ptr(Y), _ptr(ws), ws_bytes,
                                   M, N, K, _stream(stream)), "vla_gemm_mxfp4w")
+
+
+def vla_gemm_int8(A, s_a, Wq, s_w, bias, residual, Y, ws, ws_bytes, M, N, K, stream=None):
+    _check(load().vla_gemm_int8(_ptr(A), _ptr(s_a), _ptr(Wq), _ptr(s_w), _ptr(bias), _ptr(residual), _ptr(Y), _ptr(ws),
+                                ws_bytes, M, N, K, _stream(stream)), "vla_gemm_int8")
 
 
 def vla_gemm_fp8w_gelu_mul(A, Wgu, s_gu, bias, act, gu, ws, ws_bytes, M, I, K, stream=None):

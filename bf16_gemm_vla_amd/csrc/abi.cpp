@@ -64,6 +64,13 @@ int check_mnk(const char* fn, int64_t M, int64_t N, int64_t K) {
     return check_nk(fn, N, K);
 }
 
+int check_int8_k(const char* fn, int64_t K) {
+    if (K > vla::kMostInt8K)
+        return fail(VLA_ESHAPE, fn, "K=%lld: sums of 8-bit products stay inside 32 bits up to %lld", (long long)K,
+                    (long long)vla::kMostInt8K);
+    return VLA_OK;
+}
+
 int run_gemm(const char* fn, const vla::GemmProblem& pr, size_t ws_bytes, hipStream_t s) {
     const vla::GemmPlan p = vla::plan_gemm(pr.M, pr.N, pr.K, pr.atype, pr.wtype, pr.epi);
     if (!vla::plan_dispatchable(p, pr.atype, pr.wtype, pr.epi))
@@ -533,7 +540,7 @@ size_t vla_packed_bytes(int64_t N, int64_t K, int wfmt) {
 int vla_quantize_pack(const float* W, void* Wq, float* scales, int64_t N, int64_t K, int wfmt,
                       int layout, void* stream) {
     const char* fn = "vla_quantize_pack";
-    if (wfmt < VLA_WFMT_BF16 || wfmt > VLA_WFMT_MXFP4) return fail(VLA_EINVAL, fn, "unknown wfmt %d", wfmt);
+    if (wfmt < VLA_WFMT_BF16 || wfmt > VLA_WFMT_INT8) return fail(VLA_EINVAL, fn, "unknown wfmt %d", wfmt);
     if (layout != VLA_LAYOUT_ROWMAJOR && layout != VLA_LAYOUT_MFMA) return fail(VLA_EINVAL, fn, "unknown layout %d", layout);
     if (int rc = check_nk(fn, N, K)) return rc;
     REQUIRE_PTR(W);
@@ -610,6 +617,21 @@ int vla_quantize_act_static(const uint16_t* A, const float* s_a, uint8_t* qa, in
     REQUIRE_PTR(s_a);
     REQUIRE_PTR(qa);
     hipError_t e = vla::launch_quantize_act_static(A, s_a, qa, M, K, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+
+int vla_quantize_tokens_int8(const uint16_t* A, int8_t* qa, float* s_a, int64_t M, int64_t K, void* stream) {
+    const char* fn = "vla_quantize_tokens_int8";
+    if (int rc = check_mnk(fn, M, 16, K)) return rc;
+    if (M * K > (int64_t(1) << 40)) return fail(VLA_ESHAPE, fn, "M*K=%lld too large", (long long)(M * K));
+    REQUIRE_PTR(A);
+    REQUIRE_PTR(qa);
+    REQUIRE_PTR(s_a);
+    const Region in = flat(A, static_cast<size_t>(M) * K * 2), codes = flat(qa, static_cast<size_t>(M) * K),
+                 scales = flat(s_a, static_cast<size_t>(M) * 4);
+    if (regions_overlap(codes, in) || regions_overlap(scales, in)) return fail(VLA_EINVAL, fn, "an output overlaps A");
+    if (regions_overlap(codes, scales)) return fail(VLA_EINVAL, fn, "qa overlaps s_a");
+    hipError_t e = vla::launch_quantize_tokens_int8(A, qa, s_a, M, K, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
 }
 
@@ -925,6 +947,8 @@ size_t vla_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int wfmt) {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
     if (wfmt == VLA_WFMT_MXFP4)
         return vla::gemm_ws_bytes(vla::plan_gemm(M, N, K, vla::AType::BF16, vla::WType::FP4, vla::Epi::PLAIN), M, N);
+    if (wfmt == VLA_WFMT_INT8)
+        return vla::gemm_ws_bytes(vla::plan_gemm(M, N, K, vla::AType::INT8, vla::WType::INT8, vla::Epi::PLAIN), M, N);
     const vla::WType wt = (wfmt == VLA_WFMT_BF16) ? vla::WType::BF16 : vla::WType::FP8;
     size_t best = 0;
     const vla::AType ats[2] = {vla::AType::BF16, vla::AType::FP8};
@@ -946,15 +970,19 @@ int vla_gemm_plan(int64_t M, int64_t N, int64_t K, int wfmt, int fp8_act, int ge
     const char* fn = "vla_gemm_plan";
     if (n_info < 0 || (n_info > 0 && !info)) return fail(VLA_EINVAL, fn, "info is NULL or n_info < 0");
     if (int rc = check_mnk(fn, M, N, K)) return rc;
-    if (wfmt != VLA_WFMT_BF16 && wfmt != VLA_WFMT_E4M3_OCP && wfmt != VLA_WFMT_MXFP4)
+    if (wfmt != VLA_WFMT_BF16 && wfmt != VLA_WFMT_E4M3_OCP && wfmt != VLA_WFMT_MXFP4 && wfmt != VLA_WFMT_INT8)
         return fail(VLA_EINVAL, fn, "wfmt=%d", wfmt);
-    const vla::AType at = fp8_act ? vla::AType::FP8 : vla::AType::BF16;
-    const vla::WType wt = (wfmt == VLA_WFMT_BF16) ? vla::WType::BF16
-                          : (wfmt == VLA_WFMT_MXFP4 ? vla::WType::FP4 : vla::WType::FP8);
+    const vla::AType at = wfmt == VLA_WFMT_INT8 ? vla::AType::INT8 : (fp8_act ? vla::AType::FP8 : vla::AType::BF16);
+    const vla::WType wt = (wfmt == VLA_WFMT_BF16)    ? vla::WType::BF16
+                          : (wfmt == VLA_WFMT_MXFP4) ? vla::WType::FP4
+                          : (wfmt == VLA_WFMT_INT8)  ? vla::WType::INT8
+                                                     : vla::WType::FP8;
     const vla::Epi epi = gelu_mul ? vla::Epi::GELU_MUL : vla::Epi::PLAIN;
     if ((gelu_mul || fp8_act) && wt != vla::WType::FP8) return fail(VLA_EINVAL, fn, "fp8_act and gelu_mul need FP8 weights");
     if (gelu_mul && fp8_act) return fail(VLA_EINVAL, fn, "gelu_mul takes bf16 activations");
     if (gelu_mul && (N % 32) != 0) return fail(VLA_ESHAPE, fn, "gelu_mul needs N = 2I with I a multiple of 16");
+    if (at == vla::AType::INT8)
+        if (int rc = check_int8_k(fn, K)) return rc;
     const vla::GemmPlan p = vla::plan_gemm(M, N, K, at, wt, epi);
     const size_t ws = vla::gemm_ws_bytes(p, M, N);
     const int64_t v[10] = {p.kernel,
@@ -1066,6 +1094,36 @@ int vla_gemm_mxfp4w(const uint16_t* A, const uint8_t* Wq, const uint16_t* bias, 
     p.atype = vla::AType::BF16;
     p.wtype = vla::WType::FP4;
     p.epi = vla::Epi::PLAIN;
+    return run_gemm(fn, p, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+int vla_gemm_int8(const int8_t* A, const float* s_a, const int8_t* Wq, const float* s_w, const uint16_t* bias,
+                  const uint16_t* residual, uint16_t* Y, void* ws, size_t ws_bytes, int64_t M, int64_t N, int64_t K,
+                  void* stream) {
+    const char* fn = "vla_gemm_int8";
+    if (int rc = check_mnk(fn, M, N, K)) return rc;
+    if (int rc = check_int8_k(fn, K)) return rc;
+    REQUIRE_PTR(A);
+    REQUIRE_PTR(s_a);
+    REQUIRE_PTR(Wq);
+    REQUIRE_PTR(s_w);
+    OPTIONAL_PTR(bias);
+    OPTIONAL_PTR(residual);
+    REQUIRE_PTR(Y);
+    REQUIRE_PTR(ws);
+    vla::GemmProblem p{};
+    p.A = A; p.s_a = s_a; p.W = Wq; p.s_w = s_w; p.bias = bias; p.resid = residual; p.Y = Y; p.ws = ws;
+    p.M = M; p.N = N; p.K = K;
+    p.atype = vla::AType::INT8;
+    p.wtype = vla::WType::INT8;
+    p.epi = vla::Epi::PLAIN;
+    const size_t mn = static_cast<size_t>(M) * N * 2;
+    const Region out = flat(Y, mn);
+    const Region ins[6] = {flat(A, static_cast<size_t>(M) * K), flat(Wq, static_cast<size_t>(N) * K),
+                           flat(s_a, static_cast<size_t>(M) * 4), flat(s_w, static_cast<size_t>(N) * 4),
+                           flat(bias, static_cast<size_t>(N) * 2), flat(residual == Y ? nullptr : residual, mn)};
+    for (int j = 0; j < 6; ++j)
+        if (regions_overlap(out, ins[j])) return fail(VLA_EINVAL, fn, "Y overlaps input %d", j);
     return run_gemm(fn, p, ws_bytes, static_cast<hipStream_t>(stream));
 }
 

@@ -110,6 +110,34 @@ __device__ __forceinline__ uint2 encode8_quotient(const float v[8], float sc, fl
     return make_uint2(o[0], o[1]);
 }
 
+// Eight integers nearest to fp32(v / sc), ties to even, within +-127.  v * rcp
+// is within 2 ulps of the quotient (below 2^-15 up to 128), and the integer
+// changes at halves only: away from them the product serves, next to one (and
+// where rcp or the product is not finite) the division itself.
+__device__ __forceinline__ uint2 encode8_int8(const float v[8], float sc, float rcp) {
+    int c[8];
+    float far = 0.0f;                                            // largest distance from an integer
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float q = v[j] * rcp, r = __builtin_rintf(q), d = __builtin_fabsf(q - r);
+        far = fmaxf(far, d);
+        odd |= !(d <= 0.5f);                                     // NaN
+        c[j] = static_cast<int>(__builtin_amdgcn_fmed3f(r, -127.0f, 127.0f));
+    }
+    if (__builtin_expect(odd || far > 0.5f - 0x1p-14f, 0)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c[j] = static_cast<int>(__builtin_amdgcn_fmed3f(__builtin_rintf(__fdiv_rn(v[j], sc)), -127.0f, 127.0f));
+    }
+    uint32_t o[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        o[h] = (static_cast<uint32_t>(c[4 * h]) & 0xFFu) | (static_cast<uint32_t>(c[4 * h + 1]) & 0xFFu) << 8 |
+               (static_cast<uint32_t>(c[4 * h + 2]) & 0xFFu) << 16 | static_cast<uint32_t>(c[4 * h + 3]) << 24;
+    return make_uint2(o[0], o[1]);
+}
+
 // One workgroup of NT threads per 16-row tile (any K; the second read of
 // the tile mostly hits L2).  Phase 1: row absmax -> scale.  Phase 2: each
 // thread encodes 8-value slots (reads 2 x 16 B, writes 8 B / 16 B).  NT =
@@ -138,7 +166,7 @@ __global__ __launch_bounds__(NT) void quantize_pack_kernel(const float* __restri
         }
         m = group_max<TPR>(m);
         if (c == 0) {
-            const float maxv = (WFMT == VLA_WFMT_E4M3_FNUZ) ? 240.0f : 448.0f;
+            const float maxv = (WFMT == VLA_WFMT_INT8) ? 127.0f : (WFMT == VLA_WFMT_E4M3_FNUZ) ? 240.0f : 448.0f;
             const float sc = (m == 0.0f) ? 1.0f : __fdiv_rn(m, maxv);
             s_scale[r] = sc;
             scales[n0 * 16 + r] = sc;
@@ -165,6 +193,8 @@ __global__ __launch_bounds__(NT) void quantize_pack_kernel(const float* __restri
                 w[i] = f32x2_to_bf16x2(v[2 * i], v[2 * i + 1]);
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(Wq) + off) =
                 make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (WFMT == VLA_WFMT_INT8) {
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Wq) + off) = encode8_int8(v, sc, rcp);
         } else {
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Wq) + off) =
                 encode8_quotient<WFMT == VLA_WFMT_E4M3_FNUZ>(v, sc, rcp);
@@ -753,7 +783,120 @@ __global__ __launch_bounds__(kThreads) void act_encode_kernel(const uint16_t* __
     }
 }
 
+// 8-bit integers with one scale per token: row m of bf16 A gets s = fp32(max
+// |row| / 127) (1 for zeros) and the integers nearest to fp32(A / s).  A row
+// that holds an infinity or NaN gets zeros and a NaN scale, which makes its
+// products NaN.  WPR waves share a row, which stays in registers between its
+// maximum and its codes: 8 CH values per lane.
+template <int WPR, int CH>
+__global__ __launch_bounds__(kThreads) void quantize_tokens_int8_kernel(const uint16_t* __restrict__ A,
+                                                                        int8_t* __restrict__ qa,
+                                                                        float* __restrict__ s_a, int64_t M, int64_t K) {
+    __shared__ uint32_t tops[kThreads / kWave];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * (4 / WPR) + wave / WPR;
+    const bool live = m < M;
+    const int64_t k0 = 8 * ((wave % WPR) * kWave + lane);
+    const uint16_t* const row = A + m * K;
+    uint4 v[CH];
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int64_t k = k0 + c * 8 * kWave * WPR;
+        v[c] = make_uint4(0, 0, 0, 0);
+        if (live && k < K) v[c] = *reinterpret_cast<const uint4*>(row + k);
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] << 16 & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off, kWave)));
+    if constexpr (WPR > 1) {
+        if (lane == 0) tops[wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) top = max(top, tops[i]);
+    }
+    if (!live) return;
+    const bool fine = top < 0x7F800000u;
+    const float sc = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), 127.0f);
+    const float rcp = __fdiv_rn(1.0f, sc);
+    if (k0 == 0) s_a[m] = fine ? sc : __builtin_nanf("");
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int64_t k = k0 + c * 8 * kWave * WPR;
+        if (k >= K) continue;
+        const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = fine ? __uint_as_float(w[i] << 16) : 0.0f;
+            x[2 * i + 1] = fine ? __uint_as_float(w[i] & 0xFFFF0000u) : 0.0f;
+        }
+        *reinterpret_cast<uint2*>(qa + m * K + k) = fine ? encode8_int8(x, sc, rcp) : make_uint2(0, 0);
+    }
+}
+
+// Rows longer than the registers of a workgroup hold: read twice.
+__global__ __launch_bounds__(1024) void quantize_long_tokens_int8_kernel(const uint16_t* __restrict__ A,
+                                                                         int8_t* __restrict__ qa, float* __restrict__ s_a,
+                                                                         int64_t K) {
+    __shared__ uint32_t tops[16];
+    const int64_t m = blockIdx.x;
+    const uint16_t* const row = A + m * K;
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int64_t k = 8 * threadIdx.x; k < K; k += 8 * 1024) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] << 16 & 0x7FFF0000u, w[i] & 0x7FFF0000u));
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), off, kWave)));
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, tops[i]);
+    const bool fine = top < 0x7F800000u;
+    const float sc = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), 127.0f);
+    const float rcp = __fdiv_rn(1.0f, sc);
+    if (threadIdx.x == 0) s_a[m] = fine ? sc : __builtin_nanf("");
+#pragma unroll 2
+    for (int64_t k = 8 * threadIdx.x; k < K; k += 8 * 1024) {
+        const uint4 v = *reinterpret_cast<const uint4*>(row + k);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+        *reinterpret_cast<uint2*>(qa + m * K + k) = fine ? encode8_int8(x, sc, rcp) : make_uint2(0, 0);
+    }
+}
+
 }  // namespace
+
+hipError_t launch_quantize_tokens_int8(const uint16_t* A, int8_t* qa, float* s_a, int64_t M, int64_t K, hipStream_t s) {
+    if (K > 16384) {
+        quantize_long_tokens_int8_kernel<<<static_cast<unsigned>(M), 1024, 0, s>>>(A, qa, s_a, K);
+    } else if (K > 2048) {
+        const unsigned grid = static_cast<unsigned>(M);
+        if (K <= 4096) quantize_tokens_int8_kernel<4, 2><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
+        else if (K <= 8192) quantize_tokens_int8_kernel<4, 4><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
+        else quantize_tokens_int8_kernel<4, 8><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    } else {
+        const unsigned grid = static_cast<unsigned>((M + 3) / 4);
+        if (K <= 512) quantize_tokens_int8_kernel<1, 1><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
+        else if (K <= 1024) quantize_tokens_int8_kernel<1, 2><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
+        else quantize_tokens_int8_kernel<1, 4><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    }
+    return hipGetLastError();
+}
 
 // K / 128 slots per thread, 1 .. 16 (K a multiple of 128, at most 2048).
 #define VLA_SPT_CASES(X) X(1) X(2) X(3) X(4) X(5) X(6) X(7) X(8) X(9) X(10) X(11) X(12) X(13) X(14) X(15) X(16)
@@ -763,7 +906,8 @@ hipError_t launch_quantize_pack(const float* W, void* Wq, float* scales, int64_t
     const dim3 grid(static_cast<unsigned>(N / 16));
     // K a multiple of 512 up to 4096: 1024 threads per tile, one row per
     // wave, K / 512 slots per thread (the MFMA layout through LDS)
-    if (wfmt != VLA_WFMT_BF16 && K % 512 == 0 && K <= 4096) {
+    const bool fp8 = wfmt == VLA_WFMT_E4M3_OCP || wfmt == VLA_WFMT_E4M3_FNUZ;
+    if (fp8 && K % 512 == 0 && K <= 4096) {
         const int spt = static_cast<int>(K / 512);
         uint8_t* q = static_cast<uint8_t*>(Wq);
 #define VLA_Q1K(SPT_)                                                                                  \
@@ -782,7 +926,7 @@ hipError_t launch_quantize_pack(const float* W, void* Wq, float* scales, int64_t
 #undef VLA_Q1K
     }
     // other K, multiples of 128 up to 2048: 256 threads, K / 128 slots each
-    if (wfmt != VLA_WFMT_BF16 && K % 128 == 0 && K <= 2048) {
+    if (fp8 && K % 128 == 0 && K <= 2048) {
         const int spt = static_cast<int>(K / 128);
         uint8_t* q = static_cast<uint8_t*>(Wq);
 #define VLA_QP(SPT_)                                                                                   \
@@ -803,6 +947,9 @@ hipError_t launch_quantize_pack(const float* W, void* Wq, float* scales, int64_t
             break;
         case VLA_WFMT_E4M3_OCP:
             quantize_pack_kernel<VLA_WFMT_E4M3_OCP, 1024><<<grid, 1024, 0, s>>>(W, Wq, scales, K, layout);
+            break;
+        case VLA_WFMT_INT8:
+            quantize_pack_kernel<VLA_WFMT_INT8, 1024><<<grid, 1024, 0, s>>>(W, Wq, scales, K, layout);
             break;
         default:
             quantize_pack_kernel<VLA_WFMT_E4M3_FNUZ, 1024><<<grid, 1024, 0, s>>>(W, Wq, scales, K, layout);

@@ -34,6 +34,8 @@ struct WFragT;
 template <>
 struct WFragT<WType::FP8> { using type = u32x2_t; };
 template <>
+struct WFragT<WType::INT8> { using type = u32x2_t; };
+template <>
 struct WFragT<WType::BF16> { using type = u32x4_t; };
 template <>
 struct WFragT<WType::FP4> { using type = uint32_t; };
@@ -42,6 +44,8 @@ template <AType AT>
 struct AFragT;
 template <>
 struct AFragT<AType::FP8> { using type = u32x2_t; };
+template <>
+struct AFragT<AType::INT8> { using type = u32x2_t; };
 template <>
 struct AFragT<AType::BF16> { using type = u32x4_t; };
 
@@ -85,8 +89,9 @@ template <AType AT, WType WT, Epi EPI, int NT, int S, int WAVES, bool ALDS, int 
 __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     using WF = typename WFragT<WT>::type;
     using AF = typename AFragT<AT>::type;
-    constexpr int WB = (WT == WType::FP8) ? 8 : (WT == WType::FP4 ? 4 : 16);   // weight bytes per lane per fragment
-    constexpr int AB = (AT == AType::FP8) ? 1 : 2;    // activation bytes per element
+    constexpr int WB = (WT == WType::FP8 || WT == WType::INT8) ? 8 : (WT == WType::FP4 ? 4 : 16);   // weight bytes per lane per fragment
+    constexpr int AB = (AT == AType::BF16) ? 2 : 1;   // activation bytes per element
+    using Acc = typename AccT<AT, 4>::type;
     constexpr int JO = (EPI == Epi::PLAIN) ? NT : NT / 2;   // output tiles per group
     constexpr int PAIRS = JO * MT;                           // (output tile, m-tile) fragments
     constexpr int R = (PAIRS + WAVES - 1) / WAVES;           // fragments finished per wave
@@ -99,7 +104,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     constexpr int LDS_BYTES = SEPARATE ? L::BYTES + RED_BYTES : ((ALDS && L::BYTES > RED_BYTES) ? L::BYTES : RED_BYTES);
     static_assert(LDS_BYTES <= 160 * 1024 && L::BYTES % 16 == 0, "the workgroup's LDS fits");
     __shared__ __attribute__((aligned(16))) uint8_t lds[LDS_BYTES];
-    auto red = reinterpret_cast<f32x4_t(*)[NT][MT][64]>(lds + (SEPARATE ? L::BYTES : 0));
+    auto red = reinterpret_cast<Acc(*)[NT][MT][64]>(lds + (SEPARATE ? L::BYTES : 0));
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = blockIdx.x, split = blockIdx.y, mh = blockIdx.z;
@@ -119,7 +124,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     // and the LDS operand reads then overlap the weights' HBM latency.
     // 1. epilogue inputs
     EpiIn ein[R];
-    const float sa = (AT == AType::FP8) ? *a.s_a : 1.0f;
+    float sa[R];                                             // one for the tensor (FP8), or the fragments' rows' (INT8)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int pair = wave + r * WAVES, jo = pair / MT, mt = pair % MT;
@@ -127,6 +132,8 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
         const int row = mt * 16 + mrow;
         if (pair < PAIRS && tile < ntiles && row < mrows)
             ein[r] = load_epi<WT, EPI>(a, m0 + row, tile * 16 + 4 * q, a.ksplit == 1);
+        sa[r] = AT == AType::FP8 ? *a.s_a : 1.0f;
+        if (AT == AType::INT8 && row < mrows) sa[r] = a.s_a[m0 + row];
     }
     // 2. activation fragments: row m0 + mt*16 + lane%16, 8 K values at 8*(lane/16)
     AF af[S][MT];
@@ -231,16 +238,24 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
         }
     }
     // 4. MFMA
-    f32x4_t acc[NT][MT];
+    Acc acc[NT][MT];
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) acc[j][mt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int mt = 0; mt < MT; ++mt) acc[j][mt] = Acc{};
 #pragma unroll
     for (int s = 0; s < S; ++s) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             if (mt >= mt_count) break;
+            if constexpr (AT == AType::INT8) {
+                // the codes as they are: the instruction's 8 values of K per lane
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    acc[j][mt] = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(int64_t, wf[s][j]),
+                                                                       __builtin_bit_cast(int64_t, af[s][mt]), acc[j][mt], 0, 0, 0);
+                continue;
+            } else {
             const bf16x8_t bop = a_operand<AT>(af[s][mt]);
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -248,6 +263,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
                     acc[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4_to_bf16x8(wf[s][j], wsc[s][j]), bop, acc[j][mt], 0, 0, 0);
                 else
                     acc[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w_operand<WT>(wf[s][j]), bop, acc[j][mt], 0, 0, 0);
+            }
         }
     }
     if constexpr (ALDS && !SEPARATE) __syncthreads();   // activation reads done before LDS is reused
@@ -261,16 +277,16 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
             if (mt < mt_count) red[wave][j][mt][lane] = acc[j][mt];
     __syncthreads();
     auto total = [&](int j, int mt) {
-        f32x4_t v = red[0][j][mt][lane];
+        Acc v = red[0][j][mt][lane];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) v += red[w][j][mt][lane];
         return v;
     };
-    auto finish = [&](int r, int jo, int mt, f32x4_t v, f32x4_t u) {
+    auto finish = [&](int r, int jo, int mt, Acc v, Acc u) {
         const int tile = skinny_tile<EPI, NT>(g, jo, a.N);
         const int row = mt * 16 + mrow;
         if (tile >= ntiles || row >= mrows) return;
-        if constexpr (EPI == Epi::PLAIN) store_plain<AT, WT>(a, m0 + row, tile * 16 + 4 * q, v, ein[r], sa);
+        if constexpr (EPI == Epi::PLAIN) store_plain<AT, WT>(a, m0 + row, tile * 16 + 4 * q, v, ein[r], sa[r]);
         else store_gelu(a, m0 + row, tile * 16 + 4 * q, v, u, ein[r]);
     };
     constexpr int JU = (EPI == Epi::PLAIN) ? 0 : NT / 2;     // offset of the matching up tile
@@ -279,7 +295,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
         for (int r = 0; r < R; ++r) {
             const int pair = wave + r * WAVES, jo = pair / MT, mt = pair % MT;
             if (pair >= PAIRS || mt >= mt_count) continue;
-            finish(r, jo, mt, total(jo, mt), JU ? total(jo + JU, mt) : f32x4_t{});
+            finish(r, jo, mt, total(jo, mt), JU ? total(jo + JU, mt) : Acc{});
         }
         return;
     }
@@ -294,8 +310,8 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     for (int r = 0; r < R; ++r) {
         const int pair = wave + r * WAVES, jo = pair / MT, mt = pair % MT;
         if (pair >= PAIRS || mt >= mt_count) continue;
-        part.store(off(split, jo, mt), total(jo, mt));
-        if (JU) part.store(off(split, jo + JU, mt), total(jo + JU, mt));
+        part.store(off(split, jo, mt), __builtin_bit_cast(f32x4_t, total(jo, mt)));
+        if (JU) part.store(off(split, jo + JU, mt), __builtin_bit_cast(f32x4_t, total(jo + JU, mt)));
     }
     if (!splitk_arrive_last(a.tickets, slot, a.ksplit)) return;
     // the residual was not prefetched (only the last workgroup needs it)
@@ -311,11 +327,11 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     for (int r = 0; r < R; ++r) {
         const int pair = wave + r * WAVES, jo = pair / MT, mt = pair % MT;
         if (pair >= PAIRS || mt >= mt_count) continue;
-        f32x4_t v = part.load(off(0, jo, mt));
-        f32x4_t u = JU ? part.load(off(0, jo + JU, mt)) : f32x4_t{};
+        Acc v = __builtin_bit_cast(Acc, part.load(off(0, jo, mt)));
+        Acc u = JU ? __builtin_bit_cast(Acc, part.load(off(0, jo + JU, mt))) : Acc{};
         for (int sp = 1; sp < a.ksplit; ++sp) {
-            v += part.load(off(sp, jo, mt));
-            if (JU) u += part.load(off(sp, jo + JU, mt));
+            v += __builtin_bit_cast(Acc, part.load(off(sp, jo, mt)));
+            if (JU) u += __builtin_bit_cast(Acc, part.load(off(sp, jo + JU, mt)));
         }
         finish(r, jo, mt, v, u);
     }
@@ -468,7 +484,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
         }
     }
     p.waves = 8;
-    p.steps = (at == AType::FP8 && p.nt == 128) ? 128 : 64;   // K values per pipeline stage
+    p.steps = (at != AType::BF16 && p.nt == 128) ? 128 : 64;   // K values per pipeline stage
     p.wnw = p.waves / 2;
     const int64_t kt_total = (K + p.steps - 1) / p.steps;
     const int64_t base = static_cast<int64_t>(p.groups) * p.mblocks;
@@ -479,12 +495,13 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
     int ks = 1;
     while (base * (ks + 1) <= 256 && kt_total / (ks + 1) >= 8) ++ks;
     p.ksplit = ks;
-    const int64_t a_bytes = M * K * (at == AType::FP8 ? 1 : 2);
+    const int64_t a_bytes = M * K * (at == AType::BF16 ? 2 : 1);
     const int64_t w_bytes = (wt == WType::FP4) ? N * K / 2 + N * (((K >> 5) + 7) & ~int64_t(7))
-                                               : N * K * (wt == WType::FP8 ? 1 : 2);
-    // split-K counters: kWideCounters per output tile; partials addressed
-    // with 32-bit byte offsets
-    p.ok = base * kWideCounters <= kMaxCounters && a_bytes < (int64_t(1) << 31) && w_bytes < (int64_t(1) << 31) &&
+                                               : N * K * (wt == WType::BF16 ? 2 : 1);
+    // split-K counters: kWideCounters per output tile (8-bit integers, whose
+    // calls came later, may take more tiles where no K split uses them);
+    // partials addressed with 32-bit byte offsets
+    p.ok = (base * kWideCounters <= kMaxCounters || (at == AType::INT8 && p.ksplit == 1)) && a_bytes < (int64_t(1) << 31) && w_bytes < (int64_t(1) << 31) &&
            (p.ksplit == 1 || wide_part_bytes(p) < kMaxPartBytes);
     return p;
 }
@@ -520,6 +537,7 @@ hipError_t launch_gemm_plan(const GemmProblem& pr, const GemmPlan& p, hipStream_
     if (pr.wtype == WType::BF16) return launch_typed<AType::BF16, WType::BF16, Epi::PLAIN>(ka, p, s);
     if (pr.wtype == WType::FP4) return launch_typed<AType::BF16, WType::FP4, Epi::PLAIN>(ka, p, s);
     if (pr.atype == AType::FP8) return launch_typed<AType::FP8, WType::FP8, Epi::PLAIN>(ka, p, s);
+    if (pr.atype == AType::INT8) return launch_typed<AType::INT8, WType::INT8, Epi::PLAIN>(ka, p, s);
     return launch_typed<AType::BF16, WType::FP8, Epi::PLAIN>(ka, p, s);
 }
 

@@ -43,6 +43,12 @@ struct KArgs {
 // are outstanding (lgkmcnt and expcnt left unconstrained).
 constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | 0x0F70; }
 
+// Four or sixteen accumulators: fp32, or 32-bit integers where both operands are.
+template <AType AT, int N>
+struct AccT { typedef __attribute__((ext_vector_type(N))) float type; };
+template <int N>
+struct AccT<AType::INT8, N> { typedef __attribute__((ext_vector_type(N))) int type; };
+
 // ------------------------------------------------------------- epilogue
 
 // Epilogue inputs of one output fragment (row m, output columns n..n+3),
@@ -66,7 +72,7 @@ __device__ __forceinline__ EpiIn load_epi(const KArgs& a, int m, int n, bool wit
     e.bias = make_uint2(0, 0);
     e.bu = make_uint2(0, 0);
     e.resid = make_uint2(0, 0);
-    if (WT == WType::FP8) e.s = *reinterpret_cast<const float4*>(a.s_w + n);
+    if (WT == WType::FP8 || WT == WType::INT8) e.s = *reinterpret_cast<const float4*>(a.s_w + n);
     if (EPI == Epi::GELU_MUL) {
         e.su = *reinterpret_cast<const float4*>(a.s_w + (a.N >> 1) + n);
         if (a.bias) {
@@ -80,11 +86,33 @@ __device__ __forceinline__ EpiIn load_epi(const KArgs& a, int m, int n, bool wit
     return e;
 }
 
+// An integer sum times its row's and its column's scale.  The product of the
+// scales comes first unless it leaves fp32's normal range, where the whole
+// product may not (rows of 1e-20 times columns of 1e-20): then, and for a NaN
+// scale, in fp64.  Three roundings of 2^-24 at most.
+__device__ __forceinline__ float scale_sum(int v, float sa, float sw) {
+    const float p = sa * sw;
+    const float ap = __builtin_fabsf(p);
+    if (ap >= 0x1p-126f && ap < __builtin_inff()) return static_cast<float>(v) * p;
+    return static_cast<float>(static_cast<double>(v) * static_cast<double>(sa) * static_cast<double>(sw));
+}
+
 // y = v * scale (+ bias) -> bf16 for four columns (before any residual).
 template <AType AT, WType WT>
-__device__ __forceinline__ uint2 epi_plain4(const KArgs& a, f32x4_t v, const EpiIn& e, float sa) {
+__device__ __forceinline__ uint2 epi_plain4(const KArgs& a, typename AccT<AT, 4>::type v, const EpiIn& e, float sa) {
     const bool scaled = (WT == WType::FP8 || AT == AType::FP8);
-    float y[4] = {v[0], v[1], v[2], v[3]};
+    float y[4];
+    if constexpr (AT == AType::INT8) {
+        y[0] = scale_sum(v[0], sa, e.s.x);
+        y[1] = scale_sum(v[1], sa, e.s.y);
+        y[2] = scale_sum(v[2], sa, e.s.z);
+        y[3] = scale_sum(v[3], sa, e.s.w);
+    } else {
+        y[0] = v[0];
+        y[1] = v[1];
+        y[2] = v[2];
+        y[3] = v[3];
+    }
     if (scaled) {
         y[0] *= e.s.x * sa;
         y[1] *= e.s.y * sa;
@@ -107,7 +135,7 @@ __device__ __forceinline__ uint32_t add_resid2(uint32_t y, uint32_t r) {
 
 // y = v * scale (+ bias) -> bf16, then bf16(residual + y); four columns.
 template <AType AT, WType WT>
-__device__ __forceinline__ void store_plain(const KArgs& a, int m, int n, f32x4_t v, const EpiIn& e, float sa) {
+__device__ __forceinline__ void store_plain(const KArgs& a, int m, int n, typename AccT<AT, 4>::type v, const EpiIn& e, float sa) {
     uint2 o = epi_plain4<AT, WT>(a, v, e, sa);
     if (a.resid) {
         if (a.ypre) *reinterpret_cast<uint2*>(a.ypre + static_cast<int64_t>(m) * a.N + n) = o;

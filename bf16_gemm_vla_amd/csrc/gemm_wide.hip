@@ -52,9 +52,9 @@ struct WideCfg {
     static constexpr int BK = BK_;                              // K elements per pipeline stage
     static constexpr int WAVES = 2 * WNW;                       // 2 along M x WNW along N
     static constexpr int THREADS = 64 * WAVES;
-    static constexpr int AB = (AT == AType::FP8) ? 1 : 2;       // activation bytes / element
-    static constexpr int WLB = (WT == WType::FP8) ? 8 : (WT == WType::FP4 ? 4 : 16);   // weight bytes per lane slot
-    static constexpr int KMF = (AT == AType::FP8) ? 64 : 16;    // K of one MFMA
+    static constexpr int AB = (AT == AType::BF16) ? 2 : 1;      // activation bytes / element
+    static constexpr int WLB = (WT == WType::FP8 || WT == WType::INT8) ? 8 : (WT == WType::FP4 ? 4 : 16);   // weight bytes per lane slot
+    static constexpr int KMF = (AT == AType::BF16) ? 16 : 64;   // K of one MFMA (INT8: of two)
     static constexpr int NKS = BK / KMF;                        // MFMA steps per stage
     static constexpr int ARB = BK * AB;                         // A bytes per row per stage
     static constexpr int CPR = ARB / 16;                        // 16-byte chunks per A row
@@ -110,6 +110,7 @@ __device__ __forceinline__ int wide_wtile(int g, int tt, int N) {
 }
 
 typedef __attribute__((ext_vector_type(8))) int i32x8_t;
+typedef __attribute__((ext_vector_type(4))) int i32x4_t;
 
 // 16 bytes per lane from a buffer resource straight into LDS at
 // lds + 16 * lane (lds is wave-uniform); offsets past the resource read 0.
@@ -133,12 +134,14 @@ struct Frags<AType::FP8, WT, MSUB, NSUB> {
     u32x4_t a[MSUB][2];
     u32x2_t w[NSUB][4];
 };
+template <WType WT, int MSUB, int NSUB>
+struct Frags<AType::INT8, WT, MSUB, NSUB> : Frags<AType::FP8, WT, MSUB, NSUB> {};
 
 template <AType AT, WType WT, Epi EPI, int BN, int WNW, int BK>
 __global__ __launch_bounds__(128 * WNW) __attribute__((amdgpu_waves_per_eu(WNW / 2, WNW / 2)))
 void wide_gemm_kernel(KArgs a) {
     using C = WideCfg<AT, WT, BN, WNW, BK>;
-    static_assert(AT == AType::FP8 || BK == 64, "bf16 activations stage 64 K values (128 bytes per row)");
+    static_assert(AT != AType::BF16 || BK == 64, "bf16 activations stage 64 K values (128 bytes per row)");
     using F = Frags<AT, WT, C::MSUB, C::NSUB>;
     static_assert(EPI == Epi::PLAIN || (C::NSUB % 2 == 0 && AT == AType::BF16 && WT == WType::FP8),
                   "the fused gate/up epilogue pairs gate and up sub-tiles within a wave");
@@ -220,7 +223,7 @@ void wide_gemm_kernel(KArgs a) {
             } else {
                 constexpr int PER_TILE = C::WTB / 1024;
                 tt = j / PER_TILE;
-                const int chunk = (WT == WType::FP8) ? (lane ^ (8 * (tt & 1))) : lane;
+                const int chunk = (WT == WType::FP8 || WT == WType::INT8) ? (lane ^ (8 * (tt & 1))) : lane;
                 sb = (j % PER_TILE) * 1024 + chunk * 16;
             }
             const int gt = (j < C::W_LOADS) ? wide_wtile<EPI, BN, C::WN>(g, tt, a.N) : -1;   // pad slots: none
@@ -324,7 +327,8 @@ void wide_gemm_kernel(KArgs a) {
         }
     };
 
-    using Acc = __attribute__((ext_vector_type(16))) float;
+    using Acc = typename AccT<AT, 16>::type;
+    using Vec4 = typename AccT<AT, 4>::type;
     Acc acc[C::NSUB][C::MSUB];
 #pragma unroll
     for (int i = 0; i < C::NSUB; ++i)
@@ -368,6 +372,16 @@ void wide_gemm_kernel(KArgs a) {
                 if (idx < lo || idx >= hi) continue;
                 if constexpr (AT == AType::BF16) {
                     acc[ns][ms] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.wb[ns], as_bf16x8(f.a[ms]), acc[ns][ms], 0, 0, 0);
+                } else if constexpr (AT == AType::INT8) {
+                    // the step's 64 values of K in two products of 32, each
+                    // 16 from either lane half: their order does not matter
+                    // as long as both operands keep the same one
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const u32x4_t wop = {f.w[ns][2 * h].x, f.w[ns][2 * h].y, f.w[ns][2 * h + 1].x, f.w[ns][2 * h + 1].y};
+                        acc[ns][ms] = __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4_t, wop),
+                                                                            __builtin_bit_cast(i32x4_t, f.a[ms][h]), acc[ns][ms], 0, 0, 0);
+                    }
                 } else {
                     const i32x8_t wop = {(int)f.w[ns][0].x, (int)f.w[ns][0].y, (int)f.w[ns][1].x, (int)f.w[ns][1].y,
                                          (int)f.w[ns][2].x, (int)f.w[ns][2].y, (int)f.w[ns][3].x, (int)f.w[ns][3].y};
@@ -500,7 +514,12 @@ void wide_gemm_kernel(KArgs a) {
             if (n < ((EPI == Epi::PLAIN) ? a.N : (a.N >> 1))) ein[ns][rq] = load_epi<WT, EPI>(a, 0, n, false);
             else ein[ns][rq] = EpiIn{};
         }
-    const float sa = (AT == AType::FP8) ? *a.s_a : 1.0f;
+    float sa[C::MSUB];     // one for the tensor (FP8), or the lane's rows' (INT8)
+#pragma unroll
+    for (int ms = 0; ms < C::MSUB; ++ms) {
+        sa[ms] = (AT == AType::FP8) ? *a.s_a : 1.0f;
+        if (AT == AType::INT8 && m0 + wm * 96 + ms * 32 + l32 < a.M) sa[ms] = a.s_a[m0 + wm * 96 + ms * 32 + l32];
+    }
     // Wait for these loads here, once: gfx9 counts stores in vmcnt too, so a
     // wait for them placed after the first output stores would also wait for
     // every store issued so far.
@@ -541,7 +560,8 @@ void wide_gemm_kernel(KArgs a) {
 #pragma unroll
                 for (int rq = 0; rq < 4; ++rq) {
                     const Acc& v = acc[ns][ms];
-                    part.store(off(split, (ns * C::MSUB + ms) * 4 + rq), f32x4_t{v[4 * rq], v[4 * rq + 1], v[4 * rq + 2], v[4 * rq + 3]});
+                    part.store(off(split, (ns * C::MSUB + ms) * 4 + rq),
+                               __builtin_bit_cast(f32x4_t, Vec4{v[4 * rq], v[4 * rq + 1], v[4 * rq + 2], v[4 * rq + 3]}));
                 }
         };
         // the slices other workgroups may finish; an owner keeps its own
@@ -618,8 +638,12 @@ void wide_gemm_kernel(KArgs a) {
         for (int ms = 0; ms < C::MSUB; ++ms) {
             if (!(todo & (1u << ms))) continue;
             if (poisoned & (1u << ms)) {
+                if constexpr (AT == AType::INT8) {
+                    sa[ms] = __builtin_nanf("");                 // integers hold no NaN: the rows' scale does
+                } else {
 #pragma unroll
-                for (int ns = 0; ns < C::NSUB; ++ns) acc[ns][ms] = Acc{} + __builtin_nanf("");
+                    for (int ns = 0; ns < C::NSUB; ++ns) acc[ns][ms] = Acc{} + __builtin_nanf("");
+                }
                 continue;
             }
             // two splits' loads in flight at a time, summed in split order;
@@ -628,19 +652,19 @@ void wide_gemm_kernel(KArgs a) {
             const int reg_sp = (keep && ms == own) ? split : -1;
             auto part_or_reg = [&](int sp, int ns, int rq) __attribute__((always_inline)) {
                 const Acc& v = acc[ns][ms];
-                return sp == reg_sp ? f32x4_t{v[4 * rq], v[4 * rq + 1], v[4 * rq + 2], v[4 * rq + 3]}
-                                    : part.load(off(sp, (ns * C::MSUB + ms) * 4 + rq));
+                return sp == reg_sp ? Vec4{v[4 * rq], v[4 * rq + 1], v[4 * rq + 2], v[4 * rq + 3]}
+                                    : __builtin_bit_cast(Vec4, part.load(off(sp, (ns * C::MSUB + ms) * 4 + rq)));
             };
-            f32x4_t sum[C::NSUB][4];
+            Vec4 sum[C::NSUB][4];
             for (int sp = 0; sp < a.ksplit; sp += 2) {
-                f32x4_t p0[C::NSUB][4], p1[C::NSUB][4];
+                Vec4 p0[C::NSUB][4], p1[C::NSUB][4];
                 const bool two = sp + 1 < a.ksplit;
 #pragma unroll
                 for (int ns = 0; ns < C::NSUB; ++ns)
 #pragma unroll
                     for (int rq = 0; rq < 4; ++rq) {
                         p0[ns][rq] = part_or_reg(sp, ns, rq);
-                        p1[ns][rq] = two ? part_or_reg(sp + 1, ns, rq) : f32x4_t{};
+                        p1[ns][rq] = two ? part_or_reg(sp + 1, ns, rq) : Vec4{};
                     }
 #pragma unroll
                 for (int ns = 0; ns < C::NSUB; ++ns)
@@ -692,8 +716,8 @@ void wide_gemm_kernel(KArgs a) {
                     if (n >= a.N) continue;
                     const Acc& v = acc[ns][ms];
                     *reinterpret_cast<uint2*>(orow + nl * 2) =
-                        epi_plain4<AT, WT>(a, f32x4_t{v[4 * rq], v[4 * rq + 1], v[4 * rq + 2], v[4 * rq + 3]},
-                                           ein[ns][rq], sa);
+                        epi_plain4<AT, WT>(a, Vec4{v[4 * rq], v[4 * rq + 1], v[4 * rq + 2], v[4 * rq + 3]},
+                                           ein[ns][rq], sa[ms]);
                 }
             } else {
 #pragma unroll
@@ -779,7 +803,7 @@ hipError_t launch_wide(const gemm_detail::KArgs& ka, const GemmPlan& p, hipStrea
         VLA_WIDE_BF16W(VLA_WIDE)
     } else if constexpr (WT == WType::FP4) {
         VLA_WIDE_FP4W(VLA_WIDE)
-    } else if constexpr (AT == AType::FP8) {
+    } else if constexpr (AT != AType::BF16) {
         VLA_WIDE_FP8A(VLA_WIDE)
     } else {
         VLA_WIDE_BF16A(VLA_WIDE)
@@ -800,7 +824,8 @@ bool wide_dispatchable(const GemmPlan& p, AType at, WType wt, Epi epi) {
     } else if (wt == WType::FP4) {
         if (at != AType::BF16) return false;
         VLA_WIDE_FP4W(VLA_WIDE)
-    } else if (at == AType::FP8) {
+    } else if (at != AType::BF16) {
+        if ((at == AType::INT8) != (wt == WType::INT8)) return false;
         VLA_WIDE_FP8A(VLA_WIDE)
     } else {
         VLA_WIDE_BF16A(VLA_WIDE)
@@ -813,6 +838,7 @@ template hipError_t launch_wide<AType::BF16, WType::FP8, Epi::PLAIN>(const gemm_
 template hipError_t launch_wide<AType::BF16, WType::FP8, Epi::GELU_MUL>(const gemm_detail::KArgs&, const GemmPlan&, hipStream_t);
 template hipError_t launch_wide<AType::BF16, WType::BF16, Epi::PLAIN>(const gemm_detail::KArgs&, const GemmPlan&, hipStream_t);
 template hipError_t launch_wide<AType::FP8, WType::FP8, Epi::PLAIN>(const gemm_detail::KArgs&, const GemmPlan&, hipStream_t);
+template hipError_t launch_wide<AType::INT8, WType::INT8, Epi::PLAIN>(const gemm_detail::KArgs&, const GemmPlan&, hipStream_t);
 template hipError_t launch_wide<AType::BF16, WType::FP4, Epi::PLAIN>(const gemm_detail::KArgs&, const GemmPlan&, hipStream_t);
 
 }  // namespace vla

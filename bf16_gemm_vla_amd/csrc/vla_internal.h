@@ -23,6 +23,7 @@ hipError_t launch_reencode(const uint8_t* q, const float* sc, uint8_t* q2, float
 size_t quantize_act_ws_bytes(int64_t M, int64_t K);
 hipError_t launch_quantize_act(const uint16_t* A, uint8_t* qa, float* s_a, void* ws, int64_t M,
                                int64_t K, hipStream_t s);
+hipError_t launch_quantize_tokens_int8(const uint16_t* A, int8_t* qa, float* s_a, int64_t M, int64_t K, hipStream_t s);
 hipError_t launch_gate_residual_ada_norm(const uint16_t* resid, const uint16_t* out, const uint16_t* gate,
                                          const uint16_t* style, int style_per_row, float eps, uint16_t* r_out,
                                          uint16_t* h_out, uint16_t* ng_out, int64_t M, int64_t D, hipStream_t s);
@@ -128,15 +129,18 @@ hipError_t launch_quantize_act_static(const uint16_t* A, const float* s_a, uint8
                                       hipStream_t s);
 
 // ----------------------------------------------------------------- GEMM
-enum class AType { BF16 = 0, FP8 = 1 };
-enum class WType { BF16 = 0, FP8 = 1, FP4 = 2 };   // FP4: MXFP4 (E2M1 + E8M0 per 32 K)
+enum class AType { BF16 = 0, FP8 = 1, INT8 = 2 };
+enum class WType { BF16 = 0, FP8 = 1, FP4 = 2, INT8 = 3 };   // FP4: MXFP4 (E2M1 + E8M0 per 32 K); INT8 with INT8 A only
+// The longest sum of 8-bit products that any codes keep inside 32 bits:
+// K (2^7)^2 < 2^31 with K a multiple of 32.
+constexpr int64_t kMostInt8K = 131040;
 enum class Epi { PLAIN = 0, GELU_MUL = 1 };
 
 struct GemmProblem {
     const void* A;
-    const float* s_a;       // device scalar for FP8 A, else nullptr
+    const float* s_a;       // device scalar for FP8 A, M values for INT8 A, else nullptr
     const void* W;          // packed weights
-    const float* s_w;       // per-row scales (FP8 weights), else nullptr
+    const float* s_w;       // per-row scales (FP8 and INT8 weights), else nullptr
     const uint16_t* bias;   // nullable
     const uint16_t* resid;  // nullable
     uint16_t* Y;            // PLAIN: M x N; GELU_MUL: M x N/2

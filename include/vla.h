@@ -52,6 +52,7 @@ extern "C" {
 #define VLA_WFMT_E4M3_OCP 1   /* OCP E4M3: bias 7, max 448, NaN S.1111.111, no inf */
 #define VLA_WFMT_E4M3_FNUZ 2  /* E4M3 FNUZ: bias 8, max 240, NaN 0x80 only, no -0, no inf */
 #define VLA_WFMT_MXFP4 3      /* OCP MX FP4: E2M1 codes + one E8M0 scale per 32 values of K */
+#define VLA_WFMT_INT8 4       /* 8-bit integers within +-127 */
 
 /* Weight layouts. */
 #define VLA_LAYOUT_ROWMAJOR 0
@@ -98,10 +99,12 @@ size_t vla_packed_bytes(int64_t N, int64_t K, int wfmt);
  * at fixed addresses.
  *   W      device fp32, N x K row-major (one row per output channel).
  *   Wq     device output, vla_packed_bytes(N, K, wfmt) bytes, in `layout`.
- *   scales device fp32[N] output for FP8 formats, must be NULL for BF16.
+ *   scales device fp32[N] output for FP8 formats and INT8, must be NULL for BF16.
  * FP8: scales[n] = fp32(max_k |W[n,k]| / 448) (OCP) or / 240 (FNUZ), 1 for an
  * all-zero row; code = encode(fp32(W[n,k] / scales[n])), IEEE division,
  * round to nearest even, saturating at +-max.  BF16: round to nearest even.
+ * INT8: scales[n] = fp32(max_k |W[n,k]| / 127), 1 for an all-zero row; code =
+ * the integer nearest to fp32(W[n,k] / scales[n]), ties to even; both layouts.
  * MXFP4 (OCP Microscaling Formats v1.0; 4-bit weights as in "FlashRT: an
  * inference engine for real-time robot control", section 7.2, here in the
  * MX form gfx950 converts in hardware): per block of 32 values of K in one
@@ -116,8 +119,8 @@ size_t vla_packed_bytes(int64_t N, int64_t K, int wfmt);
 int vla_quantize_pack(const float *W, void *Wq, float *scales, int64_t N, int64_t K, int wfmt,
                       int layout, void *stream);
 
-/* Reorder an N x K row-major FP8 code matrix into VLA_LAYOUT_MFMA (a pure
- * byte permutation).  q_rowmajor and q_packed must not overlap. */
+/* Reorder an N x K row-major FP8 or INT8 code matrix into VLA_LAYOUT_MFMA (a
+ * pure byte permutation).  q_rowmajor and q_packed must not overlap. */
 int vla_pack_fp8(const uint8_t *q_rowmajor, uint8_t *q_packed, int64_t N, int64_t K,
                  void *stream);
 
@@ -158,6 +161,17 @@ int vla_quantize_act(const uint16_t *A, uint8_t *qa, float *s_a, void *ws, size_
  * aligned, else VLA_EALIGN. */
 int vla_quantize_act_static(const uint16_t *A, const float *s_a, uint8_t *qa, int64_t M, int64_t K,
                             void *stream);
+
+/* Tokens in 8-bit integers for vla_gemm_int8, a scale for each row of A: s_a[m]
+ * = fp32(max_k |A[m,k]| / 127), 1 for an all-zero row; qa[m,k] = the integer
+ * nearest to fp32(A[m,k] / s_a[m]), ties to even.  A row that holds an infinity
+ * or NaN gets zeros and a NaN scale, so its products are NaN; other rows are
+ * not touched by it.
+ *   A   device bf16 M x K;  qa device int8 M x K;  s_a device float[M].
+ * No workspace.  K a multiple of 32 (VLA_ESHAPE); outputs overlap neither A nor
+ * each other (VLA_EINVAL). */
+int vla_quantize_tokens_int8(const uint16_t *A, int8_t *qa, float *s_a, int64_t M, int64_t K,
+                             void *stream);
 
 /* ------------------------------------------------------- decoder boundary */
 
@@ -384,7 +398,7 @@ int vla_probe_mfma_rate(int form, const uint32_t *operands, int iters, float *ou
 
 /* ------------------------------------------------------------------ GEMM */
 
-/* Workspace for vla_gemm_fp8w / vla_gemm_bf16 / vla_gemm_fp8w_gelu_mul at
+/* Workspace for vla_gemm_fp8w / vla_gemm_bf16 / vla_gemm_int8 / vla_gemm_fp8w_gelu_mul at
  * this shape (N = weight rows; for gelu_mul N = 2 I).  Its first 60 KiB
  * hold the split-K arrival counters (the same place for every shape), the
  * next 4 KiB the status word (vla_workspace_status) and unused bytes; the
@@ -397,9 +411,9 @@ int vla_probe_mfma_rate(int form, const uint32_t *operands, int iters, float *ou
 size_t vla_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int wfmt);
 
 /* Host-only query, no device work: VLA_OK when a GEMM of this shape has a
- * compiled kernel configuration (wfmt VLA_WFMT_BF16 or VLA_WFMT_E4M3_OCP;
- * fp8_act: FP8 x FP8 with OCP activations; gelu_mul: the merged gate/up
- * GEMM with N = 2I), else the status the GEMM call itself would return
+ * compiled kernel configuration (wfmt VLA_WFMT_BF16, VLA_WFMT_E4M3_OCP,
+ * VLA_WFMT_MXFP4 or, for vla_gemm_int8, VLA_WFMT_INT8; fp8_act: FP8 x FP8 with
+ * OCP activations; gelu_mul: the merged gate/up GEMM with N = 2I), else the status the GEMM call itself would return
  * (EINVAL, ESHAPE). */
 int vla_gemm_supported(int64_t M, int64_t N, int64_t K, int wfmt, int fp8_act, int gelu_mul);
 
@@ -482,6 +496,27 @@ int vla_gemm_bf16(const uint16_t *A, const uint16_t *Wq, const uint16_t *bias,
 int vla_gemm_fp8w_gelu_mul(const uint16_t *A, const uint8_t *Wgu, const float *s_gu, const uint16_t *bias,
                            uint16_t *act, uint16_t *gu, void *ws, size_t ws_bytes, int64_t M,
                            int64_t I, int64_t K, void *stream);
+
+/* Product of 8-bit integers with a scale for each token and each channel:
+ *   Y[m,n] = bf16((sum_k A[m,k] Wq[n,k]) * s_a[m] * s_w[n] + bias[n]),
+ * then, with a residual, Y = bf16(residual + Y).  The sums are 32-bit integers
+ * and exact (any order, any K split: results are repeatable bit for bit and a
+ * row's do not depend on the other rows); scaled in fp32, or in fp64 where the
+ * product of the two scales leaves its normal range.  A NaN scale makes its
+ * row or column NaN.
+ *   A        device int8 M x K row-major, s_a device float[M]
+ *            (vla_quantize_tokens_int8, or any codes -128 .. 127 and scales);
+ *   Wq       device int8 N x K in VLA_LAYOUT_MFMA, s_w device float[N]
+ *            (vla_quantize_pack with VLA_WFMT_INT8);
+ *   bias     device bf16[N] or NULL;  residual device bf16 M x N or NULL, may
+ *            be Y;  Y device bf16 M x N, overlaps nothing else (VLA_EINVAL);
+ *   ws       zero-filled workspace of vla_gemm_workspace_bytes(M, N, K,
+ *            VLA_WFMT_INT8), as for vla_gemm_fp8w.
+ * N % 16 == 0, K % 32 == 0, K at most 131040, where no codes' sum leaves 32
+ * bits; M * K and N * K below 2^31 above 64 rows (VLA_ESHAPE). */
+int vla_gemm_int8(const int8_t *A, const float *s_a, const int8_t *Wq, const float *s_w,
+                  const uint16_t *bias, const uint16_t *residual, uint16_t *Y, void *ws,
+                  size_t ws_bytes, int64_t M, int64_t N, int64_t K, void *stream);
 
 /* As vla_gemm_fp8w with MXFP4 weights (bf16 activations, no per-channel
  * scale: each 32-value block of a weight row carries its E8M0 scale):

@@ -43,3 +43,45 @@ def test_axes_refuses_overlaps():
     for change in (dict(q_out=base["positions"] + 32), dict(k_out=base["axis_of"]), dict(k_cache=base["v"]),
                    dict(q_out=base["q"] + 16)):
         refused("vla_qk_norm_rope_axes_append", axes_args(**change), EINVAL, "overlap")
+
+
+def tokens_args(**change):
+    return dict(A=A, qa=A + GB, s_a=A + 2 * GB, M=4, K=64) | change
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(A=None), EINVAL), (dict(qa=None), EINVAL), (dict(s_a=None), EINVAL), (dict(A=A + 8), EALIGN), (dict(s_a=A + 4), EALIGN),
+    (dict(M=0), EINVAL), (dict(K=0), EINVAL), (dict(K=48), ESHAPE), (dict(M=(1 << 24) + 1), ESHAPE), (dict(qa=A), EINVAL),
+    (dict(s_a=A + 16), EINVAL), (dict(s_a=A + GB + 64), EINVAL), (dict(qa=A + 496), EINVAL)])
+def test_tokens_refuses(change, code):
+    refused("vla_quantize_tokens_int8", tokens_args(**change), code)
+
+
+def product_args(**change):
+    names = ["A", "s_a", "Wq", "s_w", "bias", "residual", "Y", "ws"]
+    a = {n: A + i * GB for i, n in enumerate(names)}
+    return a | dict(ws_bytes=1 << 28, M=50, N=64, K=128) | change
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(A=None), EINVAL), (dict(s_a=None), EINVAL), (dict(Wq=None), EINVAL), (dict(s_w=None), EINVAL), (dict(Y=None), EINVAL),
+    (dict(ws=None), EINVAL), (dict(bias=A + 2), EALIGN), (dict(residual=A + 8), EALIGN), (dict(M=0), EINVAL), (dict(N=24), ESHAPE),
+    (dict(K=48), ESHAPE), (dict(K=131072), ESHAPE), (dict(ws_bytes=100), EWS), (dict(Y=A), EINVAL), (dict(Y=A + 2 * GB), EINVAL),
+    (dict(Y=A + GB + 64), EINVAL), (dict(Y=A + 4 * GB), EINVAL), (dict(Y=A + 5 * GB + 16), EINVAL),
+    (dict(M=1 << 24, K=1024, residual=None, Y=A + 64 * GB), ESHAPE),
+    (dict(M=100, N=1 << 25, K=128, residual=None, Y=A + 64 * GB), ESHAPE)])
+def test_product_refuses(change, code):
+    refused("vla_gemm_int8", product_args(**change), code)
+
+
+def test_int8_plans():
+    n = vla.VLA_WFMT_INT8
+    assert vla.vla_packed_bytes(64, 128, n) == 64 * 128
+    for M in (1, 10, 50, 64, 65, 571, 768, 8191, 16384):
+        for N, K in ((4096, 1024), (1024, 4096), (16384, 2048), (2048, 16384), (16, 32), (1040, 96)):
+            rc, info = vla.vla_gemm_plan(M, N, K, n)
+            assert rc == 0 and info[6] == vla.vla_gemm_workspace_bytes(M, N, K, n), (M, N, K)
+            assert info[5] == 1 or info[9] <= 15360
+    assert vla.vla_gemm_supported(50, 64, 131040, n) == 0 and vla.vla_gemm_supported(50, 64, 131072, n) == ESHAPE
+    assert vla.vla_gemm_supported(50, 64, 64, n, fp8_act=True) == EINVAL
+    assert vla.vla_gemm_supported(50, 64, 64, n, gelu_mul=True) == EINVAL
