@@ -776,6 +776,86 @@ int vla_qk_norm_rope_axes_append(const uint16_t* q, const uint16_t* k, const uin
 }
 
 namespace {
+// Pages and blocks of a cache with a scale per block of tokens and head.
+int check_pages(const char* fn, int64_t num_pages, int64_t page_size) {
+    if (num_pages <= 0 || page_size <= 0)
+        return fail(VLA_EINVAL, fn, "num_pages=%lld page_size=%lld must be positive", (long long)num_pages, (long long)page_size);
+    if ((page_size & (page_size - 1)) != 0 || page_size > 65536)
+        return fail(VLA_ESHAPE, fn, "page_size=%lld must be a power of two, at most 65536", (long long)page_size);
+    if (num_pages >= (int64_t(1) << 31) || num_pages * page_size >= (int64_t(1) << 31))
+        return fail(VLA_ESHAPE, fn, "num_pages=%lld of %lld rows too large", (long long)num_pages, (long long)page_size);
+    return VLA_OK;
+}
+int check_block(const char* fn, int64_t block_size, int64_t page_size) {
+    if (block_size <= 0) return fail(VLA_EINVAL, fn, "block_size=%lld must be positive", (long long)block_size);
+    if ((block_size & (block_size - 1)) != 0 || block_size > 128 || block_size > page_size)
+        return fail(VLA_ESHAPE, fn, "block_size=%lld must be a power of two, at most 128 and page_size=%lld", (long long)block_size,
+                    (long long)page_size);
+    return VLA_OK;
+}
+}  // namespace
+
+int vla_kv_append_e4m3(const uint16_t* k, const uint16_t* v, const int32_t* cu_rows, const int32_t* block_table,
+                       const int32_t* seq_lens, uint8_t* k_cache, uint8_t* v_cache, uint8_t* k_scales,
+                       uint8_t* v_scales, int64_t B, int64_t L, int64_t total, int64_t Hkv, int64_t D,
+                       int64_t num_pages, int64_t page_size, int64_t block_size, int64_t pages_per_seq,
+                       int64_t k_stride, int64_t v_stride, void* stream) {
+    const char* fn = "vla_kv_append_e4m3";
+    REQUIRE_PTR(k);
+    REQUIRE_PTR(v);
+    OPTIONAL_PTR(cu_rows);
+    REQUIRE_PTR(block_table);
+    REQUIRE_PTR(seq_lens);
+    REQUIRE_PTR(k_cache);
+    REQUIRE_PTR(v_cache);
+    REQUIRE_PTR(k_scales);
+    REQUIRE_PTR(v_scales);
+    if (B <= 0 || L <= 0 || total <= 0 || pages_per_seq <= 0)
+        return fail(VLA_EINVAL, fn, "B=%lld L=%lld total=%lld pages_per_seq=%lld must be positive", (long long)B, (long long)L,
+                    (long long)total, (long long)pages_per_seq);
+    if (B > (int64_t(1) << 20) || L > (int64_t(1) << 30) || total > (int64_t(1) << 30))
+        return fail(VLA_ESHAPE, fn, "B=%lld L=%lld total=%lld too large", (long long)B, (long long)L, (long long)total);
+    if (!cu_rows && total != B * L)
+        return fail(VLA_ESHAPE, fn, "without cu_rows total=%lld must be B * L = %lld", (long long)total, (long long)(B * L));
+    if (int rc = check_heads(fn, Hkv, Hkv, D)) return rc;
+    if (int rc = check_pages(fn, num_pages, page_size)) return rc;
+    if (int rc = check_block(fn, block_size, page_size)) return rc;
+    if (pages_per_seq >= (int64_t(1) << 30) || pages_per_seq * page_size >= (int64_t(1) << 30))
+        return fail(VLA_ESHAPE, fn, "pages_per_seq=%lld of %lld rows too large", (long long)pages_per_seq, (long long)page_size);
+    if (int rc = check_stride(fn, "k_stride", k_stride, Hkv * D)) return rc;
+    if (int rc = check_stride(fn, "v_stride", v_stride, Hkv * D)) return rc;
+    if (L > total) L = total;                                     // no sequence has more
+    const vla::AppendPlan p = vla::plan_kv_append(B, L, total, Hkv, block_size);
+    if (p.items > vla::kMostWorkgroups)
+        return fail(VLA_ESHAPE, fn, "B=%lld L=%lld total=%lld of %lld heads are too many blocks for one launch", (long long)B,
+                    (long long)L, (long long)total, (long long)Hkv);
+    const size_t rows = static_cast<size_t>(num_pages) * page_size;
+    const size_t codes = rows * Hkv * D, scales = rows / block_size * Hkv;
+    const Region outs[4] = {flat(k_cache, codes), flat(v_cache, codes), flat(k_scales, scales), flat(v_scales, scales)};
+    const Region ins[5] = {{k, total, Hkv * D, k_stride}, {v, total, Hkv * D, v_stride}, flat(cu_rows, (B + 1) * 4),
+                           flat(block_table, B * pages_per_seq * 4), flat(seq_lens, B * 4)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 5; ++j)
+            if (regions_overlap(outs[i], ins[j])) return fail(VLA_EINVAL, fn, "output %d overlaps input %d", i, j);
+        for (int j = i + 1; j < 4; ++j)
+            if (regions_overlap(outs[i], outs[j])) return fail(VLA_EINVAL, fn, "outputs %d and %d overlap", i, j);
+    }
+    vla::AppendArgs a{};
+    a.k = k; a.v = v; a.cu_rows = cu_rows; a.block_table = block_table; a.seq_lens = seq_lens;
+    a.k_cache = k_cache; a.v_cache = v_cache; a.k_scales = k_scales; a.v_scales = v_scales;
+    a.k_stride = k_stride; a.v_stride = v_stride;
+    a.B = static_cast<int>(B); a.L = static_cast<int>(L); a.total = static_cast<int>(total);
+    a.Hkv = static_cast<int>(Hkv); a.D = static_cast<int>(D);
+    a.page_log2 = __builtin_ctzll(static_cast<unsigned long long>(page_size));
+    a.block_log2 = __builtin_ctzll(static_cast<unsigned long long>(block_size));
+    a.pages_per_seq = static_cast<int>(pages_per_seq);
+    a.capacity = static_cast<int>(pages_per_seq * page_size);
+    a.num_pages = static_cast<uint32_t>(num_pages);
+    hipError_t e = vla::launch_kv_append_e4m3(a, p, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+
+namespace {
 // The kernels work with scale * log2(e).
 int check_scale(const char* fn, float scale) {
     if (!std::isfinite(scale) || scale <= 0.0f || !std::isfinite(scale * 1.4426950408889634f))

@@ -75,6 +75,26 @@ struct Divisor {
 // fewer than 2^32 threads, 256 to a workgroup.
 constexpr int64_t kMostWorkgroups = (int64_t(1) << 24) - 1;
 
+struct AppendArgs {
+    const uint16_t *k, *v;
+    const int32_t *cu_rows;                    // nullable: L rows per sequence
+    const int32_t *block_table, *seq_lens;
+    uint8_t *k_cache, *v_cache, *k_scales, *v_scales;
+    int64_t k_stride, v_stride;
+    int B, L, total, Hkv, D, page_log2, block_log2, pages_per_seq, capacity;
+    uint32_t num_pages;
+    // set by the launcher
+    int dense, items, gw, gw_log2;
+    Divisor by_most, by_heads2;
+};
+// Work items of an append, from its host sizes alone.
+struct AppendPlan {
+    bool dense;          // `most` items per sequence, else as many as it has blocks
+    int64_t most, items; // items with the heads, keys and values apart
+};
+AppendPlan plan_kv_append(int64_t B, int64_t L, int64_t total, int64_t Hkv, int64_t block);
+hipError_t launch_kv_append_e4m3(AppendArgs a, const AppendPlan& p, hipStream_t s);
+
 struct PromptArgs {
     const uint16_t *q, *k, *v;
     const int32_t *cu_q, *cu_k;

@@ -346,6 +346,48 @@ int vla_attn_shared_prefix(const uint16_t *q, const uint16_t *k_cache, const uin
                            int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
                            int causal, float scale, void *stream);
 
+/* The cache in eight bits.  k_cache and v_cache: device OCP E4M3 codes, paged
+ * and laid out as above (a byte in the place of each bf16).  k_scales and
+ * v_scales: device E8M0 bytes (2^(byte - 127); 255 is NaN), one for every
+ * block_size rows and head: the scale of row r of page p and head h is byte
+ * ((p * page_size + r) / block_size) * Hkv + h.  A cached value is its code's
+ * value times its scale.  block_size is a power of two, at most 128 and
+ * page_size (VLA_ESHAPE).
+ *
+ * The append quantizes the newest rows of B sequences into their pages: the
+ * m_b new rows of sequence b become its rows n_b - m_b .. n_b - 1, row j in page
+ * block_table[b][j / page_size].  For each block and head that gets new rows
+ *   scale = 2^e, the least with max |x| <= 448 2^e over the new rows (e >= -127),
+ *           or the block's scale where it holds earlier rows and that is larger
+ *           (a scale byte of 255 counts as 254);
+ *   code  = the E4M3 value nearest to x / 2^e, ties to even (x finite; the
+ *           division is exact); an infinity or NaN becomes the code 0x7F (NaN)
+ *           and does not count for the scale.
+ * Where the scale of a block with earlier rows grows, their codes are encoded
+ * again under it: exactly, but for values that leave E4M3's normal range, which
+ * round (to nearest) once more; NaN codes stay.  A block whose first row is new
+ * is started afresh, whatever its codes and scale were.  Rows behind the newest
+ * one keep their codes (and mean nothing).
+ *   k, v         device bf16, `total` rows of Hkv heads (vla_qk_norm_rope_append's
+ *                k_out and the QKV GEMM's rows), rows *_stride elements apart;
+ *   cu_rows      device int32[B + 1], rows cu_rows[b] .. cu_rows[b+1]-1 are
+ *                sequence b's (bounded to 0 .. total; the first L count), or
+ *                NULL: L rows each, and total == B * L (VLA_ESHAPE);
+ *   seq_lens     device int32[B], n_b with the new rows, bounded to 0 ..
+ *                pages_per_seq * page_size; new rows that would lie before row 0
+ *                and rows on pages outside 0 .. num_pages-1 are not appended.
+ * The blocks that a call appends to must be one sequence's each, and named once.
+ * A shared prefix is appended with B = 1, its page list as the block table and
+ * its length as seq_lens.  L: the most rows that a sequence has.  B in 1 .. 2^20,
+ * L and total in 1 .. 2^30, pages_per_seq * page_size < 2^30, and what one
+ * launch holds: Hkv * (min(total, total / block_size + 2 * B)) below 2^23 always
+ * fits (VLA_ESHAPE). */
+int vla_kv_append_e4m3(const uint16_t* k, const uint16_t* v, const int32_t* cu_rows, const int32_t* block_table,
+                       const int32_t* seq_lens, uint8_t* k_cache, uint8_t* v_cache, uint8_t* k_scales,
+                       uint8_t* v_scales, int64_t B, int64_t L, int64_t total, int64_t Hkv, int64_t D,
+                       int64_t num_pages, int64_t page_size, int64_t block_size, int64_t pages_per_seq,
+                       int64_t k_stride, int64_t v_stride, void* stream);
+
 /* ----------------------------------------------------------- measurement */
 
 /* Streaming-read probe: one launch of `blocks` workgroups of 256 threads

@@ -42,15 +42,14 @@ def e8m0_value(byte):
 
 
 def e4m3_code(x):
-    """Nearest code, ties to even, saturating; NaN and infinities the NaN code with their sign (NaN's is 0)."""
+    """Nearest code, ties to even, saturating; 0x7F for what is not finite."""
     x = np.asarray(x, np.float64)
     a = np.where(np.isfinite(x), np.abs(x), 0.0)
     spacing = np.exp2(np.floor(np.log2(np.maximum(a, 2.0 ** -6))) - 3)
     v = np.minimum(np.round(a / spacing) * spacing, 448.0)
     codes = np.argsort(E4M3[:127], kind="stable")
     c = codes[np.searchsorted(E4M3[:127][codes], v)].astype(np.uint8)
-    c = np.where(np.isfinite(x), c, 0x7F).astype(np.uint8)
-    return np.where(np.signbit(x) & ~np.isnan(x), c | 0x80, c).astype(np.uint8)
+    return np.where(np.isfinite(x), np.where(np.signbit(x), c | 0x80, c), 0x7F).astype(np.uint8)
 
 
 def scale_byte(most):

@@ -85,3 +85,26 @@ def test_int8_plans():
     assert vla.vla_gemm_supported(50, 64, 131040, n) == 0 and vla.vla_gemm_supported(50, 64, 131072, n) == ESHAPE
     assert vla.vla_gemm_supported(50, 64, 64, n, fp8_act=True) == EINVAL
     assert vla.vla_gemm_supported(50, 64, 64, n, gelu_mul=True) == EINVAL
+
+
+def append_args(**change):
+    names = ["k", "v", "cu_rows", "block_table", "seq_lens", "k_cache", "v_cache", "k_scales", "v_scales"]
+    a = {n: A + i * GB for i, n in enumerate(names)}
+    a |= dict(B=3, L=2, total=6, Hkv=2, D=64, num_pages=100, page_size=16, block_size=16, pages_per_seq=4, k_stride=128,
+              v_stride=128)
+    return a | change
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(block_table=None), EINVAL), (dict(seq_lens=None), EINVAL),
+    (dict(k_cache=None), EINVAL), (dict(v_scales=None), EINVAL), (dict(k_scales=A + 8), EALIGN), (dict(cu_rows=A + 4), EALIGN),
+    (dict(B=0), EINVAL), (dict(L=0), EINVAL), (dict(total=0), EINVAL), (dict(pages_per_seq=0), EINVAL), (dict(B=(1 << 20) + 1), ESHAPE),
+    (dict(total=(1 << 30) + 1), ESHAPE), (dict(cu_rows=None, total=7), ESHAPE), (dict(Hkv=0), EINVAL), (dict(Hkv=4097, k_stride=1 << 20), ESHAPE),
+    (dict(D=60), ESHAPE), (dict(D=264), ESHAPE), (dict(num_pages=0), EINVAL), (dict(page_size=24), ESHAPE), (dict(page_size=1 << 17), ESHAPE),
+    (dict(num_pages=1 << 28), ESHAPE), (dict(block_size=0), EINVAL), (dict(block_size=-16), EINVAL), (dict(block_size=12), ESHAPE),
+    (dict(block_size=32), ESHAPE), (dict(page_size=256, block_size=256), ESHAPE), (dict(k_stride=120), ESHAPE), (dict(v_stride=132), ESHAPE),
+    (dict(pages_per_seq=1 << 27), ESHAPE), (dict(k_cache=A), EINVAL), (dict(v_cache=A + 5 * GB), EINVAL), (dict(v_scales=A + 7 * GB), EINVAL),
+    (dict(k_scales=A + 6 * GB + 64), EINVAL), (dict(v_cache=A + 4 * GB), EINVAL),
+    (dict(B=1 << 20, total=1 << 26, L=1 << 20, block_size=1), ESHAPE)])
+def test_kv_append_refuses(change, code):
+    refused("vla_kv_append_e4m3", append_args(**change), code)
