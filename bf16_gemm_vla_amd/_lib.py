@@ -61,6 +61,8 @@ SIGNATURES = {
     "vla_attn_shared_prefix_workspace_bytes": (SZ, [I64] * 7),
     "vla_attn_shared_prefix": (INT, [P] * 9 + [SZ] + [I64] * 11 + [INT, ctypes.c_float, P]),
     "vla_kv_append_e4m3": (INT, [P] * 9 + [I64] * 11 + [P]),
+    "vla_attn_shared_prefix_e4m3_workspace_bytes": (SZ, [I64] * 7),
+    "vla_attn_shared_prefix_e4m3": (INT, [P] * 11 + [SZ] + [I64] * 12 + [INT, ctypes.c_float, P]),
     "vla_probe_stream_read": (INT, [P, SZ, P, INT, P]),
     "vla_probe_mfma_rate": (INT, [INT, P, INT, P, P, INT, P]),
     "vla_gate_residual_ada_norm": (INT, [P, P, P, P, INT, ctypes.c_float, P, P, P, I64, I64, P]),
@@ -276,6 +278,20 @@ def vla_kv_append_e4m3(k, v, cu_rows, block_table, seq_lens, k_cache, v_cache, k
                                      _ptr(v_cache), _ptr(k_scales), _ptr(v_scales), B, L, total, Hkv, D, num_pages,
                                      page_size, block_size, pages_per_seq, k_stride, v_stride, _stream(stream)),
            "vla_kv_append_e4m3")
+
+
+def vla_attn_shared_prefix_e4m3_workspace_bytes(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity) -> int:
+    return load().vla_attn_shared_prefix_e4m3_workspace_bytes(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity)
+
+
+def vla_attn_shared_prefix_e4m3(q, k_cache, v_cache, k_scales, v_scales, prefix_pages, prefix_len, block_table, seq_lens, out,
+                                ws, ws_bytes, B, L, Hq, Hkv, D, num_pages, page_size, block_size, n_prefix_pages,
+                                pages_per_seq, q_stride, out_stride, causal, scale, stream=None):
+    _check(load().vla_attn_shared_prefix_e4m3(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+                                              _ptr(prefix_pages), _ptr(prefix_len), _ptr(block_table), _ptr(seq_lens),
+                                              _ptr(out), _ptr(ws), ws_bytes, B, L, Hq, Hkv, D, num_pages, page_size,
+                                              block_size, n_prefix_pages, pages_per_seq, q_stride, out_stride, int(causal),
+                                              scale, _stream(stream)), "vla_attn_shared_prefix_e4m3")
 
 
 # ----------------------------------------------------------------- probes

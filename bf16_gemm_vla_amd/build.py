@@ -21,7 +21,7 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libvla.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["codec.hip", "gemm.hip", "gemm_wide.hip", "chain.hip", "boundary.hip", "rope.hip", "cache_e4m3.hip", "attention.hip", "probe.hip", "abi.cpp"]
+SOURCES = ["codec.hip", "gemm.hip", "gemm_wide.hip", "chain.hip", "boundary.hip", "rope.hip", "cache_e4m3.hip", "attention.hip", "attention_e4m3.hip", "probe.hip", "abi.cpp"]
 HIPFLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -32,7 +32,7 @@ HIPFLAGS = [
 # may use 512: with the accumulation registers the attention kernels of 256
 # channels moved every score and output through copies (1649 of 6924
 # instructions).
-FILEFLAGS = {"attention.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+FILEFLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] for f in ("attention.hip", "attention_e4m3.hip")}
 
 
 # Host-side AddressSanitizer + UndefinedBehaviorSanitizer for the checking

@@ -936,16 +936,21 @@ size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, 
     return static_cast<size_t>(p.ws_bytes);
 }
 
-int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
-                           const int32_t* prefix_pages, const int32_t* prefix_len, const int32_t* block_table,
-                           const int32_t* seq_lens, uint16_t* out, void* ws, size_t ws_bytes, int64_t B, int64_t L,
-                           int64_t Hq, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
-                           int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
-                           int causal, float scale, void* stream) {
-    const char* fn = "vla_attn_shared_prefix";
+namespace {
+// Attention over either cache; block_size 0: bf16 rows, else E4M3 codes.
+int shared_prefix(const char* fn, const uint16_t* q, const void* k_cache, const void* v_cache, const uint8_t* k_scales,
+                  const uint8_t* v_scales, const int32_t* prefix_pages, const int32_t* prefix_len,
+                  const int32_t* block_table, const int32_t* seq_lens, uint16_t* out, void* ws, size_t ws_bytes, int64_t B,
+                  int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size, bool codes,
+                  int64_t block_size, int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
+                  int causal, float scale, void* stream) {
     REQUIRE_PTR(q);
     REQUIRE_PTR(k_cache);
     REQUIRE_PTR(v_cache);
+    if (codes) {
+        REQUIRE_PTR(k_scales);
+        REQUIRE_PTR(v_scales);
+    }
     OPTIONAL_PTR(prefix_pages);
     OPTIONAL_PTR(prefix_len);
     OPTIONAL_PTR(block_table);
@@ -961,6 +966,8 @@ int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uin
         n_prefix_pages >= (int64_t(1) << 30) || pages_per_seq >= (int64_t(1) << 30))
         return fail(VLA_ESHAPE, fn, "num_pages=%lld n_prefix_pages=%lld pages_per_seq=%lld of %lld rows too large", (long long)num_pages,
                     (long long)n_prefix_pages, (long long)pages_per_seq, (long long)page_size);
+    if (codes)
+        if (int rc = check_block(fn, block_size, page_size)) return rc;
     if ((prefix_pages != nullptr) != (n_prefix_pages > 0) || (prefix_len != nullptr) != (n_prefix_pages > 0))
         return fail(VLA_EINVAL, fn, "prefix_pages and prefix_len must be given exactly when n_prefix_pages > 0");
     if ((block_table != nullptr) != (pages_per_seq > 0) || (seq_lens != nullptr) != (pages_per_seq > 0))
@@ -974,17 +981,19 @@ int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uin
     if (int rc = check_scale(fn, scale)) return rc;
     if (ws_bytes < static_cast<size_t>(p.ws_bytes))
         return fail(VLA_EWORKSPACE, fn, "workspace %zu bytes < required %lld", ws_bytes, (long long)p.ws_bytes);
-    const size_t cache_bytes = static_cast<size_t>(num_pages) * page_size * Hkv * D * 2;
+    const size_t cache_bytes = static_cast<size_t>(num_pages) * page_size * Hkv * D * (codes ? 1 : 2);
+    const size_t scale_bytes = codes ? static_cast<size_t>(num_pages) * page_size / block_size * Hkv : 0;
     const Region outs[2] = {{out, B * L, Hq * D, out_stride}, flat(ws, static_cast<size_t>(p.ws_bytes))};
-    const Region ins[7] = {{q, B * L, Hq * D, q_stride}, flat(k_cache, cache_bytes), flat(v_cache, cache_bytes),
+    const Region ins[9] = {{q, B * L, Hq * D, q_stride}, flat(k_cache, cache_bytes), flat(v_cache, cache_bytes),
                            flat(prefix_pages, n_prefix_pages * 4), flat(prefix_len, prefix_len ? 4 : 0),
-                           flat(block_table, B * pages_per_seq * 4), flat(seq_lens, B * 4)};
+                           flat(block_table, B * pages_per_seq * 4), flat(seq_lens, B * 4), flat(k_scales, scale_bytes),
+                           flat(v_scales, scale_bytes)};
     for (int i = 0; i < 2; ++i)
-        for (int j = 0; j < 7; ++j)
+        for (int j = 0; j < 9; ++j)
             if (regions_overlap(outs[i], ins[j])) return fail(VLA_EINVAL, fn, "%s overlaps input %d", i ? "ws" : "out", j);
     if (regions_overlap(outs[0], outs[1])) return fail(VLA_EINVAL, fn, "out overlaps ws");
     vla::SharedArgs a{};
-    a.q = q; a.k_cache = k_cache; a.v_cache = v_cache;
+    a.q = q; a.k_cache = static_cast<const uint16_t*>(k_cache); a.v_cache = static_cast<const uint16_t*>(v_cache);
     a.prefix_pages = prefix_pages; a.prefix_len = prefix_len; a.block_table = block_table; a.seq_lens = seq_lens;
     a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
     a.B = static_cast<int>(B); a.L = static_cast<int>(L);
@@ -995,8 +1004,43 @@ int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uin
     a.pages_per_seq = static_cast<int>(pages_per_seq);
     a.prefix_cap = static_cast<int>(prefix_cap); a.suffix_cap = static_cast<int>(suffix_cap);
     a.num_pages = static_cast<uint32_t>(num_pages);
-    hipError_t e = vla::launch_attn_shared(a, p, ws, static_cast<hipStream_t>(stream));
+    a.k_scales = k_scales; a.v_scales = v_scales;
+    a.block_log2 = codes ? __builtin_ctzll(static_cast<unsigned long long>(block_size)) : 0;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e = codes ? vla::launch_attn_shared_e4m3(a, p, ws, s) : vla::launch_attn_shared(a, p, ws, s);
     return e == hipSuccess ? VLA_OK : hip_fail(fn, "kernel launch", e);
+}
+}  // namespace
+
+int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uint16_t* v_cache,
+                           const int32_t* prefix_pages, const int32_t* prefix_len, const int32_t* block_table,
+                           const int32_t* seq_lens, uint16_t* out, void* ws, size_t ws_bytes, int64_t B, int64_t L,
+                           int64_t Hq, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                           int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
+                           int causal, float scale, void* stream) {
+    return shared_prefix("vla_attn_shared_prefix", q, k_cache, v_cache, nullptr, nullptr, prefix_pages, prefix_len, block_table,
+                         seq_lens, out, ws, ws_bytes, B, L, Hq, Hkv, D, num_pages, page_size, false, 0, n_prefix_pages,
+                         pages_per_seq, q_stride, out_stride, causal, scale, stream);
+}
+
+size_t vla_attn_shared_prefix_e4m3_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
+                                                   int64_t prefix_capacity, int64_t suffix_capacity) {
+    vla::SharedPlan p;
+    if (check_shared("vla_attn_shared_prefix_e4m3_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, p) != VLA_OK)
+        return 0;
+    return static_cast<size_t>(p.ws_bytes);
+}
+
+int vla_attn_shared_prefix_e4m3(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* prefix_pages,
+                                const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
+                                uint16_t* out, void* ws, size_t ws_bytes, int64_t B, int64_t L, int64_t Hq, int64_t Hkv,
+                                int64_t D, int64_t num_pages, int64_t page_size, int64_t block_size,
+                                int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
+                                int causal, float scale, void* stream) {
+    return shared_prefix("vla_attn_shared_prefix_e4m3", q, k_cache, v_cache, k_scales, v_scales, prefix_pages, prefix_len,
+                         block_table, seq_lens, out, ws, ws_bytes, B, L, Hq, Hkv, D, num_pages, page_size, true, block_size,
+                         n_prefix_pages, pages_per_seq, q_stride, out_stride, causal, scale, stream);
 }
 
 int vla_probe_stream_read(const void* src, size_t bytes, uint32_t* sink, int blocks, void* stream) {

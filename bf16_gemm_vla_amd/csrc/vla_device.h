@@ -106,6 +106,17 @@ __device__ __forceinline__ bf16x8_t ocp8_to_bf16x8(u32x2_t w) {
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// Eight OCP E4M3 codes times a power of two -> eight bf16 in four dwords,
+// exact but where a value leaves bf16's range.
+__device__ __forceinline__ u32x4_t ocp8_to_bf16x8_scaled(u32x2_t w, float scale) {
+    const bf16x2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, scale, false);
+    const bf16x2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, scale, true);
+    const bf16x2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, scale, false);
+    const bf16x2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, scale, true);
+    return u32x4_t{__builtin_bit_cast(uint32_t, p0), __builtin_bit_cast(uint32_t, p1), __builtin_bit_cast(uint32_t, p2),
+                   __builtin_bit_cast(uint32_t, p3)};
+}
+
 // E8M0 block scale -> fp32 2^(e - 127) (e = 0 is the subnormal 2^-127).
 __device__ __forceinline__ float e8m0_to_f32(uint32_t e) {
     return __uint_as_float(e ? (e << 23) : 0x00400000u);

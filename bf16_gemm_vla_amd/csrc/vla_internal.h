@@ -128,6 +128,9 @@ struct SharedArgs {
     int merged, prefix_items, prefix_splits, suffix_splits, suffix_tiles, parts;
     Divisor by_group, by_q_heads, by_prefix_pairs, by_prefix_splits, by_suffix_pairs, by_suffix_splits, by_suffix_tiles;
     float *part_ml, *part_o;
+    // a cache in codes alone
+    const uint8_t *k_scales, *v_scales;
+    int block_log2;
 };
 // Launch plan of a shared-prefix call, from its host sizes alone.
 struct SharedPlan {
@@ -141,6 +144,10 @@ struct SharedPlan {
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
                             int64_t suffix_cap);
 hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipStream_t s);
+// The same over a cache in E4M3 codes (k_cache and v_cache point to bytes).
+hipError_t launch_attn_shared_e4m3(SharedArgs a, const SharedPlan& p, void* ws, hipStream_t s);
+void prepare_attn_shared(SharedArgs& a, const SharedPlan& p, void* ws);     // the launcher's fields
+hipError_t launch_attn_join(const SharedArgs& a, const SharedPlan& p, hipStream_t s);
 
 hipError_t launch_stream_read(const void* src, size_t bytes, uint32_t* sink, int blocks, hipStream_t s);
 hipError_t launch_mfma_rate(int form, const uint32_t* src, int iters, float* out, uint64_t* clocks, int blocks,

@@ -388,6 +388,26 @@ int vla_kv_append_e4m3(const uint16_t* k, const uint16_t* v, const int32_t* cu_r
                        int64_t num_pages, int64_t page_size, int64_t block_size, int64_t pages_per_seq,
                        int64_t k_stride, int64_t v_stride, void* stream);
 
+/* vla_attn_shared_prefix over the cache in eight bits: a key and a value are
+ * their codes' values times their blocks' scales.  Arguments, masks, sums and
+ * roundings are vla_attn_shared_prefix's, and so is the result over a bf16 cache of
+ * those values (they are bf16 numbers, but for products past its range: codes of
+ * 2^128 and more with their scale count as infinities, parts below 2^-133
+ * round).  A NaN code, and any code under the scale byte 255, is NaN to the rows
+ * that see it and has no part in others.
+ *   k_cache, v_cache, k_scales, v_scales, block_size  as vla_kv_append_e4m3 leaves them;
+ *   ws   device workspace of vla_attn_shared_prefix_e4m3_workspace_bytes, to
+ *        which the same applies as above. */
+size_t vla_attn_shared_prefix_e4m3_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
+                                                   int64_t prefix_capacity, int64_t suffix_capacity);
+int vla_attn_shared_prefix_e4m3(const uint16_t* q, const uint8_t* k_cache, const uint8_t* v_cache,
+                                const uint8_t* k_scales, const uint8_t* v_scales, const int32_t* prefix_pages,
+                                const int32_t* prefix_len, const int32_t* block_table, const int32_t* seq_lens,
+                                uint16_t* out, void* ws, size_t ws_bytes, int64_t B, int64_t L, int64_t Hq, int64_t Hkv,
+                                int64_t D, int64_t num_pages, int64_t page_size, int64_t block_size,
+                                int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
+                                int causal, float scale, void* stream);
+
 /* ----------------------------------------------------------- measurement */
 
 /* Streaming-read probe: one launch of `blocks` workgroups of 256 threads

@@ -108,3 +108,32 @@ def append_args(**change):
     (dict(B=1 << 20, total=1 << 26, L=1 << 20, block_size=1), ESHAPE)])
 def test_kv_append_refuses(change, code):
     refused("vla_kv_append_e4m3", append_args(**change), code)
+
+
+def attention_args(**change):
+    names = ["q", "k_cache", "v_cache", "k_scales", "v_scales", "prefix_pages", "prefix_len", "block_table", "seq_lens", "out", "ws"]
+    a = {n: A + i * GB for i, n in enumerate(names)}
+    a |= dict(ws_bytes=1 << 28, B=3, L=2, Hq=4, Hkv=2, D=64, num_pages=100, page_size=16, block_size=16, n_prefix_pages=20,
+              pages_per_seq=4, q_stride=256, out_stride=256, causal=0, scale=0.125)
+    return a | change
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(q=None), EINVAL), (dict(k_cache=None), EINVAL), (dict(v_cache=None), EINVAL), (dict(k_scales=None), EINVAL),
+    (dict(v_scales=None), EINVAL), (dict(out=None), EINVAL), (dict(ws=None), EINVAL), (dict(k_scales=A + 4), EALIGN),
+    (dict(prefix_pages=A + 4), EALIGN), (dict(B=0), EINVAL), (dict(L=0), EINVAL), (dict(num_pages=0), EINVAL), (dict(page_size=24), ESHAPE),
+    (dict(num_pages=1 << 28), ESHAPE), (dict(block_size=0), EINVAL), (dict(block_size=-1), EINVAL), (dict(block_size=24), ESHAPE),
+    (dict(block_size=32), ESHAPE), (dict(page_size=256, block_size=256), ESHAPE), (dict(prefix_pages=None), EINVAL),
+    (dict(seq_lens=None), EINVAL), (dict(pages_per_seq=0), EINVAL), (dict(Hq=5), ESHAPE), (dict(D=20), ESHAPE), (dict(q_stride=200), ESHAPE),
+    (dict(out_stride=128), ESHAPE), (dict(causal=-1), EINVAL), (dict(scale=0.0), EINVAL), (dict(scale=3e38), EINVAL), (dict(ws_bytes=0), EWS),
+    (dict(n_prefix_pages=1 << 26), ESHAPE), (dict(out=A), EINVAL), (dict(out=A + 2 * GB), EINVAL), (dict(ws=A + 4 * GB + 64), EINVAL),
+    (dict(out=A + 3 * GB), EINVAL), (dict(out=A + 10 * GB), EINVAL)])
+def test_attention_refuses(change, code):
+    refused("vla_attn_shared_prefix_e4m3", attention_args(**change), code)
+
+
+def test_attention_workspace_query():
+    n = vla.vla_attn_shared_prefix_e4m3_workspace_bytes
+    assert n(0, 1, 4, 2, 64, 16, 16) == 0 and n(1, 1, 4, 2, 64, 0, 0) == 0 and n(1, 1, 5, 2, 64, 16, 16) == 0
+    assert n(1, 1, 32, 8, 128, 0, 131072) > 0
+    assert n(1 << 20, 1 << 10, 2, 1, 8, 16, 16) == 0
