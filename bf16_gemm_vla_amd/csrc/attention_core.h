@@ -139,12 +139,20 @@ struct PagedCodes : PageTable {
         Hkv = a.Hkv;
         block_log2 = a.block_log2;
     }
-    // A slot's two scales as bf16 bits, the keys' in the high half: a power of
-    // two with eight exponent bits is a bf16 number.
-    __device__ __forceinline__ uint32_t scales(int slot) const {
-        const int64_t at = static_cast<int64_t>(slot >> block_log2) * Hkv;
-        const uint32_t ek = k_scales[at], ev = v_scales[at];
-        return scale_bits(ek) << 16 | scale_bits(ev);
+    // A slot's two scale bytes (of slot 0 where there is none: a load that no
+    // branch holds back)
+    struct Bytes {
+        uint32_t k, v;
+    };
+    __device__ __forceinline__ Bytes bytes_of(int slot) const {
+        const int64_t at = static_cast<int64_t>(max(slot, 0) >> block_log2) * Hkv;
+        return {k_scales[at], v_scales[at]};
+    }
+    // Both scales as bf16 bits, the keys' in the high half: a power of two with
+    // eight exponent bits is a bf16 number.  0 where there is no slot, so that
+    // the zeros loaded there stay zeros.
+    static __device__ __forceinline__ uint32_t scales(Bytes b, int slot) {
+        return slot >= 0 ? scale_bits(b.k) << 16 | scale_bits(b.v) : 0;
     }
     // 2^(byte - 127): 2^-127 is subnormal, 255 is NaN
     static __device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return byte == 0 ? 0x0040u : (byte == 255 ? 0x7FC0u : byte << 7); }
@@ -331,6 +339,7 @@ struct Walk {
         u32x4_t kf[C::NK];
 #pragma unroll
         for (int kk = 0; kk < C::NK; ++kk) kf[kk] = *reinterpret_cast<const u32x4_t*>(kt + (kaddr ^ (kk << 5)));
+        if constexpr (Keys::CODES) __builtin_amdgcn_sched_barrier(0);   // all reads on their way before the first product
         f32x16_t sc = f32x16_t{};
 #pragma unroll
         for (int kk = 0; kk < C::NK; ++kk) {
@@ -495,7 +504,7 @@ struct Walk {
         if (sl < 0 || !q || key >= klim) return;
         const uint8_t* const kr = keys.k + static_cast<int64_t>(sl) * keys.stride;
         const uint8_t* const vr = keys.v + static_cast<int64_t>(sl) * keys.stride;
-        const uint32_t sw = keys.scales(sl);
+        const uint32_t sw = Keys::scales(keys.bytes_of(sl), sl);
         const float ks = __uint_as_float(sw & 0xFFFF0000u), vs = __uint_as_float(sw << 16);
         float s = 0.0f;
         for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * (decode_e4m3<false>(kr[d]) * ks);
@@ -519,7 +528,7 @@ struct Walk {
         u32x2_t x[C::NI];
     };
     struct Exponents {
-        uint32_t x[C::NI];     // the rows' scales, keys' and values' (PagedCodes::scales)
+        uint32_t x[C::NI];     // the rows' scales (PagedCodes::scales)
     };
     __device__ __forceinline__ Exponents exponents_of(uint32_t scales, int from) const {
         Exponents e;
@@ -782,16 +791,15 @@ __device__ __forceinline__ void attend_code_stages(const Keys& keys, const uint1
     uint8_t* const qt = (part.qg < PER ? kb1 : vb1) + (part.qg % PER) * 32 * C::RB;
     w.template stage_q<32 / WPG / C::RPI>(q, qt, part.wave / C::QG * (32 / WPG));
     typename W::Codes ck, cv;
-    uint64_t vnext;
-    uint32_t scales;
+    int slot;
+    typename Keys::Bytes bytes;
     const typename W::Source ks = w.template source<false>(0, 0), vs = w.template source<true>(0, 0);
     auto fetch = [&](int s) __attribute__((always_inline)) {
-        const int slot = slot_of(s, page);
-        scales = slot >= 0 ? keys.scales(slot) : 0;
+        slot = slot_of(s, page);
+        bytes = keys.bytes_of(slot);
         const typename W::Slots sl = w.slots_of(slot, row0);
         w.template fetch<false>(ks, sl, row0, ck);
         w.template fetch<true>(vs, sl, row0, cv);
-        vnext = __ballot(slot >= 0);
         page = entry(s + 1);
     };
     fetch(0);
@@ -812,8 +820,8 @@ __device__ __forceinline__ void attend_code_stages(const Keys& keys, const uint1
     for (int s = 0; s < n_stages; ++s) {
         uint8_t* const kc = s & 1 ? kb1 : kb0;
         uint8_t* const vc = s & 1 ? vb1 : vb0;
-        const uint64_t vcur = vnext;
-        const typename W::Exponents e = w.exponents_of(scales, row0);
+        const uint64_t vcur = __ballot(slot >= 0);
+        const typename W::Exponents e = w.exponents_of(Keys::scales(bytes, slot), row0);
         w.template put<false>(ck, e, kc + row0 * C::RB);
         w.template put<true>(cv, e, vc + row0 * C::RB);
         wait_here<kWaitLds>();
@@ -856,11 +864,11 @@ __device__ __forceinline__ void attend_code_streams(const Keys& keys, const uint
     w.template stage_q<8 / C::RPI>(q, vb_all, wave * 8);
     typename W::Codes ck, cv;
     int slot = -1;
-    uint32_t scales = 0;
+    typename Keys::Bytes bytes;
     const typename W::Source ks = w.template source<false>(0, 0), vs = w.template source<true>(0, 0);
     auto fetch = [&](int t) __attribute__((always_inline)) {
         slot = slot_of(t, page);
-        scales = slot >= 0 ? keys.scales(slot) : 0;
+        bytes = keys.bytes_of(slot);
         const typename W::Slots sl = w.slots_of(slot, 0);
         w.template fetch<false>(ks, sl, 0, ck);
         w.template fetch<true>(vs, sl, 0, cv);
@@ -879,7 +887,7 @@ __device__ __forceinline__ void attend_code_streams(const Keys& keys, const uint
     for (int t = 0; t < n; ++t) {
         const int key0 = first + t * 128;
         const uint32_t vm = static_cast<uint32_t>(__ballot(slot >= 0));
-        const typename W::Exponents e = w.exponents_of(scales, 0);
+        const typename W::Exponents e = w.exponents_of(Keys::scales(bytes, slot), 0);
         w.template put<false>(ck, e, kb);
         w.template put<true>(cv, e, vb);
         if (t + 1 < n) fetch(t + 1);
