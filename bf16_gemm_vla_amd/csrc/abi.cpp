@@ -909,7 +909,7 @@ int vla_attn_prompt(const uint16_t* q, const uint16_t* k, const uint16_t* v, con
 namespace {
 // Sizes of a shared-prefix call that do not depend on its pointers, and their plan.
 int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap, int64_t suffix_cap,
-                 vla::SharedPlan& p) {
+                 bool codes, vla::SharedPlan& p) {
     if (B <= 0 || L <= 0) return fail(VLA_EINVAL, fn, "B=%lld L=%lld must be positive", (long long)B, (long long)L);
     if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
     if (prefix_cap < 0 || suffix_cap < 0 || prefix_cap + suffix_cap == 0)
@@ -920,7 +920,7 @@ int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, 
         prefix_cap + suffix_cap >= (int64_t(1) << 31) - (int64_t(1) << 16))
         return fail(VLA_ESHAPE, fn, "B=%lld L=%lld Hq=%lld or the capacities %lld, %lld too large", (long long)B, (long long)L,
                     (long long)Hq, (long long)prefix_cap, (long long)suffix_cap);
-    p = vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_cap, suffix_cap);
+    p = vla::plan_attn_shared(B, L, Hq, Hkv, D, prefix_cap, suffix_cap, codes);
     if (p.workgroups > vla::kMostWorkgroups)
         return fail(VLA_ESHAPE, fn, "B=%lld L=%lld of %lld heads are too many rows for one launch", (long long)B, (long long)L,
                     (long long)Hq);
@@ -931,7 +931,7 @@ int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, 
 size_t vla_attn_shared_prefix_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
                                               int64_t prefix_capacity, int64_t suffix_capacity) {
     vla::SharedPlan p;
-    if (check_shared("vla_attn_shared_prefix_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, p) != VLA_OK)
+    if (check_shared("vla_attn_shared_prefix_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, false, p) != VLA_OK)
         return 0;
     return static_cast<size_t>(p.ws_bytes);
 }
@@ -974,7 +974,7 @@ int shared_prefix(const char* fn, const uint16_t* q, const void* k_cache, const 
         return fail(VLA_EINVAL, fn, "block_table and seq_lens must be given exactly when pages_per_seq > 0");
     const int64_t prefix_cap = n_prefix_pages * page_size, suffix_cap = pages_per_seq * page_size;
     vla::SharedPlan p;
-    if (int rc = check_shared(fn, B, L, Hq, Hkv, D, prefix_cap, suffix_cap, p)) return rc;
+    if (int rc = check_shared(fn, B, L, Hq, Hkv, D, prefix_cap, suffix_cap, codes, p)) return rc;
     if (int rc = check_stride(fn, "q_stride", q_stride, Hq * D)) return rc;
     if (int rc = check_stride(fn, "out_stride", out_stride, Hq * D)) return rc;
     if (causal != 0 && causal != 1) return fail(VLA_EINVAL, fn, "causal=%d must be 0 or 1", causal);
@@ -1026,7 +1026,7 @@ int vla_attn_shared_prefix(const uint16_t* q, const uint16_t* k_cache, const uin
 size_t vla_attn_shared_prefix_e4m3_workspace_bytes(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D,
                                                    int64_t prefix_capacity, int64_t suffix_capacity) {
     vla::SharedPlan p;
-    if (check_shared("vla_attn_shared_prefix_e4m3_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, p) != VLA_OK)
+    if (check_shared("vla_attn_shared_prefix_e4m3_workspace_bytes", B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, true, p) != VLA_OK)
         return 0;
     return static_cast<size_t>(p.ws_bytes);
 }

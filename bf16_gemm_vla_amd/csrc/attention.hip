@@ -274,7 +274,7 @@ __global__ __launch_bounds__(kAThreads) void attn_join_kernel(SharedArgs a) {
 constexpr int kComputeUnits = 256;
 
 // Keys of a workgroup's step.
-int step_keys(int64_t D, int tm) { return D <= 128 && tm == 32 ? 128 : 64; }
+int step_keys(int64_t D, int tm, bool codes) { return (D <= 128 && tm == 32) || (codes && tm <= 32) ? 128 : 64; }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -315,7 +315,7 @@ hipError_t launch_attn_prompt(PromptArgs a, const PromptPlan& p, hipStream_t s) 
 }
 
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
-                            int64_t suffix_cap) {
+                            int64_t suffix_cap, bool codes) {
     SharedPlan p{};
     const int64_t G = Hq / Hkv, rows_s = L * G, rows_p = B * rows_s;
     // As for prompts: narrow tiles where all of them run at once, and none that
@@ -324,12 +324,22 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // the keys in two parts; 100 single tokens behind 4000 keys, 32 heads on 8
     // of 128: 33 us with 32 rows, 50 with 128).
     const int64_t slots = (D > 128 ? 1 : 2) * kComputeUnits;
+    // Over a cache in codes, 16 rows where those tiles run at once too, three
+    // workgroups per compute unit (16 chunks of 10 rows over 850 keys, 32 heads
+    // on 8 of 128: 17.6 us, with 32 rows 24.0), and no taller few-row tile above
+    // 128 channels, where 32 rows would not fit the registers.
     auto tile = [&](int64_t batches, int64_t rows) {
         int tm = 128;
         while (tm > 32 && (2 * rows <= tm || Hkv * batches * ceil_div(rows, tm / 2) <= slots)) tm /= 2;
+        if (codes && tm == 32 && (rows <= 16 || D > 128 || Hkv * batches * ceil_div(rows, 16) <= 3 * kComputeUnits)) tm = 16;
         return tm;
     };
     p.prefix_tm = tile(1, rows_p);
+    // A long prefix is worth 32 rows, which bring its codes half as often (64
+    // single tokens of 32 heads on 8 of 128 with 300 keys of their own behind
+    // 8000: 37.6 us, with 16 rows 47.6; behind 2051 with up to 3000 of their own
+    // 71.5, with 16 rows 61.6).
+    if (codes && p.prefix_tm == 16 && rows_p > 16 && D <= 128 && prefix_cap > 4096) p.prefix_tm = 32;
     p.suffix_tm = tile(B, rows_s);
     // A sequence whose rows fill its tiles reads the prefix no more often by
     // itself than a tile of the whole batch does: then the prefix is the head
@@ -344,9 +354,11 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // 2000, 128 rows: 287 us, two launches 241; 600 with 64 shared and up to
     // 1500 own keys, 64 rows: 403 us, two launches 396).
     if (!p.merged && p.prefix_tm == 64) p.suffix_tm = 64;
+    // one launch for both as well where both are few
+    if (codes && !p.merged && p.prefix_tm <= 32 && p.suffix_tm <= 32) p.suffix_tm = p.prefix_tm = std::max(p.prefix_tm, p.suffix_tm);
     const int64_t keys_s = suffix_cap + (p.merged ? prefix_cap : 0);
-    const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(D, p.prefix_tm));
-    const int64_t steps_s = ceil_div(keys_s, step_keys(D, p.suffix_tm));
+    const int64_t steps_p = p.merged ? 0 : ceil_div(prefix_cap, step_keys(D, p.prefix_tm, codes));
+    const int64_t steps_s = ceil_div(keys_s, step_keys(D, p.suffix_tm, codes));
     const int64_t tiles_p = p.merged ? 0 : ceil_div(rows_p, p.prefix_tm);
     p.suffix_tiles = ceil_div(rows_s, p.suffix_tm);
     // Keys are split as often as the workgroups fit the compute units once (32
@@ -357,13 +369,24 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // for those, but from 129 to 256 workgroups, where this rule does not
     // split, it is ahead: 20 such tokens 436 us, halved 323, the bytes' time
     // 312.  With 64 of them the sequences fill the GPU (891 us, the bytes' 860).
-    auto splits = [&](int64_t tiles, int64_t steps) {
+    auto splits = [&](int64_t tiles, int64_t steps, int tm) {
         if (tiles == 0 || steps == 0) return int64_t(0);
-        const int64_t most = kComputeUnits / tiles;
+        int64_t most = kComputeUnits / tiles;
+        if (codes && tm <= 32) {
+            // Few rows over codes take twice as many workgroups, whose loads
+            // overlap (one token over 131071 keys: 65 us, with 256 workgroups
+            // 69), and sequences, whose lengths differ, six times as many while
+            // a part keeps 1024 keys: the long ones' parts then even out (32
+            // heads on 8 of 128: 20 tokens over up to 20000 keys 114 us, with
+            // 512 workgroups 125; 64 over up to 3000 58, with 512 61; 64 over
+            // 1500 each 46, with parts of 512 keys 50).
+            most = 2 * kComputeUnits / tiles;
+            if (B > 1) most = std::max(most, std::min(6 * kComputeUnits / tiles, steps / 8));
+        }
         return most <= 1 ? int64_t(1) : ceil_div(steps, ceil_div(steps, most));
     };
-    p.prefix_splits = splits(Hkv * tiles_p, steps_p);
-    p.suffix_splits = splits(Hkv * B * p.suffix_tiles, steps_s);
+    p.prefix_splits = splits(Hkv * tiles_p, steps_p, 64);
+    p.suffix_splits = splits(Hkv * B * p.suffix_tiles, steps_s, p.suffix_tm);
     p.prefix_items = Hkv * tiles_p * p.prefix_splits;
     p.suffix_items = Hkv * B * p.suffix_tiles * p.suffix_splits;
     p.parts = p.prefix_splits + p.suffix_splits;

@@ -155,7 +155,7 @@ struct PagedCodes : PageTable {
         return slot >= 0 ? scale_bits(b.k) << 16 | scale_bits(b.v) : 0;
     }
     // 2^(byte - 127): 2^-127 is subnormal, 255 is NaN
-    static __device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return byte == 0 ? 0x0040u : (byte == 255 ? 0x7FC0u : byte << 7); }
+    static __device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return (byte << 7) + (byte == 0 || byte == 255 ? 0x0040u : 0u); }
 };
 
 // A wave's partial result for its 32 rows: lane = row l % 32, O^T unnormalised,
@@ -767,10 +767,10 @@ __device__ __forceinline__ void attend_streams(const Keys& keys, const uint16_t*
     });
 }
 
-// The same walks over a cache in codes.  A stage's codes are fetched while the
-// one before it is computed, two registers to eight values, and enter its
-// buffers at the step's start; its barrier also says that the buffers' reads of
-// two steps ago are done.
+// The walk of shared stages over a cache in codes.  A stage's codes are fetched
+// two steps ahead, two registers to eight values, and enter LDS a step ahead:
+// the conversions go out among the products of the stage before, each half of a
+// step taking the keys' or the values'.
 template <class C, class Keys>
 __device__ __forceinline__ void attend_code_stages(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                                    uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1, State<C>& st) {
@@ -791,18 +791,19 @@ __device__ __forceinline__ void attend_code_stages(const Keys& keys, const uint1
     uint8_t* const qt = (part.qg < PER ? kb1 : vb1) + (part.qg % PER) * 32 * C::RB;
     w.template stage_q<32 / WPG / C::RPI>(q, qt, part.wave / C::QG * (32 / WPG));
     typename W::Codes ck, cv;
+    typename W::Slots sl;
     int slot;
     typename Keys::Bytes bytes;
     const typename W::Source ks = w.template source<false>(0, 0), vs = w.template source<true>(0, 0);
-    auto fetch = [&](int s) __attribute__((always_inline)) {
+    auto locate = [&](int s) __attribute__((always_inline)) {
         slot = slot_of(s, page);
         bytes = keys.bytes_of(slot);
-        const typename W::Slots sl = w.slots_of(slot, row0);
-        w.template fetch<false>(ks, sl, row0, ck);
-        w.template fetch<true>(vs, sl, row0, cv);
+        sl = w.slots_of(slot, row0);
         page = entry(s + 1);
     };
-    fetch(0);
+    locate(0);
+    w.template fetch<false>(ks, sl, row0, ck);
+    w.template fetch<true>(vs, sl, row0, cv);
     wait_here<wait_vm(0)>();
     if constexpr (WPG > 1) {
         __builtin_amdgcn_s_barrier();
@@ -810,97 +811,69 @@ __device__ __forceinline__ void attend_code_stages(const Keys& keys, const uint1
     }
     w.read_q(qt);
     w.address(0, part.hv);
-    auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm) __attribute__((always_inline)) {
+    uint64_t vcur = __ballot(slot >= 0);
+    {
+        const typename W::Exponents e = w.exponents_of(Keys::scales(bytes, slot), row0);
+        w.template put<false>(ck, e, kb0 + row0 * C::RB);
+        w.template put<true>(cv, e, vb0 + row0 * C::RB);
+    }
+    if (n_stages > 1) {
+        locate(1);
+        w.template fetch<false>(ks, sl, row0, ck);
+        w.template fetch<true>(vs, sl, row0, cv);
+    }
+    auto sub_tile = [&](const uint8_t* kt, const uint8_t* vt, int key0, uint32_t vm, auto&& first, auto&& then) __attribute__((always_inline)) {
         f32x16_t sc = w.template scores<0>(kt, [](int) {});
+        first();
         w.scale_and_mask(sc, key0, vm);
         uint32_t pw[8];
         w.template weights<0>(sc, pw, [](int) {});
+        then();
         if (!w.put_off(vt, key0, k1)) w.add(vt, pw);
     };
-    for (int s = 0; s < n_stages; ++s) {
-        uint8_t* const kc = s & 1 ? kb1 : kb0;
-        uint8_t* const vc = s & 1 ? vb1 : vb0;
-        const uint64_t vcur = __ballot(slot >= 0);
-        const typename W::Exponents e = w.exponents_of(Keys::scales(bytes, slot), row0);
-        w.template put<false>(ck, e, kc + row0 * C::RB);
-        w.template put<true>(cv, e, vc + row0 * C::RB);
+    auto step = [&](uint8_t* kc, uint8_t* vc, uint8_t* kn, uint8_t* vn, int s, auto more) __attribute__((always_inline)) {
+        // stage s is in its buffers and every wave is done with those of stage s - 1
         wait_here<kWaitLds>();
         __builtin_amdgcn_s_barrier();
         __atomic_signal_fence(__ATOMIC_SEQ_CST);
-        if (s + 1 < n_stages) fetch(s + 1);
         const int key0 = k0 + s * C::ST;
+        typename W::Exponents e;
+        uint64_t vnext = 0;
+        if constexpr (more()) {
+            e = w.exponents_of(Keys::scales(bytes, slot), row0);
+            vnext = __ballot(slot >= 0);
+        }
+        auto move_k = [&]() __attribute__((always_inline)) {
+            if constexpr (more()) {
+                w.template put<false>(ck, e, kn + row0 * C::RB);
+                locate(s + 2);                                    // past the end: zeros
+                w.template fetch<false>(ks, sl, row0, ck);
+            }
+        };
+        auto move_v = [&]() __attribute__((always_inline)) {
+            if constexpr (more()) {
+                w.template put<true>(cv, e, vn + row0 * C::RB);
+                w.template fetch<true>(vs, sl, row0, cv);
+            }
+        };
         if constexpr (C::SUBS == 2) {
-            sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur));
-            sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32));
+            sub_tile(kc, vc, key0, static_cast<uint32_t>(vcur), move_k, [] {});
+            sub_tile(kc + 32 * C::RB, vc + 32 * C::RB, key0 + 32, static_cast<uint32_t>(vcur >> 32), move_v, [] {});
         } else {
             const int at = part.kg * 32;
-            sub_tile(kc + at * C::RB, vc + at * C::RB, key0 + at, static_cast<uint32_t>(vcur >> at));
+            sub_tile(kc + at * C::RB, vc + at * C::RB, key0 + at, static_cast<uint32_t>(vcur >> at), move_k, move_v);
         }
+        vcur = vnext;
+    };
+    for (int s = 0; s + 1 < n_stages; s += 2) {
+        step(kb0, vb0, kb1, vb1, s, std::true_type{});
+        if (s + 2 < n_stages) step(kb1, vb1, kb0, vb0, s + 1, std::true_type{});
     }
+    step(n_stages % 2 ? kb0 : kb1, n_stages % 2 ? vb0 : vb1, nullptr, nullptr, n_stages - 1, std::false_type{});
     st.l = half_sum(st.l);
     w.add_late(q, k1, [&](int key) {
         const int t = key - k0;
         return (t >> 5 & (C::KG - 1)) == part.kg ? k0 + (t & ~31) : -1;
-    });
-}
-
-// Every wave on its own: wave w takes sub-tiles w, w + 4, ...
-template <class C, class Keys>
-__device__ __forceinline__ void attend_code_streams(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
-                                                    uint8_t* kb_all, uint8_t* vb_all, State<C>& st) {
-    using W = Walk<C, Keys>;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    uint8_t* const kb = kb_all + wave * 32 * C::RB;
-    uint8_t* const vb = vb_all + wave * 32 * C::RB;
-    const int first = k0 + wave * 32;
-    const int n = k1 > first ? (k1 - first + 127) / 128 : 0;
-    auto entry = [&](int t) __attribute__((always_inline)) { return keys.entry(min(first + t * 128 + static_cast<int>(threadIdx.x & 31), k1 - 1)); };
-    auto slot_of = [&](int t, int32_t page) __attribute__((always_inline)) {
-        const int key = first + t * 128 + (threadIdx.x & 31);
-        return key < k1 ? keys.slot(key, page) : -1;
-    };
-    int32_t page = n > 0 ? entry(0) : 0;
-    W w(keys, klim, D, c, st, q != nullptr);
-    w.template stage_q<8 / C::RPI>(q, vb_all, wave * 8);
-    typename W::Codes ck, cv;
-    int slot = -1;
-    typename Keys::Bytes bytes;
-    const typename W::Source ks = w.template source<false>(0, 0), vs = w.template source<true>(0, 0);
-    auto fetch = [&](int t) __attribute__((always_inline)) {
-        slot = slot_of(t, page);
-        bytes = keys.bytes_of(slot);
-        const typename W::Slots sl = w.slots_of(slot, 0);
-        w.template fetch<false>(ks, sl, 0, ck);
-        w.template fetch<true>(vs, sl, 0, cv);
-        page = entry(t + 1);
-    };
-    if (n > 0) fetch(0);
-    wait_here<wait_vm(0)>();
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    w.read_q(vb_all);
-    w.address(wave * 32 * C::RB, 0);
-    wait_here<kWaitLds>();
-    __builtin_amdgcn_s_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    if (n <= 0) return;
-    for (int t = 0; t < n; ++t) {
-        const int key0 = first + t * 128;
-        const uint32_t vm = static_cast<uint32_t>(__ballot(slot >= 0));
-        const typename W::Exponents e = w.exponents_of(Keys::scales(bytes, slot), 0);
-        w.template put<false>(ck, e, kb);
-        w.template put<true>(cv, e, vb);
-        if (t + 1 < n) fetch(t + 1);
-        f32x16_t sc = w.template scores<0>(kb_all, [](int) {});
-        w.scale_and_mask(sc, key0, vm);
-        uint32_t pw[8];
-        w.template weights<0>(sc, pw, [](int) {});
-        if (!w.put_off(vb, key0, k1)) w.add(vb_all, pw);
-    }
-    st.l = half_sum(st.l);
-    w.add_late(q, k1, [&](int key) {
-        const int t = key - k0;
-        return (t >> 5 & 3) == wave ? k0 + (t & ~31) : -1;
     });
 }
 
@@ -1011,13 +984,9 @@ __device__ __forceinline__ void write_rows(const State<C>& st, uint64_t to, floa
 template <class C, class Keys>
 __device__ __forceinline__ void attend(const Keys& keys, const uint16_t* q, int klim, int k0, int k1, int D, float c,
                                        uint8_t* b0, uint8_t* b1, uint8_t* b2, uint8_t* b3, State<C>& st) {
-    if constexpr (Keys::CODES) {
-        if constexpr (C::SHARE) attend_code_stages<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
-        else attend_code_streams<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
-    } else {
-        if constexpr (C::SHARE) attend_stages<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
-        else attend_streams<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
-    }
+    if constexpr (Keys::CODES) attend_code_stages<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);   // tall tiles alone
+    else if constexpr (C::SHARE) attend_stages<C>(keys, q, klim, k0, k1, D, c, b0, b1, b2, b3, st);
+    else attend_streams<C>(keys, q, klim, k0, k1, D, c, b0, b1, st);
 }
 
 // ----------------------------------------------------------- shared prefix

@@ -142,7 +142,7 @@ struct SharedPlan {
     int64_t workgroups;  // of the call's largest launch
 };
 SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_cap,
-                            int64_t suffix_cap);
+                            int64_t suffix_cap, bool codes);
 hipError_t launch_attn_shared(SharedArgs a, const SharedPlan& p, void* ws, hipStream_t s);
 // The same over a cache in E4M3 codes (k_cache and v_cache point to bytes).
 hipError_t launch_attn_shared_e4m3(SharedArgs a, const SharedPlan& p, void* ws, hipStream_t s);
