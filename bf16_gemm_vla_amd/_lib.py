@@ -92,11 +92,15 @@ SIGNATURES = {
 
 _lock = threading.Lock()
 _lib = None
+_current = None                        # torch's raw stream and current device, once they are asked for
 
 
 def load() -> ctypes.CDLL:
     """Load libvla.so (built by ``python -m bf16_gemm_vla_amd.build``)."""
     global _lib
+    lib = _lib
+    if lib is not None:                # every call comes here: no lock once it is there
+        return lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -136,11 +140,16 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
-        import torch
+        global _current
+        if _current is None:
+            import torch
 
+            torch.cuda.current_device()            # sets the runtime up where nothing has yet
+            _current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         # the handle itself: building a torch.cuda.Stream around it takes
         # 2.6 us, more than a short call's own launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        raw_stream, device = _current
+        return raw_stream(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

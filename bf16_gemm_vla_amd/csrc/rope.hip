@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
     const int lo = (turned && !a.interleaved) ? u * VEC : 2 * VEC * u;
     const int hi = (turned && !a.interleaved) ? a.rot / 2 + u * VEC : 2 * VEC * u + VEC;
 
-    const int heads = a.Hq + 2 * a.Hkv;
+    const int heads = a.Hq + (a.v ? 2 : 1) * a.Hkv;
     const int first = chunk * a.steps * hpw, last = min(heads, first + a.steps * hpw);
     // q, k, v heads in one order: 0, 1, 2
     auto kind_of = [&](int h) { return h < a.Hq ? 0 : (h < a.Hq + a.Hkv ? 1 : 2); };
@@ -102,7 +102,6 @@ __global__ __launch_bounds__(kRThreads) void qk_norm_rope_append_kernel(RopeArgs
         const uint16_t* src = kind == 0 ? a.q + t * a.q_stride + static_cast<int64_t>(h) * a.D
                               : kind == 1 ? a.k + t * a.k_stride + static_cast<int64_t>(h - a.Hq) * a.D
                                           : a.v + t * a.v_stride + static_cast<int64_t>(h - a.Hq - a.Hkv) * a.D;
-        if (kind == 2 && !a.v) return;
         rx = *reinterpret_cast<const W*>(src + lo);
         ry = *reinterpret_cast<const W*>(src + hi);
     };
@@ -263,7 +262,7 @@ hipError_t launch_qk_norm_rope_append(RopeArgs a, hipStream_t s) {
     while ((1 << a.gw_log2) < units) ++a.gw_log2;
     a.gw = 1 << a.gw_log2;
     const int hpw = 64 >> a.gw_log2;
-    const int steps = (a.Hq + 2 * a.Hkv + hpw - 1) / hpw;    // wave steps of one token
+    const int steps = (a.Hq + (a.v ? 2 : 1) * a.Hkv + hpw - 1) / hpw;    // wave steps of one token
     // one wave per step while that fills the GPU's 1024 SIMDs some 8 times
     // over, then one wave per token, which computes its angles once (300
     // tokens of 8 heads on 1 of 256: 3.8 us, one wave per token 5.0; 16387
