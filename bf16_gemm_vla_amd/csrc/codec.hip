@@ -840,7 +840,8 @@ __global__ __launch_bounds__(kThreads) void quantize_tokens_int8_kernel(const ui
     }
 }
 
-// Rows longer than the registers of a workgroup hold: read twice.
+// Rows longer than the registers of a workgroup hold, and a few of more than 2048
+// channels: read twice.
 __global__ __launch_bounds__(1024) void quantize_long_tokens_int8_kernel(const uint16_t* __restrict__ A,
                                                                          int8_t* __restrict__ qa, float* __restrict__ s_a,
                                                                          int64_t K) {
@@ -881,20 +882,23 @@ __global__ __launch_bounds__(1024) void quantize_long_tokens_int8_kernel(const u
 
 }  // namespace
 
+// Rows of 1024 channels and less are a wave's, longer ones four waves', where
+// many run at once (8191 rows of 1024: 10.1 us, four waves 12.1; of 2048: 16.0,
+// one wave 16.4; of 4096: 25, 29.5); few rows take more waves, whose divisions
+// run side by side: four up to 2048 channels (50 rows of 1024: 3.4 us, one
+// wave 4.1; of 2048: 3.5, 4.6), then the 16 that read a row twice, from their L1
+// the second time (50 rows of 4096: 3.8, four waves 4.1; of 16384: 6.1, 7.0; but
+// 2048 rows of 16384: 32.2, four waves 28.7).
 hipError_t launch_quantize_tokens_int8(const uint16_t* A, int8_t* qa, float* s_a, int64_t M, int64_t K, hipStream_t s) {
-    if (K > 16384) {
-        quantize_long_tokens_int8_kernel<<<static_cast<unsigned>(M), 1024, 0, s>>>(A, qa, s_a, K);
-    } else if (K > 2048) {
-        const unsigned grid = static_cast<unsigned>(M);
-        if (K <= 4096) quantize_tokens_int8_kernel<4, 2><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
-        else if (K <= 8192) quantize_tokens_int8_kernel<4, 4><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
-        else quantize_tokens_int8_kernel<4, 8><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
-    } else {
-        const unsigned grid = static_cast<unsigned>((M + 3) / 4);
-        if (K <= 512) quantize_tokens_int8_kernel<1, 1><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
-        else if (K <= 1024) quantize_tokens_int8_kernel<1, 2><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
-        else quantize_tokens_int8_kernel<1, 4><<<grid, kThreads, 0, s>>>(A, qa, s_a, M, K);
-    }
+    const unsigned rows = static_cast<unsigned>(M), fours = static_cast<unsigned>((M + 3) / 4);
+    constexpr int64_t kSlots = 256 * 32;       // waves that run at once
+    if (K > 16384 || (K > 2048 && 16 * M <= kSlots)) quantize_long_tokens_int8_kernel<<<rows, 1024, 0, s>>>(A, qa, s_a, K);
+    else if (K > 8192) quantize_tokens_int8_kernel<4, 8><<<rows, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    else if (K > 4096) quantize_tokens_int8_kernel<4, 4><<<rows, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    else if (K > 2048) quantize_tokens_int8_kernel<4, 2><<<rows, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    else if (K > 1024 || (K > 512 && 4 * M <= kSlots)) quantize_tokens_int8_kernel<4, 1><<<rows, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    else if (K > 512) quantize_tokens_int8_kernel<1, 2><<<fours, kThreads, 0, s>>>(A, qa, s_a, M, K);
+    else quantize_tokens_int8_kernel<1, 1><<<fours, kThreads, 0, s>>>(A, qa, s_a, M, K);
     return hipGetLastError();
 }
 

@@ -50,6 +50,16 @@ def test_tokens_equal_the_division(M, K):
     run_tokens(bits(r.standard_normal((M, K)) * np.exp(2 * r.standard_normal((M, 1)))))
 
 
+@pytest.mark.parametrize("M,K", [(513, 2080), (512, 2080), (515, 4096), (520, 4128), (513, 8224), (513, 16384), (512, 16384), (2049, 544),
+                                 (2050, 1024), (2048, 1024), (4097, 2048), (9001, 32)])
+def test_tokens_many_rows(M, K):
+    """On either side of the numbers of rows from which fewer waves take a row; rows of zeros and with NaN among them."""
+    x = bits(rng(M + K).standard_normal((M, K)).astype(np.float32))
+    x[M // 2] = 0
+    x[M - 1, K - 1], x[3, 0] = 0x7FC0, 0xFF80
+    run_tokens(x)
+
+
 def test_tokens_ties_extremes_and_rows_that_are_not_finite():
     K = 96
     r = rng(1)
