@@ -787,7 +787,9 @@ __global__ __launch_bounds__(kThreads) void act_encode_kernel(const uint16_t* __
 // |row| / 127) (1 for zeros) and the integers nearest to fp32(A / s).  A row
 // that holds an infinity or NaN gets zeros and a NaN scale, which makes its
 // products NaN.  WPR waves share a row, which stays in registers between its
-// maximum and its codes: 8 CH values per lane.
+// maximum and its codes: 8 CH values per lane.  Bound by HBM where the rows are
+// many (8191 of 4096: 22.5 us captured with cold caches, 4.5 TB/s) and by one
+// row's way where they are few (50 of 1024: 3.4 us, an empty launch 2.8).
 template <int WPR, int CH>
 __global__ __launch_bounds__(kThreads) void quantize_tokens_int8_kernel(const uint16_t* __restrict__ A,
                                                                         int8_t* __restrict__ qa,

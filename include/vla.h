@@ -389,12 +389,15 @@ int vla_kv_append_e4m3(const uint16_t* k, const uint16_t* v, const int32_t* cu_r
                        int64_t k_stride, int64_t v_stride, void* stream);
 
 /* vla_attn_shared_prefix over the cache in eight bits: a key and a value are
- * their codes' values times their blocks' scales.  Arguments, masks, sums and
- * roundings are vla_attn_shared_prefix's, and so is the result over a bf16 cache of
- * those values (they are bf16 numbers, but for products past its range: codes of
- * 2^128 and more with their scale count as infinities, parts below 2^-133
- * round).  A NaN code, and any code under the scale byte 255, is NaN to the rows
- * that see it and has no part in others.
+ * their codes' values times their blocks' scales.  Arguments, masks and sums are
+ * vla_attn_shared_prefix's, and so are the roundings over a bf16 cache of those
+ * values, but where few rows share a key/value head: there a weight is rounded
+ * to bf16 together with its value's scale (the same relative error), relative to
+ * the scales met so far, and values whose scale is 2^100 below the largest of
+ * those may lose precision.  Keys of 2^128 and more with their scale count as
+ * infinities, values of that size as that or as what they are; parts below
+ * 2^-133 round.  A NaN code, and any code under the scale byte 255, is NaN to
+ * the rows that see it and has no part in others.
  *   k_cache, v_cache, k_scales, v_scales, block_size  as vla_kv_append_e4m3 leaves them;
  *   ws   device workspace of vla_attn_shared_prefix_e4m3_workspace_bytes, to
  *        which the same applies as above. */
