@@ -912,7 +912,7 @@ int check_shared(const char* fn, int64_t B, int64_t L, int64_t Hq, int64_t Hkv, 
                  bool codes, vla::SharedPlan& p) {
     if (B <= 0 || L <= 0) return fail(VLA_EINVAL, fn, "B=%lld L=%lld must be positive", (long long)B, (long long)L);
     if (int rc = check_heads(fn, Hq, Hkv, D)) return rc;
-    if (prefix_cap < 0 || suffix_cap < 0 || prefix_cap + suffix_cap == 0)
+    if (prefix_cap < 0 || suffix_cap < 0 || (prefix_cap == 0 && suffix_cap == 0))
         return fail(VLA_EINVAL, fn, "a prefix or a suffix must be there");
     if (B > (int64_t(1) << 20) || L > (int64_t(1) << 20) || B * L * Hq >= (int64_t(1) << 31) - 128 ||
         prefix_cap >= (int64_t(1) << 30) || suffix_cap >= (int64_t(1) << 30) ||
@@ -1071,6 +1071,7 @@ size_t vla_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int wfmt) {
     if (M <= 0 || N <= 0 || K <= 0) return 0;
     if (wfmt == VLA_WFMT_MXFP4)
         return vla::gemm_ws_bytes(vla::plan_gemm(M, N, K, vla::AType::BF16, vla::WType::FP4, vla::Epi::PLAIN), M, N);
+    if (wfmt == VLA_WFMT_INT8 && (M > (int64_t(1) << 24) || N > (int64_t(1) << 30) || K > vla::kMostInt8K)) return 0;
     if (wfmt == VLA_WFMT_INT8)
         return vla::gemm_ws_bytes(vla::plan_gemm(M, N, K, vla::AType::INT8, vla::WType::INT8, vla::Epi::PLAIN), M, N);
     const vla::WType wt = (wfmt == VLA_WFMT_BF16) ? vla::WType::BF16 : vla::WType::FP8;

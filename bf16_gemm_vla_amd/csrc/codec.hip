@@ -892,6 +892,11 @@ __global__ __launch_bounds__(1024) void quantize_long_tokens_int8_kernel(const u
 // the second time (50 rows of 4096: 3.8, four waves 4.1; of 16384: 6.1, 7.0; but
 // 2048 rows of 16384: 32.2, four waves 28.7).
 hipError_t launch_quantize_tokens_int8(const uint16_t* A, int8_t* qa, float* s_a, int64_t M, int64_t K, hipStream_t s) {
+    constexpr int64_t kMost = int64_t(1) << 20;    // rows of one launch: a grid holds fewer than 2^32 threads
+    for (; M > kMost; M -= kMost, A += kMost * K, qa += kMost * K, s_a += kMost) {
+        const hipError_t e = launch_quantize_tokens_int8(A, qa, s_a, kMost, K, s);
+        if (e != hipSuccess) return e;
+    }
     const unsigned rows = static_cast<unsigned>(M), fours = static_cast<unsigned>((M + 3) / 4);
     constexpr int64_t kSlots = 256 * 32;       // waves that run at once
     if (K > 16384 || (K > 2048 && 16 * M <= kSlots)) quantize_long_tokens_int8_kernel<<<rows, 1024, 0, s>>>(A, qa, s_a, K);

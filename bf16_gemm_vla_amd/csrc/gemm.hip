@@ -553,6 +553,11 @@ hipError_t launch_gemm(const GemmProblem& pr, hipStream_t s) {
 
 bool plan_dispatchable(const GemmPlan& p, AType at, WType wt, Epi epi) {
     if (!p.ok) return false;
+    // a grid holds fewer than 2^32 threads, and at most 65535 workgroups in y and
+    // z; 8-bit integers alone can ask for more, having no other bound on their tiles
+    if (at == AType::INT8 && (static_cast<int64_t>(p.groups) * p.mblocks * p.ksplit >= (int64_t(1) << 32) / (64 * p.waves) ||
+                              p.mblocks > 65535))
+        return false;
     if (p.kernel != 0) return wide_dispatchable(p, at, wt, epi);
 #define VLA_CASE(NT_, S_, W_, MT_) \
     if (p.nt == NT_ && p.steps == S_ && p.waves == W_ && p.mt == MT_) return !(epi == Epi::GELU_MUL && NT_ < 2);

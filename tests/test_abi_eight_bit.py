@@ -137,3 +137,65 @@ def test_attention_workspace_query():
     assert n(0, 1, 4, 2, 64, 16, 16) == 0 and n(1, 1, 4, 2, 64, 0, 0) == 0 and n(1, 1, 5, 2, 64, 16, 16) == 0
     assert n(1, 1, 32, 8, 128, 0, 131072) > 0
     assert n(1 << 20, 1 << 10, 2, 1, 8, 16, 16) == 0
+
+
+def test_product_grids_past_a_launch_are_refused():
+    supported = lambda M, N, K: vla.vla_gemm_supported(M, N, K, vla.VLA_WFMT_INT8)   # noqa: E731
+    assert supported(192 * 65535, 16, 32) == 0 and supported(192 * 65535 + 1, 16, 32) == ESHAPE      # blocks of rows
+    assert supported(1, 1 << 26, 32) == 0 and supported(1, 1 << 30, 32) == ESHAPE                    # threads
+    assert supported(1 << 23, 1 << 23, 32) == ESHAPE
+
+
+def test_extreme_sizes_are_planned_or_refused():
+    """Every size at both ends of its range and past it: a status code or a plan, never an overflow on the way."""
+    big = (1, 31, 1 << 20, (1 << 31) - 1, 1 << 31, 1 << 40, (1 << 62) + 16, (1 << 63) - 1, -1, -(1 << 63))
+    lib = vla.load()
+    for m in big:
+        for n in (16, (1 << 31) - 16, 1 << 40, (1 << 63) - 16):
+            for k in (32, 131040, 131072, 1 << 40, (1 << 63) - 32):
+                vla.vla_gemm_plan(m, n, k, vla.VLA_WFMT_INT8)
+                vla.vla_gemm_workspace_bytes(m, n, k, vla.VLA_WFMT_INT8)
+                vla.vla_packed_bytes(n, k, vla.VLA_WFMT_INT8)
+    for x in big:
+        for y in big:
+            for D in (8, 64, 200, 256):
+                vla.vla_attn_shared_prefix_e4m3_workspace_bytes(x, 1, 32, 8, D, 0, y)
+                vla.vla_attn_shared_prefix_e4m3_workspace_bytes(1, x, 8, 1, D, y, 16)
+                vla.vla_attn_shared_prefix_e4m3_workspace_bytes(4, x, y, 1, D, 4096, 4096)
+    for name, make, keys in (("vla_kv_append_e4m3", append_args, ("B", "L", "total", "Hkv", "D", "num_pages", "page_size", "block_size",
+                                                                  "pages_per_seq", "k_stride", "v_stride")),
+                             ("vla_attn_shared_prefix_e4m3", attention_args, ("B", "L", "Hq", "Hkv", "D", "num_pages", "page_size",
+                                                                              "block_size", "pages_per_seq", "q_stride", "out_stride")),
+                             ("vla_quantize_tokens_int8", tokens_args, ("M", "K")), ("vla_gemm_int8", product_args, ("M", "N", "K")),
+                             ("vla_qk_norm_rope_axes_append", axes_args, ("T", "Hq", "Hkv", "D", "rot", "axes", "num_slots"))):
+        for key in keys:
+            for x in (0, -1, -(1 << 63), 1 << 62, (1 << 63) - 1):
+                if name == "vla_qk_norm_rope_axes_append" and key == "rot" and x == 0:
+                    continue
+                assert getattr(lib, name)(*make(**{key: x}).values(), None) in (EINVAL, ESHAPE, EALIGN, EWS), (name, key, x)
+
+
+def test_refusals_under_asan_and_ubsan():
+    """The tests above against a build whose host code is instrumented."""
+    import glob
+    import os
+    import subprocess
+    import sys
+
+    from bf16_gemm_vla_amd import build as vla_build
+
+    runtime = sorted(glob.glob("/opt/rocm/llvm/lib/clang/*/lib/linux/libclang_rt.asan-x86_64.so"))
+    if not runtime:
+        pytest.skip("clang's AddressSanitizer runtime is not installed")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    lib = vla_build.build(sanitize=True)
+    runner = ("import sys; sys.path.insert(0, %r)\n"
+              "import bf16_gemm_vla_amd._lib as L; L.LIB_PATH = %r\n"
+              "import pytest; sys.exit(pytest.main(['-q', '-x', '-p', 'no:cacheprovider', '-k', 'not asan', "
+              "'tests/test_abi_eight_bit.py']))\n") % (root, lib)
+    env = dict(os.environ, LD_PRELOAD=runtime[-1], ASAN_OPTIONS="detect_leaks=0:abort_on_error=1:halt_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-c", runner], cwd=root, env=env, capture_output=True, text=True, timeout=900)
+    tail = (r.stdout + r.stderr)[-4000:]
+    assert r.returncode == 0, tail
+    assert "passed" in r.stdout and "ERROR: AddressSanitizer" not in tail and "runtime error" not in tail, tail

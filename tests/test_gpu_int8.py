@@ -331,3 +331,16 @@ def test_tokens_then_product():
     exact = bf16_f64(x[keep]) @ W.astype(np.float64).T
     bound = 0.5 * (np.abs(bf16_f64(x[keep])).sum(1)[:, None] * ws_ + host(s)[keep][:, None] * (np.abs(W).sum(1) + 0.5 * K * ws_))
     assert (np.abs(got[keep] - exact) <= bound + 2.0 ** -7 * np.abs(exact)).all()
+
+
+def test_tokens_past_one_launch():
+    """More rows than a launch takes, the first, the last and those on either side of the seam."""
+    M, K = (1 << 20) + 3, 32
+    x = bits(rng(77).standard_normal((64, K)))
+    rows = dev(x).repeat(M // 64 + 1, 1)[:M].contiguous()
+    q, s = torch.zeros(M, K, dtype=torch.int8, device="cuda"), torch.zeros(M, device="cuda")
+    vla.vla_quantize_tokens_int8(rows, q, s, M, K)
+    want_q, want_s = quantize_tokens(bf16_f64(x))
+    want_q, want_s = torch.from_numpy(want_q).cuda(), torch.from_numpy(want_s).cuda()
+    at = torch.arange(M, device="cuda") % 64
+    assert torch.equal(q, want_q[at]) and torch.equal(s, want_s[at])
