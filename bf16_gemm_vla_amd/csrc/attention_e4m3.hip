@@ -154,7 +154,9 @@ void attn_few_codes_kernel(SharedArgs a) {
     const int steps = (keys.n + C::ST - 1) / C::ST;
     int unused;
     const int per = (prefix ? a.by_prefix_splits : a.by_suffix_splits).divide(steps + splits - 1, unused);
-    const int k0 = min(split * per * C::ST, keys.n), k1 = min((split + 1) * per * C::ST, keys.n);
+    // steps first: the last part's end in keys could pass 32 bits
+    const int s0 = split * per, s1 = s0 + per;
+    const int k0 = s0 >= steps ? keys.n : s0 * C::ST, k1 = s1 >= steps ? keys.n : s1 * C::ST;
     const int first = k0 + wave * 32;
     const int n = k1 > first ? (k1 - first + 127) / 128 : 0;
 
