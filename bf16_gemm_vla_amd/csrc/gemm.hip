@@ -19,9 +19,11 @@
 // partials and counts its arrival; the last to arrive sums the partials in
 // split order (bitwise repeatable) and runs the epilogue.
 //
-// 8-bit integers take FP8's tilings, their codes having FP8's sizes: 50 rows,
-// 1024 -> 4096, 5.6 us as FP8 x FP8 5.7; weights of 4 MiB are 0.8 us of that,
-// an empty launch 2.8, the rest the way of one load and one sum.
+// 8-bit integers, whose activations go through LDS as bf16 ones do: 50 rows, 1024
+// -> 4096, 4.5 us, 4096 -> 1024 5.1 (with fragments from memory, as FP8 x FP8
+// has them, 5.5 and 7.9); weights of 4 MiB are 0.8 us of that, an empty launch
+// 2.8, the rest the way of one load and one sum.  10 rows, 2048 -> 16384 8.5 us
+// (4 TB/s).
 #include <algorithm>
 #include <mutex>
 
@@ -76,13 +78,14 @@ __device__ __forceinline__ int skinny_tile(int g, int j, int N) {
     }
 }
 
-// ALDS: stage the (row-major bf16) activation chunk through LDS with direct
-// global->LDS loads, one contiguous KiB per wave instruction, instead of
-// loading MFMA fragments (16 rows x 64 B per instruction) from global memory.
-template <int WAVES, int S, int MT>
+// ALDS: stage the (row-major bf16 or 8-bit integer) activation chunk through LDS
+// with direct global->LDS loads, one contiguous KiB per wave instruction, instead
+// of loading MFMA fragments (16 rows x 64 or 32 B per instruction) from global
+// memory.  AB: bytes per activation.
+template <int AB, int WAVES, int S, int MT>
 struct SkinnyLds {
     static constexpr int CH = WAVES * S;             // K steps per workgroup chunk
-    static constexpr int RB = CH * 64;               // bf16 bytes of one row's chunk
+    static constexpr int RB = CH * 32 * AB;          // bytes of one row's chunk
     static constexpr int RS = RB + 16;               // LDS row stride (bank spread)
     static constexpr int BYTES = MT * 16 * RS;       // the workgroup's rows
 };
@@ -101,7 +104,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     constexpr int PAIRS = JO * MT;                           // (output tile, m-tile) fragments
     constexpr int R = (PAIRS + WAVES - 1) / WAVES;           // fragments finished per wave
 
-    using L = SkinnyLds<WAVES, S, MT>;
+    using L = SkinnyLds<AB, WAVES, S, MT>;
     constexpr int RED_BYTES = WAVES * NT * MT * 64 * 16;
     // the reduction area follows the activation chunk when both fit, so the
     // partial sums need not wait for every wave to finish its LDS reads
@@ -150,9 +153,9 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
         for (int piece = wave; piece < mrows * PIECES; piece += WAVES) {
             const int row = piece / PIECES, p = piece % PIECES;    // row within the workgroup
             const int byte = p * 1024 + lane * 16;             // within the row chunk
-            const int kel = kel_row + byte / 2;
+            const int kel = kel_row + byte / AB;
             if (byte < L::RB && kel < a.K) {
-                const uint8_t* src = static_cast<const uint8_t*>(a.A) + (static_cast<int64_t>(m0 + row) * a.K + kel) * 2;
+                const uint8_t* src = static_cast<const uint8_t*>(a.A) + (static_cast<int64_t>(m0 + row) * a.K + kel) * AB;
                 __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void*)(lds + row * L::RS + p * 1024), 16, 0, 0);
             }
         }
@@ -236,7 +239,7 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
             for (int mt = 0; mt < MT; ++mt) {
                 const int row = mt * 16 + mrow;
                 if (ok && row < mrows)
-                    af[s][mt] = *reinterpret_cast<const AF*>(lds + row * L::RS + ((wave * S + s) * 32 + 8 * q) * 2);
+                    af[s][mt] = *reinterpret_cast<const AF*>(lds + row * L::RS + ((wave * S + s) * 32 + 8 * q) * AB);
                 else
                     af[s][mt] = AF{};
             }
@@ -362,7 +365,9 @@ hipError_t launch_skinny(const KArgs& ka, const GemmPlan& p, hipStream_t s) {
     if (p.nt == NT_ && p.steps == S_ && p.waves == W_ && p.mt == MT_) {                            \
         if constexpr (EPI == Epi::GELU_MUL && NT_ < 2) {                                           \
             return hipErrorInvalidValue;                                                           \
-        } else if constexpr (AT == AType::BF16 && SkinnyLds<W_, S_, MT_>::BYTES <= 160 * 1024) {   \
+        } else if constexpr (AT == AType::INT8) {                                                  \
+            skinny_gemm_kernel<AT, WT, EPI, NT_, S_, W_, true, MT_><<<grid, W_ * 64, 0, s>>>(ka);       \
+        } else if constexpr (AT == AType::BF16 && SkinnyLds<2, W_, S_, MT_>::BYTES <= 160 * 1024) { \
             if (p.alds) skinny_gemm_kernel<AT, WT, EPI, NT_, S_, W_, true, MT_><<<grid, W_ * 64, 0, s>>>(ka); \
             else skinny_gemm_kernel<AT, WT, EPI, NT_, S_, W_, false, MT_><<<grid, W_ * 64, 0, s>>>(ka);  \
         } else {                                                                                   \
@@ -409,7 +414,13 @@ GemmPlan skinny_plan(int64_t M, int64_t N, int64_t K, Epi epi, int nt, int steps
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi) {
     const int64_t ksteps = K / 32;
     const int64_t tiles = N / 16;
-    if (M <= 64) {
+    // 8-bit integers take the wide kernel below 65 rows where the weights are large,
+    // since it splits K among no more workgroups than fill the GPU (50 rows, 8192 ->
+    // 8192: 24.0 us, the skinny kernel 35.0; 16384 -> 2048 29.7, 35.2; 4096 ->
+    // 4096 16.2 at 65 rows, 13.1; 30 rows, 8192 -> 28672 60.6, 74.8; 8192 -> 8192
+    // 23.7, 20.9).
+    const bool wide = M > 64 || (at == AType::INT8 && M > 16 && N * K >= int64_t(1) << (M > 32 ? 25 : 27) && N * K < int64_t(1) << 31);
+    if (!wide) {
         // One 16-column tile (a gate/up pair for the fused epilogue) per
         // workgroup.  With at least ~256 such groups every workgroup takes
         // all rows and K chunks of at most 32 MFMA steps (1024 K).  With
@@ -421,17 +432,26 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
         // for what remains.  Tilings measured on MI355X at M = 50: FP8
         // weights 8 waves x 4 steps, BF16 weights 16 waves x 2 steps;
         // bf16 activations staged through LDS.
+        const bool alds = at != AType::FP8;
         const int nt = (epi == Epi::GELU_MUL) ? 2 : 1;
         const int64_t groups = std::max<int64_t>(1, (epi == Epi::GELU_MUL) ? tiles / 2 : tiles);
         const int64_t mt_total = (M + 15) / 16;
         const int64_t want = groups >= 256 ? 1 : (256 + groups - 1) / groups;   // splits wanted
         // MXFP4 weights take the FP8 tilings (fewer weight bytes per fragment)
+        // 8-bit integers, one 16-row tile and more than 1024 K: 16 waves, no K split
+        // up to 4096 K, two column tiles where those are enough workgroups or K
+        // is split all the same (10 rows, chunks of 8 waves x 4 steps beside it:
+        // 2048 -> 4096 4.3 us, 5.6; 4096 -> 4096 5.9, 8.0; 8192 -> 8192 15.7,
+        // 17.9; one column tile: 2048 -> 16384 9.3 us, two 8.4; 2048 -> 4096 4.3,
+        // 5.1).
+        if (at == AType::INT8 && mt_total == 1 && ksteps > 32)
+            return skinny_plan(M, N, K, epi, groups >= 512 || ksteps > 128 ? 2 : 1, ksteps > 64 && ksteps <= 128 ? 8 : 4, 16, 1, alds);
         // one 16-row tile and too few column groups, FP8 weights: no K split
         // up to 128 MFMA steps (K = 4096) — one 16-wave workgroup per tile
         // beats the cross-workgroup exchange (the 10-row 4096 -> 1024
         // down-projection: 6.30 -> 5.31 us against four K splits)
         if (want > 1 && mt_total == 1 && wt != WType::BF16 && epi == Epi::PLAIN && ksteps > 16 && ksteps <= 128)
-            return skinny_plan(M, N, K, epi, nt, ksteps <= 64 ? 4 : 8, 16, 1, at == AType::BF16);
+            return skinny_plan(M, N, K, epi, nt, ksteps <= 64 ? 4 : 8, 16, 1, alds);
         if (want > 1 && mt_total > 1) {
             const int64_t ksplit = (want + mt_total - 1) / mt_total;
             const int64_t chunk = (ksteps + ksplit - 1) / ksplit;               // K steps per workgroup
@@ -440,7 +460,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
             else if (chunk <= 32) { waves = 8; steps = 4; }
             else if (chunk <= 64) { waves = 16; steps = 4; }
             else { waves = 16; steps = 8; }
-            return skinny_plan(M, N, K, epi, nt, steps, waves, 1, at == AType::BF16);
+            return skinny_plan(M, N, K, epi, nt, steps, waves, 1, alds);
         }
         const int64_t chunk = (ksteps + want - 1) / want;   // K steps per workgroup
         int steps, waves;
@@ -451,6 +471,12 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
             waves = 8;
             steps = chunk <= 16 ? 2 : 4;
         }
+        // 8-bit integers, whose chunk of activations is half as large: a block of
+        // 16 or 32 rows takes LDS for no more rows than that, so that more
+        // workgroups fit a compute unit (10 rows, 2048 -> 16384: 10.7 us, with LDS
+        // for 64 rows 23.5; 17 rows 11.6, 24.9).
+        if (at == AType::INT8 && mt_total == 1) return skinny_plan(M, N, K, epi, nt, steps, waves, 1, alds);
+        if (at == AType::INT8 && mt_total == 2 && steps == 4) return skinny_plan(M, N, K, epi, 2 * nt, steps, waves, 2, alds);
         // FP8 weights, more than 32 rows: two 16-column tiles (two gate/up
         // pairs for the fused epilogue) x two row halves per workgroup read
         // 36% fewer bytes per CU than one tile (pair) x all rows (the
@@ -459,8 +485,8 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
         // number of gate tiles (a group never straddles the gate/up halves).
         if (mt_total > 2 && ((wt != WType::BF16 && steps == 4) || (wt == WType::BF16 && steps == 2)) &&
             (epi == Epi::PLAIN || (tiles / 2) % 2 == 0))
-            return skinny_plan(M, N, K, epi, 2 * nt, steps, waves, 2, at == AType::BF16);
-        return skinny_plan(M, N, K, epi, nt, steps, waves, 4, at == AType::BF16);
+            return skinny_plan(M, N, K, epi, 2 * nt, steps, waves, 2, alds);
+        return skinny_plan(M, N, K, epi, nt, steps, waves, 4, alds);
     }
     // Wide kernel: 192-row blocks; 256-column tiles when they give enough
     // workgroups, else 128-column tiles and K split until ~256 workgroups

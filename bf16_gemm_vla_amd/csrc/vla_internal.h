@@ -182,7 +182,7 @@ struct GemmProblem {
 
 // Launch plan chosen for a problem (host-side, deterministic per shape).
 struct GemmPlan {
-    int kernel;     // 0 = skinny (M <= 64), 1 = wide
+    int kernel;     // 0 = skinny (M <= 64), 1 = wide (above; 8-bit integers: also above 16 rows, large weights)
     int nt;         // skinny: 16-column tiles per workgroup; wide: tile width BN
     int steps;      // K steps (of 32) per wave per workgroup chunk (skinny)
     int waves;      // wavefronts per workgroup

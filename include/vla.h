@@ -484,7 +484,8 @@ int vla_gemm_supported(int64_t M, int64_t N, int64_t K, int wfmt, int fp8_act, i
 
 /* Host-only query, no device work: the launch plan a GEMM of this shape
  * takes (arguments as vla_gemm_supported).  Writes min(n_info, 10) values:
- *   [0] kernel (0 = skinny, M <= 64; 1 = wide)
+ *   [0] kernel (0 = skinny, M <= 64; 1 = wide, above and for 8-bit integers of
+ *       more than 16 rows with large weights)
  *   [1] skinny: 16-column weight tiles per workgroup; wide: tile width
  *   [2] [3] [4] grid x, y, z (skinny: column groups, K splits, row blocks;
  *               wide: column groups, 192-row blocks, K splits)

@@ -144,6 +144,9 @@ def test_product_grids_past_a_launch_are_refused():
     assert supported(192 * 65535, 16, 32) == 0 and supported(192 * 65535 + 1, 16, 32) == ESHAPE      # blocks of rows
     assert supported(1, 1 << 26, 32) == 0 and supported(1, 1 << 30, 32) == ESHAPE                    # threads
     assert supported(1 << 23, 1 << 23, 32) == ESHAPE
+    for M in (1, 16, 17, 32, 33, 64):                                                                # weights past 2 GiB
+        assert supported(M, 1 << 17, 1 << 14) == 0 and supported(M, (1 << 17) - 16, 1 << 14) == 0
+    assert supported(65, 1 << 17, 1 << 14) == ESHAPE
 
 
 def test_extreme_sizes_are_planned_or_refused():
