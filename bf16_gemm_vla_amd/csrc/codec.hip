@@ -110,6 +110,16 @@ __device__ __forceinline__ uint2 encode8_quotient(const float v[8], float sc, fl
     return make_uint2(o[0], o[1]);
 }
 
+// Scale of 8-bit integers whose largest magnitude is m: m / 127 with the
+// reciprocal rounded first (within one step of it), which is what array
+// libraries make of a division by a constant, so that their codes and these are
+// the same.
+__device__ __forceinline__ float scale_int8(float m) {
+    constexpr float kStep = 1.0f / 127.0f;
+    const float sc = __fmul_rn(m, kStep);
+    return sc == 0.0f ? 1.0f : sc;
+}
+
 // Eight integers nearest to fp32(v / sc), ties to even, within +-127.  v * rcp
 // is within 2 ulps of the quotient (below 2^-15 up to 128), and the integer
 // changes at halves only: away from them the product serves, next to one (and
@@ -166,8 +176,8 @@ __global__ __launch_bounds__(NT) void quantize_pack_kernel(const float* __restri
         }
         m = group_max<TPR>(m);
         if (c == 0) {
-            const float maxv = (WFMT == VLA_WFMT_INT8) ? 127.0f : (WFMT == VLA_WFMT_E4M3_FNUZ) ? 240.0f : 448.0f;
-            const float sc = (m == 0.0f) ? 1.0f : __fdiv_rn(m, maxv);
+            const float maxv = (WFMT == VLA_WFMT_E4M3_FNUZ) ? 240.0f : 448.0f;
+            const float sc = (WFMT == VLA_WFMT_INT8) ? scale_int8(m) : (m == 0.0f) ? 1.0f : __fdiv_rn(m, maxv);
             s_scale[r] = sc;
             scales[n0 * 16 + r] = sc;
         }
@@ -783,8 +793,8 @@ __global__ __launch_bounds__(kThreads) void act_encode_kernel(const uint16_t* __
     }
 }
 
-// 8-bit integers with one scale per token: row m of bf16 A gets s = fp32(max
-// |row| / 127) (1 for zeros) and the integers nearest to fp32(A / s).  A row
+// 8-bit integers with one scale per token: row m of bf16 A gets s =
+// scale_int8(max |row|) and the integers nearest to fp32(A / s).  A row
 // that holds an infinity or NaN gets zeros and a NaN scale, which makes its
 // products NaN.  WPR waves share a row, which stays in registers between its
 // maximum and its codes: 8 CH values per lane.  Bound by HBM where the rows are
@@ -824,7 +834,7 @@ __global__ __launch_bounds__(kThreads) void quantize_tokens_int8_kernel(const ui
     }
     if (!live) return;
     const bool fine = top < 0x7F800000u;
-    const float sc = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), 127.0f);
+    const float sc = scale_int8(__uint_as_float(top));
     const float rcp = __fdiv_rn(1.0f, sc);
     if (k0 == 0) s_a[m] = fine ? sc : __builtin_nanf("");
 #pragma unroll
@@ -865,7 +875,7 @@ __global__ __launch_bounds__(1024) void quantize_long_tokens_int8_kernel(const u
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, tops[i]);
     const bool fine = top < 0x7F800000u;
-    const float sc = top == 0 ? 1.0f : __fdiv_rn(__uint_as_float(top), 127.0f);
+    const float sc = scale_int8(__uint_as_float(top));
     const float rcp = __fdiv_rn(1.0f, sc);
     if (threadIdx.x == 0) s_a[m] = fine ? sc : __builtin_nanf("");
 #pragma unroll 2

@@ -103,8 +103,8 @@ size_t vla_packed_bytes(int64_t N, int64_t K, int wfmt);
  * FP8: scales[n] = fp32(max_k |W[n,k]| / 448) (OCP) or / 240 (FNUZ), 1 for an
  * all-zero row; code = encode(fp32(W[n,k] / scales[n])), IEEE division,
  * round to nearest even, saturating at +-max.  BF16: round to nearest even.
- * INT8: scales[n] = fp32(max_k |W[n,k]| / 127), 1 for an all-zero row; code =
- * the integer nearest to fp32(W[n,k] / scales[n]), ties to even; both layouts.
+ * INT8: scales[n] = fp32(max_k |W[n,k]| * fp32(1 / 127)), 1 where that is 0;
+ * code = the integer nearest to fp32(W[n,k] / scales[n]), ties to even; both layouts.
  * MXFP4 (OCP Microscaling Formats v1.0; 4-bit weights as in "FlashRT: an
  * inference engine for real-time robot control", section 7.2, here in the
  * MX form gfx950 converts in hardware): per block of 32 values of K in one
@@ -163,7 +163,7 @@ int vla_quantize_act_static(const uint16_t *A, const float *s_a, uint8_t *qa, in
                             void *stream);
 
 /* Tokens in 8-bit integers for vla_gemm_int8, a scale for each row of A: s_a[m]
- * = fp32(max_k |A[m,k]| / 127), 1 for an all-zero row; qa[m,k] = the integer
+ * = fp32(max_k |A[m,k]| * fp32(1 / 127)), 1 where that is 0; qa[m,k] = the integer
  * nearest to fp32(A[m,k] / s_a[m]), ties to even.  A row that holds an infinity
  * or NaN gets zeros and a NaN scale, so its products are NaN; other rows are
  * not touched by it.

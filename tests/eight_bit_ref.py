@@ -91,12 +91,12 @@ def append(x, cu, table, lens, cache, scales, page, block, longest):
 
 
 def quantize_tokens(x):
-    """(codes, scales) of the rows of x (values of bf16 numbers): scale = fp32(max |row| / 127), 1 for a row of zeros;
+    """(codes, scales) of the rows of x (values of bf16 numbers): scale = fp32(max |row| fp32(1 / 127)), 1 where that is 0;
     the integer nearest to fp32(x / scale), ties to even; a row with a value that is not finite: zeros, NaN."""
     x = np.asarray(x, np.float32)
     bad = ~np.isfinite(x).all(1)
     y = np.where(bad[:, None], np.float32(0), x)
-    s = np.abs(y).max(1) / np.float32(127)
+    s = np.abs(y).max(1) * (np.float32(1) / np.float32(127))
     s = np.where(s == 0, np.float32(1), s).astype(np.float32)
     q = np.clip(np.rint(y / s[:, None]), -127, 127).astype(np.int8)
     return q, np.where(bad, np.float32(np.nan), s).astype(np.float32)

@@ -354,3 +354,14 @@ def test_tokens_past_one_launch():
     want_q, want_s = torch.from_numpy(want_q).cuda(), torch.from_numpy(want_s).cuda()
     at = torch.arange(M, device="cuda") % 64
     assert torch.equal(q, want_q[at]) and torch.equal(s, want_s[at])
+
+
+@pytest.mark.parametrize("M,K", [(50, 1024), (700, 4096), (2100, 544)])
+def test_tokens_equal_an_array_programs(M, K):
+    """The codes and scales of the definition in array operations, bit for bit."""
+    x = torch.randn(M, K, device="cuda", generator=torch.Generator(device="cuda").manual_seed(M)).bfloat16()
+    q, s = torch.empty(M, K, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+    vla.vla_quantize_tokens_int8(x, q, s, M, K)
+    scale = x.float().abs().amax(1) / 127.0
+    assert torch.equal(s, scale)
+    assert torch.equal(q, torch.round(x.float() / scale[:, None]).to(torch.int8))
