@@ -18,9 +18,9 @@
 // registers between their maximum and their codes.
 //
 // Bound by HBM on prompts and by latency on single tokens.  Measured, captured
-// calls one behind another, 8 heads of 128, blocks of 16: 16 prompts of 9001
-// rows together 14.5 us, 3.8 TB/s of the 10.8 us that a copy's rate would take,
-// 2.8 of it an empty launch; 64 single tokens 4.7 us.
+// calls one behind another, 8 heads of 128: 16 prompts of 9001 rows together in
+// blocks of 32 14.6 us (3.8 TB/s; a copy's rate would take 10.8, an empty launch
+// takes 2.8), 64 single tokens in blocks of 16 4.9 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
