@@ -414,12 +414,13 @@ GemmPlan skinny_plan(int64_t M, int64_t N, int64_t K, Epi epi, int nt, int steps
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi) {
     const int64_t ksteps = K / 32;
     const int64_t tiles = N / 16;
-    // 8-bit integers take the wide kernel below 65 rows where the weights are large,
-    // since it splits K among no more workgroups than fill the GPU (50 rows, 8192 ->
-    // 8192: 24.0 us, the skinny kernel 35.0; 16384 -> 2048 29.7, 35.2; 4096 ->
-    // 4096 16.2 at 65 rows, 13.1; 30 rows, 8192 -> 28672 60.6, 74.8; 8192 -> 8192
-    // 23.7, 20.9).
-    const bool wide = M > 64 || (at == AType::INT8 && M > 16 && N * K >= int64_t(1) << (M > 32 ? 25 : 27) && N * K < int64_t(1) << 31);
+    // 8-bit integers take the wide kernel below 65 rows where the weights are large:
+    // there each is read once, by the skinny kernel once for every 16 or 32 rows
+    // (64 rows, 2^25 weights, 2048 -> 16384: 18.5 us, the skinny kernel 19.8, 48
+    // rows 18.6, 16.2; 33 rows, 2^26, 2048 -> 32768: 18.2, 31.6; 30 rows, 2^26,
+    // 8192 -> 8192: 23.7, 20.9; 2^27, 4096 -> 32768: 35.7, 50.5).
+    const int large = M > 48 ? 25 : M > 32 ? 26 : 27;
+    const bool wide = M > 64 || (at == AType::INT8 && M > 16 && N * K >= int64_t(1) << large && N * K < int64_t(1) << 31);
     if (!wide) {
         // One 16-column tile (a gate/up pair for the fused epilogue) per
         // workgroup.  With at least ~256 such groups every workgroup takes
@@ -438,14 +439,17 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, AType at, WType wt, Epi epi)
         const int64_t mt_total = (M + 15) / 16;
         const int64_t want = groups >= 256 ? 1 : (256 + groups - 1) / groups;   // splits wanted
         // MXFP4 weights take the FP8 tilings (fewer weight bytes per fragment)
-        // 8-bit integers, one 16-row tile and more than 1024 K: 16 waves, no K split
-        // up to 4096 K, two column tiles where those are enough workgroups or K
-        // is split all the same (10 rows, chunks of 8 waves x 4 steps beside it:
-        // 2048 -> 4096 4.3 us, 5.6; 4096 -> 4096 5.9, 8.0; 8192 -> 8192 15.7,
-        // 17.9; one column tile: 2048 -> 16384 9.3 us, two 8.4; 2048 -> 4096 4.3,
-        // 5.1).
-        if (at == AType::INT8 && mt_total == 1 && ksteps > 32)
-            return skinny_plan(M, N, K, epi, groups >= 512 || ksteps > 128 ? 2 : 1, ksteps > 64 && ksteps <= 128 ? 8 : 4, 16, 1, alds);
+        // 8-bit integers and more than 1024 K: 16 waves and one 16-row tile, no K
+        // split up to 4096 K; two column tiles where those are enough workgroups or
+        // K is split all the same (beside them 8 waves x 4 steps, for more than 16
+        // rows with the tilings below: 10 rows, 2048 -> 4096 4.3 us, 5.6; 4096 ->
+        // 4096 5.9, 8.0; 8192 -> 8192 15.7, 17.9; 30 rows, 2048 -> 4096 4.9, 6.6;
+        // 50 rows, 4096 -> 4096 11.1, 13.4; 2048 -> 8192 10.2, 12.3; 4096 -> 2048
+        // 6.4, 8.2.  Two column tiles against one: 10 rows, 2048 -> 16384 8.4, 9.3;
+        // 2048 -> 4096, where 128 workgroups are left, 5.1, 4.3).
+        const bool two = groups / 2 * mt_total >= 256;
+        if (at == AType::INT8 && ksteps > 32 && (mt_total == 1 || (two && ksteps <= 128)))
+            return skinny_plan(M, N, K, epi, two || ksteps > 128 ? 2 : 1, ksteps > 64 && ksteps <= 128 ? 8 : 4, 16, 1, alds);
         // one 16-row tile and too few column groups, FP8 weights: no K split
         // up to 128 MFMA steps (K = 4096) — one 16-wave workgroup per tile
         // beats the cross-workgroup exchange (the 10-row 4096 -> 1024

@@ -185,7 +185,8 @@ def test_product_matches_the_exact_sums(M, N, K):
 @pytest.mark.parametrize("M,N,K", [
     (10, 8208, 2080), (16, 16384, 2048), (1, 8192, 1056), (10, 8192, 4096), (9, 4112, 8192), (3, 1024, 16384), (16, 48, 8224),
     (16, 4096, 4096), (17, 4112, 4096), (32, 8208, 1056), (30, 4096, 1024), (33, 2064, 16416), (64, 16384, 2048), (40, 32768, 1024),
-    (20, 8192, 16384), (17, 131072, 1024), (50, 1048576, 32)])
+    (20, 8192, 16384), (17, 131072, 1024), (50, 1048576, 32),
+    (50, 2048, 4096), (33, 2064, 2080), (30, 4112, 2048), (17, 4096, 4096), (64, 8208, 1056), (30, 2048, 4096), (24, 4096, 8192)])
 def test_few_rows_of_every_tiling(M, N, K):
     """Tilings of few rows by rows, columns and K, partial column groups, and those that the wide kernel takes."""
     print(M, N, K, vla.vla_gemm_plan(M, N, K, vla.VLA_WFMT_INT8), flush=True)
