@@ -147,6 +147,9 @@ def test_product_grids_past_a_launch_are_refused():
     for M in (1, 16, 17, 32, 33, 64):                                                                # weights past 2 GiB
         assert supported(M, 1 << 17, 1 << 14) == 0 and supported(M, (1 << 17) - 16, 1 << 14) == 0
     assert supported(65, 1 << 17, 1 << 14) == ESHAPE
+    for M in (1, 10, 16, 17, 30, 33, 50, 64):
+        for K in (32, 1024, 1056, 4096, 4128, 8192, 8704):
+            assert supported(M, 245760, K) == 0, (M, K)
 
 
 def test_extreme_sizes_are_planned_or_refused():
