@@ -358,12 +358,18 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
     X(2, 2, 8, 1) X(2, 4, 8, 1) X(2, 4, 16, 1) X(2, 8, 16, 1)                                            \
     X(2, 4, 8, 2) X(4, 4, 8, 2) X(4, 4, 8, 1) X(8, 4, 8, 1) X(2, 2, 16, 2)
 
+// Of these, 8-bit integers get the ones that their plans name.
+constexpr bool int8_tiling(int nt, int steps, int waves, int mt) {
+    return mt == 1 ? nt == 1 || waves == 16 : mt == 2 ? nt == 2 && steps == 4 : nt == 1 && steps == 2 && waves == 8;
+}
+
 template <AType AT, WType WT, Epi EPI>
 hipError_t launch_skinny(const KArgs& ka, const GemmPlan& p, hipStream_t s) {
     const dim3 grid(p.groups, p.ksplit, p.mblocks);
 #define VLA_CASE(NT_, S_, W_, MT_)                                                                 \
     if (p.nt == NT_ && p.steps == S_ && p.waves == W_ && p.mt == MT_) {                            \
-        if constexpr (EPI == Epi::GELU_MUL && NT_ < 2) {                                           \
+        if constexpr ((EPI == Epi::GELU_MUL && NT_ < 2) ||                                         \
+                      (AT == AType::INT8 && !int8_tiling(NT_, S_, W_, MT_))) {                     \
             return hipErrorInvalidValue;                                                           \
         } else if constexpr (AT == AType::INT8) {                                                  \
             skinny_gemm_kernel<AT, WT, EPI, NT_, S_, W_, true, MT_><<<grid, W_ * 64, 0, s>>>(ka);       \
@@ -590,7 +596,8 @@ bool plan_dispatchable(const GemmPlan& p, AType at, WType wt, Epi epi) {
         return false;
     if (p.kernel != 0) return wide_dispatchable(p, at, wt, epi);
 #define VLA_CASE(NT_, S_, W_, MT_) \
-    if (p.nt == NT_ && p.steps == S_ && p.waves == W_ && p.mt == MT_) return !(epi == Epi::GELU_MUL && NT_ < 2);
+    if (p.nt == NT_ && p.steps == S_ && p.waves == W_ && p.mt == MT_)                              \
+        return !(epi == Epi::GELU_MUL && NT_ < 2) && (at != AType::INT8 || int8_tiling(NT_, S_, W_, MT_));
     VLA_SKINNY_CONFIGS(VLA_CASE)
 #undef VLA_CASE
     return false;
