@@ -19,6 +19,6 @@ from ._lib import (  # noqa: F401
     VLA_MFMA_BF16_32X32X16, VLA_MFMA_BF16_16X16X32, VLA_MFMA_FP8_32X32X64, VLA_MFMA_FP8_16X16X128,
     VLA_ROPE_HALF, VLA_ROPE_INTERLEAVED, vla_kv_append_e4m3, vla_attn_shared_prefix_e4m3,
     vla_attn_shared_prefix_e4m3_workspace_bytes, vla_attn_prompt, vla_attn_shared_prefix,
-    vla_attn_shared_prefix_workspace_bytes, vla_qk_norm_rope_append, vla_qk_norm_rope_axes_append,
+    vla_attn_shared_prefix_workspace_bytes, vla_attn_shared_prefix_plan, vla_qk_norm_rope_append, vla_qk_norm_rope_axes_append,
     vla_quantize_act_static, vla_quantize_tokens_int8, vla_quantize_act_workspace_bytes, vla_quantize_pack, vla_reencode_fnuz_to_ocp,
 )

@@ -63,6 +63,7 @@ SIGNATURES = {
     "vla_kv_append_e4m3": (INT, [P] * 9 + [I64] * 11 + [P]),
     "vla_attn_shared_prefix_e4m3_workspace_bytes": (SZ, [I64] * 7),
     "vla_attn_shared_prefix_e4m3": (INT, [P] * 11 + [SZ] + [I64] * 12 + [INT, ctypes.c_float, P]),
+    "vla_attn_shared_prefix_plan": (INT, [I64] * 7 + [INT, P, INT]),
     "vla_probe_stream_read": (INT, [P, SZ, P, INT, P]),
     "vla_probe_mfma_rate": (INT, [INT, P, INT, P, P, INT, P]),
     "vla_gate_residual_ada_norm": (INT, [P, P, P, P, INT, ctypes.c_float, P, P, P, I64, I64, P]),
@@ -291,6 +292,13 @@ def vla_kv_append_e4m3(k, v, cu_rows, block_table, seq_lens, k_cache, v_cache, k
 
 def vla_attn_shared_prefix_e4m3_workspace_bytes(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity) -> int:
     return load().vla_attn_shared_prefix_e4m3_workspace_bytes(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity)
+
+
+def vla_attn_shared_prefix_plan(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, e4m3=False):
+    """(status, info) with info the 6 plan values of include/vla.h; host only."""
+    info = (ctypes.c_int64 * 6)()
+    rc = load().vla_attn_shared_prefix_plan(B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, int(bool(e4m3)), info, 6)
+    return rc, list(info)
 
 
 def vla_attn_shared_prefix_e4m3(q, k_cache, v_cache, k_scales, v_scales, prefix_pages, prefix_len, block_table, seq_lens, out,

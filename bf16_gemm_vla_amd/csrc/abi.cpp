@@ -1043,6 +1043,19 @@ int vla_attn_shared_prefix_e4m3(const uint16_t* q, const uint8_t* k_cache, const
                          n_prefix_pages, pages_per_seq, q_stride, out_stride, causal, scale, stream);
 }
 
+int vla_attn_shared_prefix_plan(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_capacity,
+                                int64_t suffix_capacity, int e4m3, int64_t* info, int n_info) {
+    const char* fn = "vla_attn_shared_prefix_plan";
+    if (n_info < 0 || (n_info > 0 && !info)) return fail(VLA_EINVAL, fn, "info is NULL or n_info < 0");
+    if (e4m3 != 0 && e4m3 != 1) return fail(VLA_EINVAL, fn, "e4m3=%d must be 0 or 1", e4m3);
+    vla::SharedPlan p;
+    if (int rc = check_shared(fn, B, L, Hq, Hkv, D, prefix_capacity, suffix_capacity, e4m3 != 0, p)) return rc;
+    const int64_t v[6] = {p.prefix_splits ? p.prefix_tm : 0, p.suffix_splits ? p.suffix_tm : 0, p.prefix_splits, p.suffix_splits,
+                          p.merged, p.ws_bytes};
+    for (int i = 0; i < n_info && i < 6; ++i) info[i] = v[i];
+    return VLA_OK;
+}
+
 int vla_probe_stream_read(const void* src, size_t bytes, uint32_t* sink, int blocks, void* stream) {
     const char* fn = "vla_probe_stream_read";
     REQUIRE_PTR(src);

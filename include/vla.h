@@ -411,6 +411,17 @@ int vla_attn_shared_prefix_e4m3(const uint16_t* q, const uint8_t* k_cache, const
                                 int64_t n_prefix_pages, int64_t pages_per_seq, int64_t q_stride, int64_t out_stride,
                                 int causal, float scale, void* stream);
 
+/* Host-only query, no device work: how a call of these sizes over the bf16 cache
+ * (e4m3 0) or the cache in eight bits (1) is cut up.  Writes min(n_info, 6) values:
+ *   [0] query rows per tile against the shared prefix (0: none of its own)
+ *   [1] query rows per tile against a sequence's keys (0: none)
+ *   [2] [3] parts that the prefix's and a sequence's keys are split into
+ *   [4] 1 where the prefix is read with each sequence's own keys
+ *   [5] workspace bytes
+ * Returns VLA_OK or the status with which the call refuses these sizes. */
+int vla_attn_shared_prefix_plan(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64_t D, int64_t prefix_capacity,
+                                int64_t suffix_capacity, int e4m3, int64_t *info, int n_info);
+
 /* ----------------------------------------------------------- measurement */
 
 /* Streaming-read probe: one launch of `blocks` workgroups of 256 threads
