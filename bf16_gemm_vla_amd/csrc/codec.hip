@@ -169,15 +169,20 @@ __global__ __launch_bounds__(NT) void quantize_pack_kernel(const float* __restri
         const int r = t / TPR, c = t % TPR;
         const float* row = tile + static_cast<int64_t>(r) * K;
         float m = 0.0f;
+        bool nan = false;                        // fmaxf drops them; integers hold none, their scale has to
 #pragma unroll 4
         for (int64_t k = 4 * c; k < K; k += 4 * TPR) {
             float4 v = *reinterpret_cast<const float4*>(row + k);
             m = fmaxf(m, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+            if (WFMT == VLA_WFMT_INT8) nan |= v.x != v.x || v.y != v.y || v.z != v.z || v.w != v.w;
         }
+        if (WFMT == VLA_WFMT_INT8 && nan) m = __builtin_inff();
         m = group_max<TPR>(m);
         if (c == 0) {
             const float maxv = (WFMT == VLA_WFMT_E4M3_FNUZ) ? 240.0f : 448.0f;
-            const float sc = (WFMT == VLA_WFMT_INT8) ? scale_int8(m) : (m == 0.0f) ? 1.0f : __fdiv_rn(m, maxv);
+            const float sc = (WFMT == VLA_WFMT_INT8) ? (m < __builtin_inff() ? scale_int8(m) : __builtin_nanf(""))
+                             : (m == 0.0f)           ? 1.0f
+                                                     : __fdiv_rn(m, maxv);
             s_scale[r] = sc;
             scales[n0 * 16 + r] = sc;
         }
@@ -204,7 +209,8 @@ __global__ __launch_bounds__(NT) void quantize_pack_kernel(const float* __restri
             *reinterpret_cast<uint4*>(static_cast<uint16_t*>(Wq) + off) =
                 make_uint4(w[0], w[1], w[2], w[3]);
         } else if (WFMT == VLA_WFMT_INT8) {
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Wq) + off) = encode8_int8(v, sc, rcp);
+            // a row that is not finite: zeros
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Wq) + off) = sc == sc ? encode8_int8(v, sc, rcp) : make_uint2(0, 0);
         } else {
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(Wq) + off) =
                 encode8_quotient<WFMT == VLA_WFMT_E4M3_FNUZ>(v, sc, rcp);

@@ -105,6 +105,8 @@ size_t vla_packed_bytes(int64_t N, int64_t K, int wfmt);
  * round to nearest even, saturating at +-max.  BF16: round to nearest even.
  * INT8: scales[n] = fp32(max_k |W[n,k]| * fp32(1 / 127)), 1 where that is 0;
  * code = the integer nearest to fp32(W[n,k] / scales[n]), ties to even; both layouts.
+ * A row that holds an infinity or NaN gets zeros and a NaN scale, so its channel
+ * of the product is NaN.
  * MXFP4 (OCP Microscaling Formats v1.0; 4-bit weights as in "FlashRT: an
  * inference engine for real-time robot control", section 7.2, here in the
  * MX form gfx950 converts in hardware): per block of 32 values of K in one
