@@ -1262,6 +1262,13 @@ int vla_gemm_int8(const int8_t* A, const float* s_a, const int8_t* Wq, const flo
                            flat(bias, static_cast<size_t>(N) * 2), flat(residual == Y ? nullptr : residual, mn)};
     for (int j = 0; j < 6; ++j)
         if (regions_overlap(out, ins[j])) return fail(VLA_EINVAL, fn, "Y overlaps input %d", j);
+    const vla::GemmPlan plan = vla::plan_gemm(M, N, K, p.atype, p.wtype, p.epi);
+    if (vla::plan_dispatchable(plan, p.atype, p.wtype, p.epi)) {          // else run_gemm refuses the sizes
+        const Region work = flat(ws, vla::gemm_ws_bytes(plan, M, N));
+        if (regions_overlap(work, out)) return fail(VLA_EINVAL, fn, "Y overlaps ws");
+        for (int j = 0; j < 6; ++j)
+            if (regions_overlap(work, ins[j])) return fail(VLA_EINVAL, fn, "ws overlaps input %d", j);
+    }
     return run_gemm(fn, p, ws_bytes, static_cast<hipStream_t>(stream));
 }
 

@@ -590,7 +590,8 @@ int vla_gemm_fp8w_gelu_mul(const uint16_t *A, const uint8_t *Wgu, const float *s
  *   bias     device bf16[N] or NULL;  residual device bf16 M x N or NULL, may
  *            be Y;  Y device bf16 M x N, overlaps nothing else (VLA_EINVAL);
  *   ws       zero-filled workspace of vla_gemm_workspace_bytes(M, N, K,
- *            VLA_WFMT_INT8), as for vla_gemm_fp8w.
+ *            VLA_WFMT_INT8), as for vla_gemm_fp8w; those bytes overlap no tensor
+ *            of the call (VLA_EINVAL).
  * N % 16 == 0, K % 32 == 0, K at most 131040, where no codes' sum leaves 32
  * bits; M * K and N * K below 2^31 above 64 rows, M at most 12582720, no more
  * tiles than a launch and the split-K counters hold (N up to 245760 always;

@@ -1,7 +1,35 @@
 """Limits of the eight-bit layer's operators that their documentation states,
 before any device work.  Addresses are fake and never dereferenced."""
+import pytest
+
 import bf16_gemm_vla_amd as vla
-from tests.test_abi_eight_bit import EINVAL, ESHAPE
+from tests.test_abi_eight_bit import A, EINVAL, ESHAPE, GB, product_args, refused
+
+INT8 = vla.VLA_WFMT_INT8
+
+
+# ------------------------------------------------ workspace of the product
+
+@pytest.mark.parametrize("M,N,K", [(50, 64, 128), (50, 1024, 4096), (768, 2048, 16384), (8191, 1024, 1024)])
+def test_product_refuses_a_workspace_that_overlaps(M, N, K):
+    """Counters that a later call needs at zero, partial sums that other workgroups still read."""
+    need = vla.vla_gemm_workspace_bytes(M, N, K, INT8)
+    ws = A + 7 * GB
+    for at in (ws, ws + 16, ws + 61440, ws + (need - 1) // 16 * 16):
+        refused("vla_gemm_int8", product_args(M=M, N=N, K=K, residual=None, Y=at), EINVAL, "Y overlaps ws")
+        for name in ("A", "s_a", "Wq", "s_w", "bias", "residual"):
+            refused("vla_gemm_int8", product_args(M=M, N=N, K=K, **{name: at}), EINVAL, "ws overlaps input")
+    # the workspace's end inside Y, and a residual that is Y
+    refused("vla_gemm_int8", product_args(M=M, N=N, K=K, residual=None, Y=ws - 16), EINVAL, "Y overlaps ws")
+    refused("vla_gemm_int8", product_args(M=M, N=N, K=K, residual=ws, Y=ws), EINVAL, "overlaps")
+
+
+def test_product_counts_the_bytes_it_uses():
+    """What lies behind the bytes that a shape needs is another tensor's, however large the workspace is said to be."""
+    need = vla.vla_gemm_workspace_bytes(50, 64, 128, INT8)
+    assert need % 16 == 0
+    args = product_args(residual=None, Y=A + 7 * GB + need, ws_bytes=need - 1)
+    refused("vla_gemm_int8", args, vla.VLA_EWORKSPACE)               # no overlap is seen, the size is
 
 
 # ------------------------------------------------------------- the planner
