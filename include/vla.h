@@ -593,9 +593,10 @@ int vla_gemm_fp8w_gelu_mul(const uint16_t *A, const uint8_t *Wgu, const float *s
  *            VLA_WFMT_INT8), as for vla_gemm_fp8w; those bytes overlap no tensor
  *            of the call (VLA_EINVAL).
  * N % 16 == 0, K % 32 == 0, K at most 131040, where no codes' sum leaves 32
- * bits; M * K and N * K below 2^31 above 64 rows, M at most 12582720, no more
- * tiles than a launch and the split-K counters hold (N up to 245760 always;
- * vla_gemm_supported tells; VLA_ESHAPE). */
+ * bits; M * K and N * K below 2^31 above 64 rows, M at most 12582720; no more
+ * tiles than a launch and the split-K counters hold, and split-K partials below
+ * 4 GiB: N up to 32768 always fits (vla_gemm_supported tells for more;
+ * VLA_ESHAPE). */
 int vla_gemm_int8(const int8_t *A, const float *s_a, const int8_t *Wq, const float *s_w,
                   const uint16_t *bias, const uint16_t *residual, uint16_t *Y, void *ws,
                   size_t ws_bytes, int64_t M, int64_t N, int64_t K, void *stream);

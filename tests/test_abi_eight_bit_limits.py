@@ -8,6 +8,10 @@ from tests.test_abi_eight_bit import A, EINVAL, ESHAPE, GB, product_args, refuse
 INT8 = vla.VLA_WFMT_INT8
 
 
+def supported(M, N, K):
+    return vla.vla_gemm_supported(M, N, K, INT8)
+
+
 # ------------------------------------------------ workspace of the product
 
 @pytest.mark.parametrize("M,N,K", [(50, 64, 128), (50, 1024, 4096), (768, 2048, 16384), (8191, 1024, 1024)])
@@ -30,6 +34,27 @@ def test_product_counts_the_bytes_it_uses():
     assert need % 16 == 0
     args = product_args(residual=None, Y=A + 7 * GB + need, ws_bytes=need - 1)
     refused("vla_gemm_int8", args, vla.VLA_EWORKSPACE)               # no overlap is seen, the size is
+
+
+# --------------------------------------------------------- channels that fit
+
+def test_channels_that_always_fit():
+    """N up to 32768 with every number of rows and every K that the product takes."""
+    rows = [1, 2, 5, 10, 15, 16, 17, 31, 32, 33, 47, 48, 49, 50, 63, 64, 65, 128, 191, 192, 193, 384, 385, 768, 1000, 8191, 65536, 1 << 20,
+            (1 << 23) + 1, 12582720]
+    depths = [32, 64, 160, 512, 544, 1024, 1056, 2048, 2080, 4096, 4128, 8192, 8704, 16384, 32768, 65536, 65568, 98304, 131008, 131040]
+    for N in (16, 1024, 16384, 16400, 32752, 32768):
+        for M in rows:
+            for K in depths:
+                fits = M <= 64 or (M * K < 1 << 31 and N * K < 1 << 31)
+                assert supported(M, N, K) == (0 if fits else ESHAPE), (M, N, K)
+
+
+def test_more_channels_fit_where_the_documentation_says():
+    for M, N, K, code in ((50, 245760, 131040, ESHAPE), (2000000, 245760, 32, ESHAPE), (12582720, 245760, 32, ESHAPE),
+                          (12582720, 32784, 32, ESHAPE), (12582720, 32768, 32, 0), (64, 245760, 65536, 0), (64, 32768, 131040, 0),
+                          (8191, 245760, 8704, 0)):
+        assert supported(M, N, K) == code, (M, N, K)
 
 
 # ------------------------------------------------------------- the planner
