@@ -96,6 +96,15 @@ _lib = None
 _current = None                        # torch's raw stream and current device, once they are asked for
 
 
+def _forget_current():
+    global _current
+    _current = None
+
+
+# the GPU's runtime does not outlive a fork: torch is asked again in the child, and refuses
+os.register_at_fork(after_in_child=_forget_current)
+
+
 def load() -> ctypes.CDLL:
     """Load libvla.so (built by ``python -m bf16_gemm_vla_amd.build``)."""
     global _lib

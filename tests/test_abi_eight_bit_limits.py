@@ -1,5 +1,9 @@
 """Limits of the eight-bit layer's operators that their documentation states,
 before any device work.  Addresses are fake and never dereferenced."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 import bf16_gemm_vla_amd as vla
@@ -77,3 +81,28 @@ def test_attention_plan_query():
     assert lib.vla_attn_shared_prefix_plan(1, 1, 4, 2, 64, 16, 16, 1, None, -1) == EINVAL
     assert lib.vla_attn_shared_prefix_plan(1, 1, 4, 2, 64, 16, 16, 1, None, 0) == 0
     assert "vla_attn_shared_prefix_plan" in vla.last_error()
+
+
+# -------------------------------------------------------- a forked process
+
+def test_a_forked_process_asks_torch_again():
+    """The GPU's runtime does not outlive a fork: torch refuses its first call in the child, and so does a call that takes
+    the stream from torch, whatever the parent had looked up."""
+    script = ("import os, sys\n"
+              "import bf16_gemm_vla_amd._lib as L\n"
+              "L._current = (lambda device: 7), (lambda: 0)\n"
+              "assert L._stream(None) == 7\n"
+              "pid = os.fork()\n"
+              "if pid == 0:\n"
+              "    import torch\n"
+              "    def refuse(): raise RuntimeError('forked')\n"
+              "    torch.cuda.current_device = refuse\n"
+              "    try:\n"
+              "        L._stream(None)\n"
+              "    except RuntimeError as e:\n"
+              "        os._exit(0 if 'forked' in str(e) else 2)\n"
+              "    os._exit(1)\n"
+              "sys.exit(os.waitstatus_to_exitcode(os.waitpid(pid, 0)[1]) or (L._stream(None) != 7))\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", script], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
