@@ -281,11 +281,15 @@ void attn_few_codes_kernel(SharedArgs a) {
         float f[2], ks[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            f[h] = e[h] == 255 ? __builtin_nanf("") : __uint_as_float(static_cast<uint32_t>(max(e[h] - ref + 127, 0)) << 23);
+            f[h] = e[h] == 255 ? 0.0f : __uint_as_float(static_cast<uint32_t>(max(e[h] - ref + 127, 0)) << 23);
             // 0 where there is no slot, so that the zeros loaded there stay zeros
             ks[h] = __uint_as_float(PagedCodes<WIDE>::scale_bits(st.bytes[h].k) << 16 & ~(st.slot[h] >> 31));
         }
         if (g < 2) v_factor[wave][lane] = g ? f[1] : f[0];
+        // values whose scale is NaN: they count as 0 in the weights, so that unseen
+        // ones stay out, and reach the rows that see them after the product's weights
+        const uint32_t nan_scales = static_cast<uint32_t>(__ballot(e[0] == 255) & 0xFFFFu) |
+                                    static_cast<uint32_t>(__ballot(e[1] == 255) & 0xFFFFu) << 16;
         bool bad = false;                          // a NaN code that some row may not see
         if (key0 + 32 > kfull) {
             uint32_t any = 0;
@@ -368,10 +372,9 @@ void attn_few_codes_kernel(SharedArgs a) {
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float x = s[r][h][i], w = __builtin_amdgcn_exp2f(x - m0);
+                    const float w = __builtin_amdgcn_exp2f(s[r][h][i] - m0);
                     sum[h] = i ? sum[h] + w : w;
-                    // an unseen key's scale may be NaN
-                    p[4 * h + i] = x == -__builtin_inff() ? 0.0f : w * (h ? vf1[i] : vf0[i]);
+                    p[4 * h + i] = w * (h ? vf1[i] : vf0[i]);
                 }
             l[r] += sum[0] + sum[1];
             pw[r] = u32x4_t{f32x2_to_bf16x2(p[0], p[1]), f32x2_to_bf16x2(p[2], p[3]), f32x2_to_bf16x2(p[4], p[5]), f32x2_to_bf16x2(p[6], p[7])};
@@ -399,6 +402,16 @@ void attn_few_codes_kernel(SharedArgs a) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x) w[x] &= ~((nan_codes(w[x]) >> 7) * 0xFFu);
                 *at = w;
+            }
+        }
+        if (nan_scales != 0) {
+            // every channel of the rows that see the first of them, also where its
+            // weight is 0 (a score of -inf)
+#pragma unroll
+            for (int r = 0; r < C::NR; ++r) {
+                const float sees = key0 + __builtin_ctz(nan_scales) < klim[r] ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+                for (int d = 0; d < C::ND; ++d) acc[r][d] += sees;
             }
         }
         __builtin_amdgcn_sched_barrier(0);

@@ -135,6 +135,38 @@ def test_nan_reaches_the_rows_that_see_it(B, L, hq, hkv, D, rows, what):
 
 
 @pytest.mark.parametrize("B,L,hq,hkv,D,rows", FORMS)
+def test_nan_value_of_a_key_whose_score_is_minus_infinity(B, L, hq, hkv, D, rows):
+    """The weight is 0, and 0 times NaN is NaN; with a finite value there the row is as without the key."""
+    lens = [L + b % 23 for b in range(B)]
+    q = rand(3900, B * L, hq, D, scale=2.0)
+    q[:, :, 0] = 0x7F7F                                       # bf16's largest: times -2 the score leaves fp32
+    for nan in (None, "code", "scale"):
+        c = Cache(B, hkv, D, 16, 1, 0, lens, 3901)
+        planned(c, B, L, hq, 0, rows)
+        c.codes[0][:, :, 0] = 0
+        for b in range(B):
+            slot = c.keys[b][0]                               # every row sees it
+            c.codes[0][slot, :, 0] = 0xC0                     # -2
+            c.bytes[0][slot] = 127
+            if nan == "code":
+                c.codes[1][slot] = 0x7F
+            elif nan == "scale":
+                c.bytes[1][slot] = 255
+        got = c.call(q, 0, lens, L, hq, True, 1.0)
+        for b in range(B):
+            g, lim = bf16_f64(got[b]), limits(L, 0, lens[b], True)
+            sees_more = lim > 1                               # a row whose only score is -inf gives 0, whatever the value
+            if nan:
+                assert np.isnan(g[sees_more]).all(), (b, nan)
+            else:
+                k, v = c.values(0, c.keys[b][1:]), c.values(1, c.keys[b][1:])
+                ref, tol = attention_bound(q.reshape(B, L, hq, D)[b][sees_more], k, v, lim[sees_more] - 1, 1.0)
+                # scores differ by hundreds here: exponentials below 2^-126 are 0 beside the largest one's, which is at least 1
+                tol += 2.0 ** -126 * np.repeat(np.abs(bf16_f64(v)).sum(0), hq // hkv, 0)
+                assert (np.abs(g[sees_more] - ref) <= tol).all(), b
+
+
+@pytest.mark.parametrize("B,L,hq,hkv,D,rows", FORMS)
 def test_pages_that_are_not_there(B, L, hq, hkv, D, rows):
     lens = [L + 20 + b % 23 for b in range(B)]
     c = Cache(B, hkv, D, 16, 16, 0, lens, 3950)
