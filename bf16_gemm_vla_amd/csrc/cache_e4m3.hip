@@ -233,7 +233,8 @@ AppendPlan plan_kv_append(int64_t B, int64_t L, int64_t total, int64_t Hkv, int6
     AppendPlan p{};
     // L rows in a line touch at most this many blocks
     p.most = (L + block - 2) / block + 1;
-    // all rows together: a sequence's rows fill blocks but for two
+    // all rows together: a sequence's rows fill blocks but for two (and rows are
+    // one sequence's each: offsets that fall could ask for more)
     const int64_t packed = total / block + 2 * B < total ? total / block + 2 * B : total;
     p.dense = B * p.most <= packed;
     p.items = (p.dense ? B * p.most : packed) * Hkv * 2;

@@ -372,8 +372,9 @@ int vla_attn_shared_prefix(const uint16_t *q, const uint16_t *k_cache, const uin
  * one keep their codes (and mean nothing).
  *   k, v         device bf16, `total` rows of Hkv heads (vla_qk_norm_rope_append's
  *                k_out and the QKV GEMM's rows), rows *_stride elements apart;
- *   cu_rows      device int32[B + 1], rows cu_rows[b] .. cu_rows[b+1]-1 are
- *                sequence b's (bounded to 0 .. total; the first L count), or
+ *   cu_rows      device int32[B + 1], non-decreasing: rows cu_rows[b] ..
+ *                cu_rows[b+1]-1 are sequence b's (bounded to 0 .. total; the
+ *                first L count; where offsets fall, blocks may be left out), or
  *                NULL: L rows each, and total == B * L (VLA_ESHAPE);
  *   seq_lens     device int32[B], n_b with the new rows, bounded to 0 ..
  *                pages_per_seq * page_size; new rows that would lie before row 0

@@ -108,3 +108,28 @@ def test_append_behind_any_scale_byte(block, D):
         k, v = rows(5301 + n, 6, 1, D)
         c.append(k, v, None, table, [n] * 6, 1)
         assert (max(h[first].max() for h in c.host[1::2]) == 254) == (n > 1)
+
+
+def test_append_offsets_that_fall_leave_rows_out_at_most():
+    """Offsets are to rise; where they do not, so that sequences share rows, a block is appended as the definition has it or
+    not at all."""
+    B, n, page, block, hkv, D = 12, 300, 16, 16, 2, 64
+    each = n // page + 1
+    c = AppendCache(B * each, page, block, hkv, D, 5400)
+    table = np.arange(B * each).reshape(B, each)
+    k, v = rows(5401, n, hkv, D)
+    cu, lens = np.array([0, n] * (B // 2) + [0]), np.full(B, n)
+    before = [h.copy() for h in c.host]
+    dk, dv = dev(k.reshape(n, -1)), dev(v.reshape(n, -1))
+    vla.vla_kv_append_e4m3(dk, dv, dev(cu.astype(np.int32)), dev(table.astype(np.int32)), dev(lens.astype(np.int32)), c.gpu[0].t,
+                           c.gpu[2].t, c.gpu[1].t, c.gpu[3].t, B, n, n, hkv, D, B * each, page, block, each, hkv * D, hkv * D)
+    for x, codes, scales in ((k, 0, 1), (v, 2, 3)):
+        for b in range(0, B, 2):                                  # the even sequences have all of the rows, the odd ones none
+            append(bf16_f64(x), np.array([0, n]), table[b:b + 1], [n], c.host[codes], c.host[scales], page, block, n)
+        got = [c.gpu[i].numpy(np.uint8).reshape(c.host[i].shape) for i in (codes, scales)]
+        blocks = [y.reshape(B * each, -1, hkv, D) for y in (got[0], c.host[codes], before[codes])]
+        done = (got[1] == c.host[scales]) & (blocks[0] == blocks[1]).all((1, 3))
+        kept = (got[1] == before[scales]) & (blocks[0] == blocks[2]).all((1, 3))
+        assert (done | kept).all() and done.any()
+    for g in c.gpu:
+        g.check()
