@@ -467,35 +467,34 @@ struct Walk {
             if (key0 < 0 || key0 + 32 <= kfull || !((st.late >> ((key0 + 32 - kfull) >> 5)) & 1u)) continue;
             if constexpr (Keys::CODES) {
                 add_late_code(q, key);
-                continue;
             } else {
-            const uint16_t *kr, *vr;
-            if constexpr (PAGED) {
-                const int sl = keys.slot(key, keys.entry(key));
-                if (sl < 0) continue;
-                const int64_t at = static_cast<int64_t>(sl) * (keys.stride / 2);
-                kr = keys.k + at;
-                vr = keys.v + at;
-            } else {
-                kr = keys.k + static_cast<int64_t>(key) * (keys.k_stride / 2);
-                vr = keys.v + static_cast<int64_t>(key) * (keys.v_stride / 2);
-            }
-            if (!q || key >= klim) continue;
-            float s = 0.0f;
-            for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * bf16_to_f32(kr[d]);
-            const float p = bf16_to_f32(f32_to_bf16(__builtin_amdgcn_exp2f(s * c - st.m)));
-#pragma unroll
-            for (int d = 0; d < C::ND; ++d)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int ch = ch0 + 32 * d + 8 * x + 4 * g2;
-                    uint2 v = make_uint2(0, 0);
-                    if (ch < D) v = *reinterpret_cast<const uint2*>(vr + ch);
-                    st.acc[d][4 * x] += p * __uint_as_float(v.x << 16);
-                    st.acc[d][4 * x + 1] += p * __uint_as_float(v.x & 0xFFFF0000u);
-                    st.acc[d][4 * x + 2] += p * __uint_as_float(v.y << 16);
-                    st.acc[d][4 * x + 3] += p * __uint_as_float(v.y & 0xFFFF0000u);
+                const uint16_t *kr, *vr;
+                if constexpr (PAGED) {
+                    const int sl = keys.slot(key, keys.entry(key));
+                    if (sl < 0) continue;
+                    const int64_t at = static_cast<int64_t>(sl) * (keys.stride / 2);
+                    kr = keys.k + at;
+                    vr = keys.v + at;
+                } else {
+                    kr = keys.k + static_cast<int64_t>(key) * (keys.k_stride / 2);
+                    vr = keys.v + static_cast<int64_t>(key) * (keys.v_stride / 2);
                 }
+                if (!q || key >= klim) continue;
+                float s = 0.0f;
+                for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * bf16_to_f32(kr[d]);
+                const float p = bf16_to_f32(f32_to_bf16(__builtin_amdgcn_exp2f(s * c - st.m)));
+#pragma unroll
+                for (int d = 0; d < C::ND; ++d)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int ch = ch0 + 32 * d + 8 * x + 4 * g2;
+                        uint2 v = make_uint2(0, 0);
+                        if (ch < D) v = *reinterpret_cast<const uint2*>(vr + ch);
+                        st.acc[d][4 * x] += p * __uint_as_float(v.x << 16);
+                        st.acc[d][4 * x + 1] += p * __uint_as_float(v.x & 0xFFFF0000u);
+                        st.acc[d][4 * x + 2] += p * __uint_as_float(v.y << 16);
+                        st.acc[d][4 * x + 3] += p * __uint_as_float(v.y & 0xFFFF0000u);
+                    }
             }
         }
     }

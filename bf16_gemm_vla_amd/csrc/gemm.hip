@@ -262,15 +262,14 @@ __global__ __launch_bounds__(WAVES * 64) void skinny_gemm_kernel(KArgs a) {
                 for (int j = 0; j < NT; ++j)
                     acc[j][mt] = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(int64_t, wf[s][j]),
                                                                        __builtin_bit_cast(int64_t, af[s][mt]), acc[j][mt], 0, 0, 0);
-                continue;
             } else {
-            const bf16x8_t bop = a_operand<AT>(af[s][mt]);
+                const bf16x8_t bop = a_operand<AT>(af[s][mt]);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
-                if constexpr (WT == WType::FP4)
-                    acc[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4_to_bf16x8(wf[s][j], wsc[s][j]), bop, acc[j][mt], 0, 0, 0);
-                else
-                    acc[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w_operand<WT>(wf[s][j]), bop, acc[j][mt], 0, 0, 0);
+                for (int j = 0; j < NT; ++j)
+                    if constexpr (WT == WType::FP4)
+                        acc[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fp4_to_bf16x8(wf[s][j], wsc[s][j]), bop, acc[j][mt], 0, 0, 0);
+                    else
+                        acc[j][mt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w_operand<WT>(wf[s][j]), bop, acc[j][mt], 0, 0, 0);
             }
         }
     }
