@@ -338,7 +338,8 @@ SharedPlan plan_attn_shared(int64_t B, int64_t L, int64_t Hq, int64_t Hkv, int64
     // A long prefix is worth 32 rows, which bring its codes half as often (64
     // single tokens of 32 heads on 8 of 128 with 300 keys of their own behind
     // 8000: 37.6 us, with 16 rows 47.6; behind 2051 with up to 3000 of their own
-    // 71.5, with 16 rows 61.6).
+    // 71.5, with 16 rows 61.6).  The border lies between these two, unmeasured
+    // there, and goes by the table's capacity, which is what the host knows.
     if (codes && p.prefix_tm == 16 && rows_p > 16 && D <= 128 && prefix_cap > 4096) p.prefix_tm = 32;
     p.suffix_tm = tile(B, rows_s);
     // A sequence whose rows fill its tiles reads the prefix no more often by

@@ -29,8 +29,8 @@
 //
 // Measured, captured calls one behind another on caches of their own, 32 heads
 // on 8 of 128 unless another is said (in parentheses the same keys in bf16): one
-// token over 131071 keys 63 us, 4.25 TB/s (112); 64 single tokens behind 2051
-// shared and up to 3000 own keys 60 us, 3.5 TB/s (116); over 1500 own keys each
+// token over 131071 keys 60-63 us, 4.25-4.5 TB/s (112); 64 single tokens behind
+// 2051 shared and up to 3000 own keys 58-60 us, 3.5 TB/s (116); over 1500 own keys each
 // 46 (79); 8 heads on 1 of 256, 10 rows over 778 keys 11.5 (11.1), one token over
 // 30000 21.5 (23).  Bound by the loads of the cache, which three waves per SIMD
 // keep in flight with one sub-tile each (128 channels; two need more registers
@@ -68,7 +68,9 @@ struct FCfg {
 
 // Position of a row's 16-byte chunks in LDS: chunk ^ swizzle.  One chunk of 16
 // rows in a line (the keys' reads) and of rows 0-7 and 16-23, or 8-15 and 24-31
-// (a half wave's transpose read), lies in as many places of the banks.
+// (a half wave's transpose read), lies in as many places of the banks.  (The
+// conflicts that counters show are the results' exchange at the end: 128 cycles a
+// workgroup of 256 channels over 128 keys and over 512.)
 template <int DP>
 __device__ __forceinline__ int swz_codes(int row) {
     if constexpr (DP == 64) return (row >> 2 & 3) ^ (row >> 4) << 1;

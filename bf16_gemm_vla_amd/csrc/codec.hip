@@ -110,10 +110,11 @@ __device__ __forceinline__ uint2 encode8_quotient(const float v[8], float sc, fl
     return make_uint2(o[0], o[1]);
 }
 
-// Scale of 8-bit integers whose largest magnitude is m: m / 127 with the
-// reciprocal rounded first (within one step of it), which is what array
-// libraries make of a division by a constant, so that their codes and these are
-// the same.
+// Scale of 8-bit integers whose largest magnitude is m: m times the rounded
+// reciprocal of 127, within one step of m / 127.  That is what torch computes for
+// a division by the number 127 on the GPU, so codes and scales made there are
+// these bit for bit; NumPy, and torch on the CPU, divide, and their scale can be
+// the next number (and then 9 of 33.5 million codes, at ties, were others).
 __device__ __forceinline__ float scale_int8(float m) {
     constexpr float kStep = 1.0f / 127.0f;
     const float sc = __fmul_rn(m, kStep);
@@ -152,7 +153,10 @@ __device__ __forceinline__ uint2 encode8_int8(const float v[8], float sc, float 
 // the tile mostly hits L2).  Phase 1: row absmax -> scale.  Phase 2: each
 // thread encodes 8-value slots (reads 2 x 16 B, writes 8 B / 16 B).  NT =
 // 1024 keeps 16 waves' loads in flight per tile: a 2048 x 16384 matrix has
-// only 128 tiles.
+// only 128 tiles.  8-bit integers have this form alone (captured, cold caches,
+// E4M3's forms in parentheses: 4096 x 1024 8.1 us (6.7), 1024 x 4096 14.8
+// (10.4), 16384 x 2048 50.5 (34.2), 2048 x 16384 67 (66); the bytes' time 4.1,
+// 4.1, 32.8, 32.8): once per weight, when it is loaded.
 template <int WFMT, int NT>
 __global__ __launch_bounds__(NT) void quantize_pack_kernel(const float* __restrict__ W,
                                                            void* __restrict__ Wq,
@@ -804,8 +808,9 @@ __global__ __launch_bounds__(kThreads) void act_encode_kernel(const uint16_t* __
 // that holds an infinity or NaN gets zeros and a NaN scale, which makes its
 // products NaN.  WPR waves share a row, which stays in registers between its
 // maximum and its codes: 8 CH values per lane.  Bound by HBM where the rows are
-// many (8191 of 4096: 22.5 us captured with cold caches, 4.5 TB/s) and by one
-// row's way where they are few (50 of 1024: 3.4 us, an empty launch 2.8).
+// many (8191 of 4096, captured: 21-23 us on three sets of inputs in turn, 23.7 on
+// ten, 4.2-4.8 TB/s) and by one row's way where they are few (50 of 1024: 2.5-3.4
+// us, an empty launch 2.8 beside the latter).
 template <int WPR, int CH>
 __global__ __launch_bounds__(kThreads) void quantize_tokens_int8_kernel(const uint16_t* __restrict__ A,
                                                                         int8_t* __restrict__ qa,
@@ -902,7 +907,7 @@ __global__ __launch_bounds__(1024) void quantize_long_tokens_int8_kernel(const u
 
 // Rows of 1024 channels and less are a wave's, longer ones four waves', where
 // many run at once (8191 rows of 1024: 10.1 us, four waves 12.1; of 2048: 16.0,
-// one wave 16.4; of 4096: 25, 29.5); few rows take more waves, whose divisions
+// one wave 16.4; of 4096: 23.7, 28.6); few rows take more waves, whose divisions
 // run side by side: four up to 2048 channels (50 rows of 1024: 3.4 us, one
 // wave 4.1; of 2048: 3.5, 4.6), then the 16 that read a row twice, from their L1
 // the second time (50 rows of 4096: 3.8, four waves 4.1; of 16384: 6.1, 7.0; but

@@ -87,7 +87,7 @@ __device__ __forceinline__ EpiIn load_epi(const KArgs& a, int m, int n, bool wit
 }
 
 // An integer sum times its row's and its column's scale: the product of the
-// scales first, two roundings of 2^-24 in all, unless that product leaves
+// scales first, two roundings of 2^-24 beside the sum's own, unless that product leaves
 // fp32's normal range, where the whole need not (rows of 1e-20 times columns
 // of 1e-20), or is NaN: then all of it in fp64.
 __device__ __forceinline__ bool normal_scale(float lo, float hi) { return lo >= 0x1p-126f && hi < __builtin_inff(); }

@@ -37,8 +37,8 @@
 // step s+1 (and of the next stage's first step, right after the barrier)
 // overlap the MFMAs of step s.
 //
-// 8-bit integers, 8191 rows, 2048 -> 16384: 310 us, 1.77 POP/s (FP8 x FP8 272;
-// the 268 MB of results alone 52).  The matrix pipes are busy half of
+// 8-bit integers, 8191 rows, 2048 -> 16384: 290-310 us over the boxes it ran on,
+// 1.8-1.9 POP/s (FP8 x FP8 265-272; the 268 MB of results alone 52).  The matrix pipes are busy half of
 // the cycles, at 1.9 GHz; loads that always hit L2 gain 3%, LDS reads left out 9%,
 // and neither the order of the two products nor where the barrier stands among
 // them changes the time, nor 4 waves of 96 x 128 (470 us).  768 rows: 16384 ->

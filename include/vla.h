@@ -166,7 +166,9 @@ int vla_quantize_act_static(const uint16_t *A, const float *s_a, uint8_t *qa, in
 
 /* Tokens in 8-bit integers for vla_gemm_int8, a scale for each row of A: s_a[m]
  * = fp32(max_k |A[m,k]| * fp32(1 / 127)), 1 where that is 0; qa[m,k] = the integer
- * nearest to fp32(A[m,k] / s_a[m]), ties to even.  A row that holds an infinity
+ * nearest to fp32(A[m,k] / s_a[m]), ties to even.  That scale is torch's
+ * `max / 127` on the GPU, bit for bit; the quotient rounded once, as NumPy and
+ * torch on the CPU form it, can be the next fp32 number.  A row that holds an infinity
  * or NaN gets zeros and a NaN scale, so its products are NaN; other rows are
  * not touched by it.
  *   A   device bf16 M x K;  qa device int8 M x K;  s_a device float[M].
@@ -401,6 +403,11 @@ int vla_kv_append_e4m3(const uint16_t* k, const uint16_t* v, const int32_t* cu_r
  * infinities, values of that size as that or as what they are; parts below
  * 2^-133 round.  A NaN code, and any code under the scale byte 255, is NaN to
  * the rows that see it and has no part in others.
+ * The codes are half the bytes, which is what single tokens and short chunks over
+ * long caches gain by.  Where many rows read the same keys the products bind, and
+ * turning codes into bf16 comes on top: 2048 rows over 8192 keys take 1.13 of the
+ * bf16 cache's time up to 128 channels and 1.5 with 256, 32 chunks of 50 rows
+ * with 256 channels 1.4, and 10 rows over 800 keys the same.
  *   k_cache, v_cache, k_scales, v_scales, block_size  as vla_kv_append_e4m3 leaves them;
  *   ws   device workspace of vla_attn_shared_prefix_e4m3_workspace_bytes, to
  *        which the same applies as above. */
@@ -583,7 +590,9 @@ int vla_gemm_fp8w_gelu_mul(const uint16_t *A, const uint8_t *Wgu, const float *s
  * and exact (any order, any K split: results are repeatable bit for bit and a
  * row's do not depend on the other rows); scaled in fp32, or in fp64 where the
  * product of the two scales leaves its normal range.  A NaN scale makes its
- * row or column NaN.
+ * row or column NaN.  Up to 64 rows this is the faster one beside FP8 x FP8
+ * (vla_gemm_fp8w with s_a, one scale for all tokens; 10 rows, 4096 -> 4096, 6.4
+ * us against 10.3), above it 3-11% slower.
  *   A        device int8 M x K row-major, s_a device float[M]
  *            (vla_quantize_tokens_int8, or any codes -128 .. 127 and scales);
  *   Wq       device int8 N x K in VLA_LAYOUT_MFMA, s_w device float[N]
