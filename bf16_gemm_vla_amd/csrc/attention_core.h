@@ -22,6 +22,9 @@ typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 
 constexpr int kAThreads = 256;
 constexpr float kLag = 8.0f;                     // log2 of the largest weight, see weights()
+// The maximum of a part whose keys a row sees and whose scores are all -inf: the
+// join reads it, for the NaN among its values, and a part without keys it does not.
+constexpr float kSeen = -3.402823466e38f;
 constexpr uint32_t kNoOffset = 0xFFFFF000u;      // a buffer offset past every cache that takes 32-bit ones
 constexpr int kBufferWord3 = 0x00020000;          // raw buffer, 32-bit data format
 
@@ -1040,6 +1043,7 @@ void attn_shared_kernel(SharedArgs a) {
     const int k0 = min(split * per * C::ST, keys.n), k1 = min((split + 1) * per * C::ST, keys.n);
     State<C> st;
     attend<C>(keys, q, klim, k0, k1, a.D, a.c, b0, b1, b2, b3, st);
+    if (klim > k0) st.m = fmaxf(st.m, kSeen);
     if (a.parts == 1) {
         uint16_t* const out = a.out + token * a.out_stride + static_cast<int64_t>(head) * a.D;
         write_rows<C, false>(st, live ? reinterpret_cast<uint64_t>(out) : 0, nullptr, nullptr, a.D, b0, b1, b2, b3, ml, row_at);

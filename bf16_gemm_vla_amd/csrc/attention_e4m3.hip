@@ -461,7 +461,7 @@ void attn_few_codes_kernel(SharedArgs a) {
             int h;
             const int64_t token = static_cast<int64_t>(b) * a.L + a.by_group.divide(row0 + row, h);
             const int64_t at = (token * a.Hq + hk * G + h) * a.parts + (prefix ? 0 : a.prefix_splits) + split;
-            *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(mm, ll);
+            *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(klim[r] > k0 ? fmaxf(mm, kSeen) : mm, ll);
         }
         uint8_t* const mine = lds + wave * C::O_BYTES + row * C::DP * 4;
 #pragma unroll
