@@ -461,6 +461,10 @@ struct Walk {
         st.late |= 1u << ((key0 + 32 - kfull) >> 5);
         return true;
     }
+    // weights() for one score (of a row whose scores are all -inf: 0)
+    __device__ __forceinline__ float late_weight(float s) const {
+        return bf16_to_f32(f32_to_bf16(__builtin_amdgcn_exp2f(s * c - (st.m == -__builtin_inff() ? 0.0f : st.m))));
+    }
     // key0_of: first key of this wave's sub-tile that holds a key, or -1 (another wave's)
     template <class F>
     __device__ __forceinline__ void add_late(const uint16_t* q, int k1, F&& key0_of) const {
@@ -485,7 +489,7 @@ struct Walk {
                 if (!q || key >= klim) continue;
                 float s = 0.0f;
                 for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * bf16_to_f32(kr[d]);
-                const float p = bf16_to_f32(f32_to_bf16(__builtin_amdgcn_exp2f(s * c - st.m)));
+                const float p = late_weight(s);
 #pragma unroll
                 for (int d = 0; d < C::ND; ++d)
 #pragma unroll
@@ -510,7 +514,7 @@ struct Walk {
         const float ks = __uint_as_float(sw & 0xFFFF0000u), vs = __uint_as_float(sw << 16);
         float s = 0.0f;
         for (int d = 0; d < D; ++d) s += bf16_to_f32(q[d]) * (decode_e4m3<false>(kr[d]) * ks);
-        const float p = bf16_to_f32(f32_to_bf16(__builtin_amdgcn_exp2f(s * c - st.m)));
+        const float p = late_weight(s);
 #pragma unroll
         for (int d = 0; d < C::ND; ++d)
 #pragma unroll

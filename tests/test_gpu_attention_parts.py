@@ -97,3 +97,25 @@ def test_rows_that_see_nothing_stay_0_beside_them():
             c.table[:] = -1
         got = c.call(q, 0, [1, 2, 130], L, hq, True, 1.0)
         assert not got.any()
+
+
+@pytest.mark.parametrize("B,L,hq,hkv,D", [(5, 9, 4, 2, 64), (100, 5, 20, 4, 128), (300, 10, 4, 1, 64), (65, 20, 8, 2, 256)])
+def test_first_rows_whose_only_score_is_minus_infinity(B, L, hq, hkv, D):
+    """Causal rows over their own keys: the first sees one key, whose value is NaN in one channel.  That channel is NaN, the
+    others are 0, over codes (16, 32, 64 and 128 rows a tile) and for packed prompts."""
+    c = Cache(B, hkv, D, 16, 1, 0, [L] * B, 7020)
+    q = queries(B, L, hq, D)
+    c.codes[0][:, :, 0] = 0
+    for b in range(B):
+        slot = c.keys[b][0]
+        c.codes[0][slot, :, 0], c.bytes[0][slot], c.codes[1][slot, :, 5] = 0xC0, 127, 0x7F
+    rows = [c.call(q, 0, [L] * B, L, hq, True, 1.0)[:, 0]]
+    k, v = (np.concatenate([c.values(i, c.keys[b]) for b in range(B)]) for i in range(2))
+    cu = np.arange(B + 1, dtype=np.int32) * L
+    o = Guarded(B * L * hq * D * 2, fill=0x5A)
+    vla.vla_attn_prompt(dev(q), dev(k), dev(v), dev(cu), None, o.t, B, B * L, B * L, hq, hkv, D, hq * D, hkv * D, hkv * D, hq * D, True, 1.0)
+    o.check()
+    rows.append(o.numpy(np.uint16).reshape(B, L, hq, D)[:, 0])
+    for g in rows:
+        g = bf16_f64(g)
+        assert np.isnan(g[..., 5]).all() and not np.delete(g, 5, 2).any()
