@@ -37,7 +37,7 @@
 // step s+1 (and of the next stage's first step, right after the barrier)
 // overlap the MFMAs of step s.
 //
-// 8-bit integers, 8191 rows, 2048 -> 16384: 290-310 us over the boxes it ran on,
+// 8-bit integers, 8191 rows, 2048 -> 16384: 290-310 us over several cards,
 // 1.8-1.9 POP/s (FP8 x FP8 265-272; the 268 MB of results alone 52).  The matrix pipes are busy half of
 // the cycles, at 1.9 GHz; loads that always hit L2 gain 3%, LDS reads left out 9%,
 // and neither the order of the two products nor where the barrier stands among
